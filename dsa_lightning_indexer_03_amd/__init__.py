@@ -8,6 +8,9 @@ device, and passes pointers and the current HIP stream.
     indexer_prefill(q, k, w, topk, q_scale=None, k_scale=None, want_scores=False)
     indexer_decode_paged(q, w, k_cache, k_scale, block_table, context_lens, topk, max_context_len=None)
     topk_select(scores, topk, row_len=None)
+    cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin, index_k=None, ...)
+    latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim, scale, ...)
+    latent_attention_shared(q, latent_cache, prefix_table, prefix_len, block_table, context_lens, v_dim, scale, ...)
 
 Input formats: fp32 tensors; bf16 as torch.bfloat16 or int16/uint16 bit
 patterns; OCP FP8 E4M3 as torch.float8_e4m3fn or uint8 codes with fp32
@@ -23,7 +26,8 @@ F32, BF16, FP8_E4M3 = 0, 1, 2
 
 __all__ = ["indexer_prefill", "indexer_prefill_noalloc", "indexer_decode_paged", "topk_select", "kcache_append", "topk_gather",
            "topk_gather_layers",
-           "prefill_chunk_paged", "prefill_chunk_varlen", "dtype_code", "F32", "BF16", "FP8_E4M3"]
+           "prefill_chunk_paged", "prefill_chunk_varlen",
+           "cache_append_rope", "latent_attention_topk", "latent_attention_shared", "dtype_code", "F32", "BF16", "FP8_E4M3"]
 
 
 def dtype_code(t: torch.Tensor) -> int:
@@ -402,3 +406,191 @@ def prefill_chunk_paged(q, q_scale, w, k_cache, k_scale, block_table, q0: int, t
                                     k_cache, k_scale, block_table, topk, int(q0) + Lq,
                                     want_topk_score=want_topk_score, workspace=workspace)
     return idx.view(B, Lq, topk), None if val is None else val.view(B, Lq, topk)
+
+
+def _same_device(dev, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, the device of the other tensors")
+
+
+def _rows(t, name: str) -> int:
+    """Row stride (elements) of a 2-D device tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    return t.stride(0)
+
+
+def _inference_only(where: str, *tensors) -> None:
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{where} has no backward: call it under torch.no_grad() or detach its inputs")
+
+
+def cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin, latent_scale=None,
+                      kv_interleaved: bool = True, index_k=None, k_cache=None, k_scale=None,
+                      index_interleaved: bool = False) -> None:
+    """Rotates T new tokens' latent rows and index keys by their positions and
+    writes them into the two paged caches in place, in one launch.
+
+    kv [T,E] bf16 or fp32 (rows may be strided), its last R columns rotated;
+    cos_sin [rope_len,R] fp32 (R/2 cosines, then R/2 sines, of each position);
+    seq_ids, positions [T] int32 (a token outside the table, rope_len or the
+    pool is skipped); block_table [B,max_pages] int32; latent_cache [P,page,E]
+    bf16, or uint8 / float8_e4m3fn codes with latent_scale [P,page] fp32.
+    index_k [T,D] (kv's type, its first R columns rotated) goes to k_cache
+    [P,page,D] codes and k_scale [P,page] fp32 as kcache_append writes them;
+    all three None: latent rows only.  kv_interleaved, index_interleaved: pair
+    i is columns (2i, 2i+1), else (i, i + R/2).  Returns nothing."""
+    lib = _lib.load()
+    dev = kv.device
+    kv_stride = _rows(kv, "kv")
+    T, E = kv.shape
+    _need(kv, "kv", torch.bfloat16, _F32)
+    _need(latent_cache, "latent_cache", torch.bfloat16, *_CODES)
+    _need(latent_scale, "latent_scale", _F32)
+    _need(cos_sin, "cos_sin", _F32)
+    _need(seq_ids, "seq_ids", _I32)
+    _need(positions, "positions", _I32)
+    _need(block_table, "block_table", _I32)
+    if latent_cache.dim() != 3 or latent_cache.shape[2] != E:
+        raise ValueError("latent_cache must be [P, page, E] with the E of kv")
+    P, page = latent_cache.shape[:2]
+    fp8 = latent_cache.dtype != torch.bfloat16
+    if fp8 != (latent_scale is not None) or (fp8 and tuple(latent_scale.shape) != (P, page)):
+        raise ValueError("latent_scale [P, page] goes with fp8 latent rows, None with bf16 rows")
+    if cos_sin.dim() != 2 or block_table.dim() != 2:
+        raise ValueError("cos_sin must be [rope_len, R] and block_table [B, max_pages]")
+    if tuple(seq_ids.shape) != (T,) or tuple(positions.shape) != (T,):
+        raise ValueError("seq_ids / positions must have one entry per token")
+    index_stride, D = 0, 128
+    if (index_k is None) != (k_cache is None) or (index_k is None) != (k_scale is None):
+        raise ValueError("index_k, k_cache and k_scale go together")
+    if index_k is not None:
+        index_stride = _rows(index_k, "index_k")
+        D = index_k.shape[1]
+        if index_k.dtype != kv.dtype or index_k.shape[0] != T:
+            raise ValueError("index_k must be [T, D] of kv's type")
+        _need(k_cache, "k_cache", *_CODES)
+        _need(k_scale, "k_scale", _F32)
+        if tuple(k_cache.shape) != (P, page, D) or tuple(k_scale.shape) != (P, page):
+            raise ValueError("k_cache [P, page, D] / k_scale [P, page] shape mismatch")
+    for name, t in (("seq_ids", seq_ids), ("positions", positions), ("block_table", block_table),
+                    ("latent_cache", latent_cache), ("cos_sin", cos_sin), ("latent_scale", latent_scale),
+                    ("k_cache", k_cache), ("k_scale", k_scale)):
+        if t is not None:
+            _dev(t, name)
+    _same_device(dev, seq_ids=seq_ids, positions=positions, block_table=block_table, latent_cache=latent_cache,
+                 cos_sin=cos_sin, latent_scale=latent_scale, index_k=index_k, k_cache=k_cache, k_scale=k_scale)
+    _inference_only("cache_append_rope", kv, index_k)
+    with torch.cuda.device(dev):
+        st = lib.indexer_cache_append_rope(_ptr(kv), kv_stride, int(kv_interleaved), _ptr(index_k), index_stride,
+                                           int(index_interleaved), dtype_code(kv), _ptr(cos_sin), cos_sin.shape[0],
+                                           cos_sin.shape[1], _ptr(seq_ids), _ptr(positions), _ptr(block_table),
+                                           block_table.shape[0], block_table.shape[1], _ptr(latent_cache),
+                                           _ptr(latent_scale), FP8_E4M3 if fp8 else BF16, _ptr(k_cache),
+                                           _ptr(k_scale), P, T, E, D, page, _stream(dev))
+    _lib.check(st, "indexer_cache_append_rope")
+
+
+def _latent_inputs(q, latent_cache, latent_scale, block_table, where: str, **others):
+    """Checks that the latent-attention calls share; returns (P, page, dtype code of the rows)."""
+    _need(q, "q", torch.bfloat16)
+    _need(latent_cache, "latent_cache", torch.bfloat16, *_CODES)
+    _need(latent_scale, "latent_scale", _F32)
+    if q.dim() != 3 or latent_cache.dim() != 3 or latent_cache.shape[2] != q.shape[2]:
+        raise ValueError("q must be [rows, H, E] and latent_cache [P, page, E]")
+    P, page = latent_cache.shape[:2]
+    fp8 = latent_cache.dtype != torch.bfloat16
+    if fp8 != (latent_scale is not None) or (fp8 and tuple(latent_scale.shape) != (P, page)):
+        raise ValueError("latent_scale [P, page] goes with fp8 latent rows, None with bf16 rows")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    tensors = dict(q=q, latent_cache=latent_cache, latent_scale=latent_scale, block_table=block_table, **others)
+    for name, t in tensors.items():
+        if t is not None:
+            if name not in ("q", "latent_cache", "latent_scale"):
+                _need(t, name, _I32)
+            _dev(t, name)
+    _same_device(q.device, **tensors)
+    _inference_only(where, q, latent_cache)
+    return P, page, FP8_E4M3 if fp8 else BF16
+
+
+def latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim: int, scale: float, latent_scale=None,
+                          seq_ids=None, want_lse: bool = False, workspace: torch.Tensor | None = None):
+    """Attention of every head over the latent rows at each query's selected
+    positions, read in place (no gathered copy).
+
+    q [T,H,E] bf16, latent_cache [P,page,E] bf16, or uint8 / float8_e4m3fn
+    codes with latent_scale [P,page] fp32; the first v_dim columns of a row are
+    its value.  block_table [B,max_pages] int32; topk_idx [T,K] int32 positions
+    (-1, or outside the table: no row); seq_ids [T] int32 gives each query's
+    row of the table (outside [0, B): no rows), None: query t uses row t.
+    Returns (out bf16 [T,H,v_dim], lse fp32 [T,H] or None); a query without a
+    row gives zeros and -inf."""
+    lib = _lib.load()
+    P, page, dt = _latent_inputs(q, latent_cache, latent_scale, block_table, "latent_attention_topk",
+                                 topk_idx=topk_idx, seq_ids=seq_ids)
+    T, H, E = q.shape
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must be [T, K]")
+    if seq_ids is not None and tuple(seq_ids.shape) != (T,):
+        raise ValueError("seq_ids must have one entry per query")
+    if seq_ids is None and block_table.shape[0] != T:
+        raise ValueError("block_table must have one row per query (or give seq_ids)")
+    dev, K = q.device, topk_idx.shape[1]
+    out = torch.empty((T, H, v_dim), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((T, H), dtype=torch.float32, device=dev) if want_lse else None
+    nws = lib.indexer_latent_attention_topk_workspace_bytes(T, H, E, v_dim, K)
+    ws = workspace if workspace is not None and workspace.numel() >= nws else _workspace(nws, dev)
+    with torch.cuda.device(dev):
+        st = lib.indexer_latent_attention_topk(_ptr(q), BF16, _ptr(latent_cache), _ptr(latent_scale), dt,
+                                               _ptr(block_table), block_table.shape[1], P, _ptr(topk_idx),
+                                               _ptr(seq_ids), max(1, block_table.shape[0]), T, H, E, v_dim, page, K,
+                                               float(scale), _ptr(out), _ptr(lse), _ptr(ws), nws, _stream(dev))
+    _lib.check(st, "indexer_latent_attention_topk")
+    return out, lse
+
+
+def latent_attention_shared(q, latent_cache, prefix_table, prefix_len: int, block_table, context_lens, v_dim: int,
+                            scale: float, max_context_len: int | None = None, latent_scale=None,
+                            want_lse: bool = False, workspace: torch.Tensor | None = None):
+    """One decode step of B queries over a prefix that all of them share, read
+    once for the batch, and each sequence's own positions behind it.
+
+    q [B,H,E] bf16, latent_cache and latent_scale as latent_attention_topk;
+    prefix_table [n] int32 page ids of the prefix's first ``prefix_len``
+    positions (None when that is 0); block_table [B,max_pages] int32 and
+    context_lens [B] int32: the sequences' own pages and lengths.
+    ``max_context_len`` bounds context_lens (default: max_pages * page).
+    Returns (out bf16 [B,H,v_dim], lse fp32 [B,H] or None); a query without a
+    position gives zeros and -inf."""
+    lib = _lib.load()
+    P, page, dt = _latent_inputs(q, latent_cache, latent_scale, block_table, "latent_attention_shared",
+                                 prefix_table=prefix_table, context_lens=context_lens)
+    B, H, E = q.shape
+    if block_table.shape[0] != B or tuple(context_lens.shape) != (B,):
+        raise ValueError("block_table / context_lens shape mismatch")
+    if prefix_table is not None and prefix_table.dim() != 1:
+        raise ValueError("prefix_table must be one-dimensional")
+    mpp = block_table.shape[1]
+    mcl = mpp * page if max_context_len is None else int(max_context_len)
+    dev = q.device
+    out = torch.empty((B, H, v_dim), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((B, H), dtype=torch.float32, device=dev) if want_lse else None
+    prefix_len = int(prefix_len)
+    nws = lib.indexer_latent_attention_shared_workspace_bytes(B, H, E, v_dim, prefix_len, mcl)
+    ws = workspace if workspace is not None and workspace.numel() >= nws else _workspace(nws, dev)
+    with torch.cuda.device(dev):
+        st = lib.indexer_latent_attention_shared(_ptr(q), BF16, _ptr(latent_cache), _ptr(latent_scale), dt,
+                                                 _ptr(prefix_table),
+                                                 0 if prefix_table is None else prefix_table.shape[0], prefix_len,
+                                                 _ptr(block_table), mpp, P, _ptr(context_lens), mcl, B, H, E, v_dim,
+                                                 page, float(scale), _ptr(out), _ptr(lse), _ptr(ws), nws,
+                                                 _stream(dev))
+    _lib.check(st, "indexer_latent_attention_shared")
+    return out, lse

@@ -12,6 +12,7 @@ _c_void_p = ctypes.c_void_p
 _c_int = ctypes.c_int
 _c_size_t = ctypes.c_size_t
 _c_int64 = ctypes.c_int64
+_c_float = ctypes.c_float
 
 # (name, restype, argtypes) for every symbol declared in include/dsaidx.h
 SIGNATURES = {
@@ -42,6 +43,21 @@ SIGNATURES = {
     "indexer_topk_gather_layers": (_c_int, [ctypes.POINTER(_c_void_p), ctypes.POINTER(_c_void_p), _c_int, _c_int,
                                             _c_void_p, _c_int, _c_int, _c_int, _c_void_p, _c_int, _c_int,
                                             _c_void_p]),
+    "indexer_cache_append_rope": (_c_int, [_c_void_p, _c_int64, _c_int, _c_void_p, _c_int64, _c_int, _c_int,
+                                           _c_void_p, _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p, _c_int,
+                                           _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_void_p, _c_int,
+                                           _c_int, _c_int, _c_int, _c_int, _c_void_p]),
+    "indexer_latent_attention_topk": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int,
+                                               _c_int, _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int,
+                                               _c_int, _c_int, _c_int, _c_float, _c_void_p, _c_void_p, _c_void_p,
+                                               _c_size_t, _c_void_p]),
+    "indexer_latent_attention_topk_workspace_bytes": (_c_size_t, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "indexer_latent_attention_shared": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int,
+                                                 _c_int, _c_void_p, _c_int, _c_int, _c_void_p, _c_int, _c_int,
+                                                 _c_int, _c_int, _c_int, _c_int, _c_float, _c_void_p, _c_void_p,
+                                                 _c_void_p, _c_size_t, _c_void_p]),
+    "indexer_latent_attention_shared_workspace_bytes": (_c_size_t, [_c_int, _c_int, _c_int, _c_int, _c_int,
+                                                                    _c_int]),
     "dsaidx_probe_mfma": (_c_int, [_c_int, _c_int, _c_int, _c_void_p, _c_void_p]),
     "dsaidx_probe_page_read": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_void_p, _c_void_p]),
     "dsaidx_status_string": (ctypes.c_char_p, [_c_int]),

@@ -165,6 +165,226 @@ dsaidx_status indexer_topk_gather_layers(const void* const* latent_caches, void*
     return DSAIDX_OK;
 }
 
+dsaidx_status indexer_cache_append_rope(const void* kv, int64_t kv_stride, int kv_interleaved, const void* index_k,
+                                        int64_t index_stride, int index_interleaved, int in_dtype,
+                                        const float* cos_sin, int rope_len, int rope_dim, const int32_t* seq_ids,
+                                        const int32_t* positions, const int32_t* block_table, int B,
+                                        int max_pages_per_seq, void* latent_cache, float* latent_scale,
+                                        int latent_dtype, uint8_t* k_cache, float* k_scale, int num_pages, int T,
+                                        int E, int D, int page_size, void* stream) {
+    g_err[0] = 0;
+    if (T < 0 || B < 1 || max_pages_per_seq < 1 || num_pages < 1 || E < 1 || D < 1 || page_size < 1 || rope_len < 1 ||
+        rope_dim < 1)
+        return fail(DSAIDX_ERR_SHAPE,
+                    "T=%d B=%d max_pages_per_seq=%d num_pages=%d E=%d D=%d page_size=%d rope_len=%d rope_dim=%d", T, B,
+                    max_pages_per_seq, num_pages, E, D, page_size, rope_len, rope_dim);
+    if (in_dtype != DSAIDX_F32 && in_dtype != DSAIDX_BF16 && in_dtype != DSAIDX_FP8_E4M3)
+        return fail(DSAIDX_ERR_DTYPE, "in_dtype=%d", in_dtype);
+    if (latent_dtype != DSAIDX_F32 && latent_dtype != DSAIDX_BF16 && latent_dtype != DSAIDX_FP8_E4M3)
+        return fail(DSAIDX_ERR_DTYPE, "latent_dtype=%d", latent_dtype);
+    if (in_dtype == DSAIDX_FP8_E4M3) return fail(DSAIDX_ERR_UNSUPPORTED, "new rows must be bf16 or f32");
+    if (latent_dtype == DSAIDX_F32) return fail(DSAIDX_ERR_UNSUPPORTED, "the latent cache must be bf16 or fp8");
+    if (D != 128) return fail(DSAIDX_ERR_UNSUPPORTED, "D=%d (128)", D);
+    if (page_size != 64) return fail(DSAIDX_ERR_UNSUPPORTED, "page_size=%d (64)", page_size);
+    if (E % 8 != 0 || E > 1024) return fail(DSAIDX_ERR_UNSUPPORTED, "E=%d (a multiple of 8, at most 1024)", E);
+    if (rope_dim % 16 != 0 || rope_dim > 128 || rope_dim > E)
+        return fail(DSAIDX_ERR_UNSUPPORTED, "rope_dim=%d (a multiple of 16, at most 128 and E)", rope_dim);
+    if ((latent_dtype == DSAIDX_FP8_E4M3) != (latent_scale != nullptr))
+        return fail(DSAIDX_ERR_SHAPE, "latent_scale goes with an fp8 latent cache, NULL with a bf16 one");
+    if ((index_k != nullptr) != (k_cache != nullptr) || (index_k != nullptr) != (k_scale != nullptr))
+        return fail(DSAIDX_ERR_SHAPE, "index_k, k_cache and k_scale are given together or not at all");
+    if (T == 0) return DSAIDX_OK;
+    if (!kv) return fail(DSAIDX_ERR_NULL, "kv is NULL");
+    if (!cos_sin) return fail(DSAIDX_ERR_NULL, "cos_sin is NULL");
+    if (!seq_ids) return fail(DSAIDX_ERR_NULL, "seq_ids is NULL");
+    if (!positions) return fail(DSAIDX_ERR_NULL, "positions is NULL");
+    if (!block_table) return fail(DSAIDX_ERR_NULL, "block_table is NULL");
+    if (!latent_cache) return fail(DSAIDX_ERR_NULL, "latent_cache is NULL");
+    if (T > 1 && (kv_stride < E || (index_k && index_stride < D)))
+        return fail(DSAIDX_ERR_SHAPE, "kv_stride=%lld < E=%d or index_stride=%lld < D=%d", (long long)kv_stride, E,
+                    (long long)index_stride, D);
+    const int per16 = in_dtype == DSAIDX_BF16 ? 8 : 4;  // elements of 16 bytes
+    if (!aligned16(kv) || !aligned16(index_k) || !aligned16(cos_sin) || !aligned16(latent_cache) ||
+        ((uintptr_t)k_cache & 7u) != 0 || (T > 1 && (kv_stride % per16 != 0 || (index_k && index_stride % per16 != 0))))
+        return fail(DSAIDX_ERR_UNSUPPORTED,
+                    "kv and index_k rows, cos_sin and latent_cache must be 16-byte, k_cache 8-byte aligned");
+    dsaidx::AppendRopeArgs a{};
+    a.kv = kv;
+    a.index_k = index_k;
+    a.kv_stride = kv_stride;
+    a.index_stride = index_stride;
+    a.cos_sin = cos_sin;
+    a.seq_ids = seq_ids;
+    a.positions = positions;
+    a.block_table = block_table;
+    a.latent = latent_cache;
+    a.latent_scale = latent_scale;
+    a.k_cache = k_cache;
+    a.k_scale = k_scale;
+    a.T = T;
+    a.B = B;
+    a.max_pages = max_pages_per_seq;
+    a.num_pages = num_pages;
+    a.E = E;
+    a.R = rope_dim;
+    a.rope_len = rope_len;
+    a.kv_pairs = kv_interleaved != 0;
+    a.index_pairs = index_interleaved != 0;
+    const hipError_t e = dsaidx::launch_cache_append_rope(a, in_dtype == DSAIDX_F32, latent_dtype == DSAIDX_FP8_E4M3,
+                                                          (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "indexer_cache_append_rope");
+    return DSAIDX_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int kMaxLatentTokens = 1 << 27;  // longest list of keys of one query
+constexpr int kMaxLatentHeads = 128;
+
+// The checks that both latent-attention entry points share; 0 when all pass.
+dsaidx_status latent_check(const void* q, int q_dtype, const void* latent_cache, const float* latent_scale,
+                           int latent_dtype, const int32_t* block_table, int max_pages_per_seq, int num_pages, int B,
+                           int T, int H, int E, int V, int page_size, float scale, const void* out) {
+    if (T < 0 || B < 1 || H < 1 || E < 1 || V < 1 || page_size < 1 || num_pages < 1 || max_pages_per_seq < 1)
+        return fail(DSAIDX_ERR_SHAPE, "rows=%d B=%d H=%d E=%d V=%d page_size=%d num_pages=%d max_pages_per_seq=%d", T,
+                    B, H, E, V, page_size, num_pages, max_pages_per_seq);
+    if (q_dtype != DSAIDX_F32 && q_dtype != DSAIDX_BF16 && q_dtype != DSAIDX_FP8_E4M3)
+        return fail(DSAIDX_ERR_DTYPE, "q_dtype=%d", q_dtype);
+    if (latent_dtype != DSAIDX_F32 && latent_dtype != DSAIDX_BF16 && latent_dtype != DSAIDX_FP8_E4M3)
+        return fail(DSAIDX_ERR_DTYPE, "latent_dtype=%d", latent_dtype);
+    if (q_dtype != DSAIDX_BF16) return fail(DSAIDX_ERR_UNSUPPORTED, "queries must be bf16");
+    if (latent_dtype == DSAIDX_F32) return fail(DSAIDX_ERR_UNSUPPORTED, "the latent cache must be bf16 or fp8");
+    if ((latent_dtype == DSAIDX_FP8_E4M3) != (latent_scale != nullptr))
+        return fail(DSAIDX_ERR_SHAPE, "latent_scale goes with an fp8 latent cache, NULL with a bf16 one");
+    if (V != 512 || (E != 512 && E != 576))
+        return fail(DSAIDX_ERR_UNSUPPORTED, "E=%d V=%d (E 512 or 576, V 512)", E, V);
+    if (H > kMaxLatentHeads) return fail(DSAIDX_ERR_UNSUPPORTED, "H=%d > %d", H, kMaxLatentHeads);
+    if (page_size != 64) return fail(DSAIDX_ERR_UNSUPPORTED, "page_size=%d (64)", page_size);
+    if ((int64_t)max_pages_per_seq * page_size > kMaxLatentTokens || num_pages > kMaxLatentTokens / 64)
+        return fail(DSAIDX_ERR_UNSUPPORTED, "max_pages_per_seq=%d num_pages=%d (tables and pools of at most %d tokens)",
+                    max_pages_per_seq, num_pages, kMaxLatentTokens);
+    if ((int64_t)T * H > (1 << 24)) return fail(DSAIDX_ERR_UNSUPPORTED, "rows * H = %lld > 2^24", (long long)T * H);
+    if (!(scale - scale == 0.f)) return fail(DSAIDX_ERR_SHAPE, "scale must be finite");
+    if (T == 0) return DSAIDX_OK;
+    if (!q) return fail(DSAIDX_ERR_NULL, "q is NULL");
+    if (!latent_cache) return fail(DSAIDX_ERR_NULL, "latent_cache is NULL");
+    if (!block_table) return fail(DSAIDX_ERR_NULL, "block_table is NULL");
+    if (!out) return fail(DSAIDX_ERR_NULL, "out is NULL");
+    if (!aligned16(q) || !aligned16(latent_cache) || !aligned16(out))
+        return fail(DSAIDX_ERR_UNSUPPORTED, "q, latent_cache and out must be 16-byte aligned");
+    return DSAIDX_OK;
+}
+
+dsaidx_status latent_run(dsaidx::LatentArgs& a, int latent_dtype, float scale, void* workspace,
+                         size_t workspace_bytes, size_t need, const char* name, void* stream) {
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(DSAIDX_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    if (need > 0 && !aligned16(workspace)) return fail(DSAIDX_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
+    a.workspace = workspace;
+    a.scale_log2 = scale * 1.44269504088896341f;
+    const hipError_t e = dsaidx::launch_latent_attention(a, latent_dtype == DSAIDX_FP8_E4M3, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, name);
+    return DSAIDX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t indexer_latent_attention_topk_workspace_bytes(int T, int H, int E, int V, int topk) {
+    (void)V;
+    if (T < 1 || H < 1 || topk < 1) return 0;
+    return dsaidx::latent_topk_workspace_bytes(T, H, E, topk);
+}
+
+dsaidx_status indexer_latent_attention_topk(const void* q, int q_dtype, const void* latent_cache,
+                                            const float* latent_scale, int latent_dtype, const int32_t* block_table,
+                                            int max_pages_per_seq, int num_pages, const int32_t* topk_idx,
+                                            const int32_t* seq_ids, int B, int T, int H, int E, int V, int page_size,
+                                            int topk, float scale, void* out, float* lse, void* workspace,
+                                            size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    const dsaidx_status st = latent_check(q, q_dtype, latent_cache, latent_scale, latent_dtype, block_table,
+                                          max_pages_per_seq, num_pages, B, T, H, E, V, page_size, scale, out);
+    if (st != DSAIDX_OK) return st;
+    if (topk < 1) return fail(DSAIDX_ERR_SHAPE, "topk=%d must be >= 1", topk);
+    if (topk > kMaxL) return fail(DSAIDX_ERR_UNSUPPORTED, "topk=%d > %d", topk, kMaxL);
+    if (!seq_ids && T > B) return fail(DSAIDX_ERR_SHAPE, "T=%d > B=%d needs seq_ids", T, B);
+    if (T == 0) return DSAIDX_OK;
+    if (!topk_idx) return fail(DSAIDX_ERR_NULL, "topk_idx is NULL");
+    dsaidx::LatentArgs a{};
+    a.q = reinterpret_cast<const uint16_t*>(q);
+    a.cache = latent_cache;
+    a.cache_scale = latent_scale;
+    a.block_table = block_table;
+    a.idx = topk_idx;
+    a.seq_ids = seq_ids;
+    a.out = reinterpret_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.T = T;
+    a.H = H;
+    a.E = E;
+    a.B = B;
+    a.max_pages = max_pages_per_seq;
+    a.num_pages = num_pages;
+    a.K = topk;
+    return latent_run(a, latent_dtype, scale, workspace, workspace_bytes,
+                      indexer_latent_attention_topk_workspace_bytes(T, H, E, V, topk),
+                      "indexer_latent_attention_topk", stream);
+}
+
+size_t indexer_latent_attention_shared_workspace_bytes(int B, int H, int E, int V, int prefix_len,
+                                                       int max_context_len) {
+    (void)V;
+    if (B < 1 || H < 1 || prefix_len < 0 || max_context_len < 0) return 0;
+    return dsaidx::latent_shared_workspace_bytes(B, H, E, prefix_len, max_context_len);
+}
+
+dsaidx_status indexer_latent_attention_shared(const void* q, int q_dtype, const void* latent_cache,
+                                              const float* latent_scale, int latent_dtype,
+                                              const int32_t* prefix_table, int prefix_pages, int prefix_len,
+                                              const int32_t* block_table, int max_pages_per_seq, int num_pages,
+                                              const int32_t* context_lens, int max_context_len, int B, int H, int E,
+                                              int V, int page_size, float scale, void* out, float* lse,
+                                              void* workspace, size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    const dsaidx_status st = latent_check(q, q_dtype, latent_cache, latent_scale, latent_dtype, block_table,
+                                          max_pages_per_seq, num_pages, B < 1 ? 1 : B, B, H, E, V, page_size, scale,
+                                          out);
+    if (st != DSAIDX_OK) return st;
+    if (prefix_pages < 0 || prefix_len < 0 || (int64_t)prefix_len > (int64_t)prefix_pages * page_size)
+        return fail(DSAIDX_ERR_SHAPE, "prefix_len=%d in %d pages", prefix_len, prefix_pages);
+    if (max_context_len < 0 || (int64_t)max_context_len > (int64_t)max_pages_per_seq * page_size)
+        return fail(DSAIDX_ERR_SHAPE, "max_context_len=%d > max_pages_per_seq*page_size=%lld", max_context_len,
+                    (long long)max_pages_per_seq * page_size);
+    if (prefix_len > kMaxLatentTokens) return fail(DSAIDX_ERR_UNSUPPORTED, "prefix_len=%d > %d", prefix_len, kMaxLatentTokens);
+    if (B == 0) return DSAIDX_OK;
+    if (prefix_len > 0 && !prefix_table) return fail(DSAIDX_ERR_NULL, "prefix_table is NULL");
+    if (!context_lens) return fail(DSAIDX_ERR_NULL, "context_lens is NULL");
+    dsaidx::LatentArgs a{};
+    a.q = reinterpret_cast<const uint16_t*>(q);
+    a.cache = latent_cache;
+    a.cache_scale = latent_scale;
+    a.block_table = block_table;
+    a.prefix_table = prefix_table;
+    a.context_lens = context_lens;
+    a.out = reinterpret_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.T = B;
+    a.H = H;
+    a.E = E;
+    a.B = B;
+    a.max_pages = max_pages_per_seq;
+    a.num_pages = num_pages;
+    a.prefix_len = prefix_len;
+    a.max_ctx = max_context_len;
+    return latent_run(a, latent_dtype, scale, workspace, workspace_bytes,
+                      indexer_latent_attention_shared_workspace_bytes(B, H, E, V, prefix_len, max_context_len),
+                      "indexer_latent_attention_shared", stream);
+}
+
 dsaidx_status dsaidx_probe_mfma(int kind, int blocks, int iters, float* out, void* stream) {
     g_err[0] = 0;
     if (!out) return fail(DSAIDX_ERR_NULL, "out is NULL");

@@ -1,0 +1,49 @@
+// One row of values to the library's FP8 storage: E4M3FN codes and one fp32
+// scale, scale = max|x| / 448 (1 for an all-zero row), code = the E4M3FN value
+// nearest to the correctly rounded quotient x / scale, ties to even.
+#pragma once
+
+#include "common.h"
+
+namespace dsaidx {
+
+constexpr float kE4m3Max = 448.f;
+
+__device__ __forceinline__ float row_scale(float absmax) { return absmax > 0.f ? absmax / kE4m3Max : 1.f; }
+
+// Codes of eight consecutive elements of a row with this scale.
+__device__ __forceinline__ uint2 quant8(const float (&x)[8], float scale) {
+    float q[8];
+    if (scale >= 0x1p-80f && scale <= 0x1p+80f) {
+        // RN(x / scale) from y = RN(1 / scale) (one correctly rounded
+        // division per row): q0 = RN(x y) lies within 1.5 ulp of
+        // x / scale; one correction q1 = RN(q0 + r0 y) with the
+        // remainder r0 = x - scale q0 taken in an fma is within half an
+        // ulp plus a few 2^-24 ulp, so faithful; the remainder of a
+        // faithful quotient is exact, and one more correction from it
+        // gives the correctly rounded quotient (Markstein's theorem for
+        // a correctly rounded reciprocal).  No step overflows (|x y| <=
+        // 448.1) and the remainders stay off the subnormal grid for
+        // |x| >= 2^-100; below that the quotient is under 2^-19, whose
+        // E4M3 code is a signed zero on any path.  The sign is put back
+        // for x = -0, which the corrections turn into +0.
+        const float y = 1.f / scale;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float q0 = x[j] * y;
+            const float q1 = fmaf(fmaf(-scale, q0, x[j]), y, q0);
+            const float q2 = fmaf(fmaf(-scale, q1, x[j]), y, q1);
+            q[j] = fminf(fmaxf(__builtin_copysignf(q2, x[j]), -kE4m3Max), kE4m3Max);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = fminf(fmaxf(x[j] / scale, -kE4m3Max), kE4m3Max);
+    }
+    int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+    w0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w0, true);
+    int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
+    w1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], w1, true);
+    return uint2{(uint32_t)w0, (uint32_t)w1};
+}
+
+}  // namespace dsaidx

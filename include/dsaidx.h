@@ -345,6 +345,136 @@ dsaidx_status indexer_topk_gather_layers(const void* const* latent_caches, void*
                                          void* stream);
 
 /*
+ * indexer_cache_append_rope -- the layer's cache write: T new tokens' latent
+ * rows and index keys, rotated by their positions and appended to the two
+ * paged caches in one launch.
+ *
+ * Passage: "Study MLA Indexer", the data-flow diagram and the notes on its
+ * two caches (the key path rotates, then quantises; both caches are written
+ * before the scoring decision).  The last rope_dim columns of a latent row
+ * and the first rope_dim columns of an index key are rotated: with the
+ * token's position p, c_i = cos_sin[p][i] and s_i = cos_sin[p][rope_dim/2 + i],
+ * the pair (a, b) number i becomes (a c_i - b s_i, b c_i + a s_i) in fp32.
+ * Pair i is the rotated part's columns (2i, 2i + 1) when the row's
+ * `interleaved` argument is nonzero, (i, i + rope_dim/2) when it is zero.
+ * bf16 rows are rounded once to nearest even; fp8 rows are quantised as
+ * indexer_kcache_append does, from the rotated row.
+ *
+ *   kv           [T] rows of E elements in in_dtype (BF16 or F32), kv_stride
+ *                elements apart
+ *   index_k      [T] rows of D elements in in_dtype, index_stride apart, or
+ *                NULL (with k_cache and k_scale NULL): latent rows only
+ *   cos_sin      [rope_len][rope_dim] fp32
+ *   seq_ids, positions, block_table: as indexer_kcache_append.  A token whose
+ *                sequence lies outside [0, B), whose position lies outside
+ *                [0, min(rope_len, max_pages_per_seq * page_size)) or whose
+ *                page id lies outside [0, num_pages) is skipped
+ *   latent_cache [num_pages][page_size][E] in latent_dtype (BF16, or
+ *                FP8_E4M3 codes with latent_scale [num_pages][page_size]
+ *                fp32, NULL with BF16), updated in place
+ *   k_cache, k_scale: as indexer_kcache_append, updated in place
+ * Slots no token addresses are not touched.  Two tokens of one call with the
+ * same (sequence, position) leave that slot's contents undefined.  T = 0 is
+ * a no-op.  No workspace.
+ *
+ * Supported: D = 128, page_size = 64, E a multiple of 8 up to 1024, rope_dim
+ * a multiple of 16 up to 128 (and E); rows, cos_sin and latent_cache 16-byte
+ * aligned, k_cache 8-byte.
+ */
+dsaidx_status indexer_cache_append_rope(const void* kv, int64_t kv_stride, int kv_interleaved, const void* index_k,
+                                        int64_t index_stride, int index_interleaved, int in_dtype,
+                                        const float* cos_sin, int rope_len, int rope_dim, const int32_t* seq_ids,
+                                        const int32_t* positions, const int32_t* block_table, int B,
+                                        int max_pages_per_seq, void* latent_cache, float* latent_scale,
+                                        int latent_dtype, uint8_t* k_cache, float* k_scale, int num_pages, int T,
+                                        int E, int D, int page_size, void* stream);
+
+/*
+ * indexer_latent_attention_topk -- the sparse attention that the selection is
+ * made for: every head of a query attends over the latent rows at the query's
+ * selected positions, read in place through the block table.
+ *
+ * Passage: "Study MLA Indexer", the data-flow diagram's last step, and
+ * "Lightning Indexer explained", section 1 (the core attention runs over the
+ * selected set only).  All heads share one E-wide row per token, whose first
+ * V columns are also its value:
+ *     S[t,h,j] = scale * q[t,h] . c[j]      over the query's selected rows j
+ *     out[t,h] = sum_j softmax_j(S) c[j][:V],  lse[t,h] = log sum_j exp S[t,h,j]
+ * Scores, sums and the softmax's statistics are fp32; the probabilities
+ * enter the second product rounded to bf16; out is rounded once to bf16.
+ * A query without a row gives out = 0 and lse = -inf.
+ *
+ *   q            [T][H][E] bf16 (q_dtype must be DSAIDX_BF16)
+ *   latent_cache [num_pages][page_size][E] in latent_dtype (BF16, or FP8_E4M3
+ *                codes with latent_scale [num_pages][page_size] fp32; NULL
+ *                with BF16).  fp8 codes enter the products exactly; the row's
+ *                scale multiplies its score and its probability
+ *   block_table  [B][max_pages_per_seq] int32 page ids
+ *   topk_idx     [T][topk] int32 positions in any order, e.g. the output of
+ *                indexer_decode_paged or indexer_prefill_chunk_paged.  An
+ *                entry outside [0, max_pages_per_seq * page_size), or whose
+ *                page id lies outside [0, num_pages), is no row (-1 pads); a
+ *                position listed twice counts twice
+ *   seq_ids      [T] int32 row of block_table of each query (outside [0, B):
+ *                a query without a row), or NULL: query t uses row t (T <= B)
+ *   out          out [T][H][V] bf16;  lse  out [T][H] fp32 or NULL
+ *   workspace    indexer_latent_attention_topk_workspace_bytes(T, H, E, V,
+ *                topk) bytes of caller-owned device memory, 16-byte aligned,
+ *                scratch (its contents on entry do not matter; two calls in
+ *                flight on one workspace race)
+ * T = 0 is a no-op.
+ *
+ * Supported: (E, V) = (576, 512) or (512, 512), 1 <= H <= 128, page_size = 64,
+ * 1 <= topk <= 131072, T * H <= 2^24, tables and pools of at most 2^27 tokens.
+ */
+dsaidx_status indexer_latent_attention_topk(const void* q, int q_dtype, const void* latent_cache,
+                                            const float* latent_scale, int latent_dtype, const int32_t* block_table,
+                                            int max_pages_per_seq, int num_pages, const int32_t* topk_idx,
+                                            const int32_t* seq_ids, int B, int T, int H, int E, int V, int page_size,
+                                            int topk, float scale, void* out, float* lse, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
+size_t indexer_latent_attention_topk_workspace_bytes(int T, int H, int E, int V, int topk);
+
+/*
+ * indexer_latent_attention_shared -- one decode step of B queries that share
+ * a long prefix: the prefix's rows are read once for the whole batch (the
+ * B * H query rows are stacked against them), each sequence's own rows once
+ * for its H heads, and the two parts are joined.
+ *
+ * The same attention as indexer_latent_attention_topk (shapes, types,
+ * rounding), over every position: query b sees the prefix's positions
+ * 0 .. prefix_len - 1, then its own 0 .. context_lens[b] - 1.  Position s of
+ * the prefix lives in page prefix_table[s / page_size], own position s of b
+ * in page block_table[b][s / page_size], slot s % page_size.  This is the
+ * attention of layers or contexts that do not select (short contexts, where
+ * every position would be selected: "Study MLA Indexer", the last of the
+ * "three whys").
+ *
+ *   prefix_table [prefix_pages] int32 page ids (NULL when prefix_len is 0)
+ *   prefix_len   host value in [0, prefix_pages * page_size]; 0: no prefix
+ *   block_table  [B][max_pages_per_seq] int32 page ids
+ *   context_lens [B] int32 (device), clamped to [0, max_context_len]
+ *   max_context_len  host bound, <= max_pages_per_seq * page_size
+ * A page id outside [0, num_pages) is a page without rows.  A query without
+ * a row gives out = 0 and lse = -inf.  B = 0 is a no-op.
+ *   workspace    indexer_latent_attention_shared_workspace_bytes(B, H, E, V,
+ *                prefix_len, max_context_len) bytes, as for topk
+ *
+ * Supported: as indexer_latent_attention_topk; prefix_len <= 2^27.
+ */
+dsaidx_status indexer_latent_attention_shared(const void* q, int q_dtype, const void* latent_cache,
+                                              const float* latent_scale, int latent_dtype,
+                                              const int32_t* prefix_table, int prefix_pages, int prefix_len,
+                                              const int32_t* block_table, int max_pages_per_seq, int num_pages,
+                                              const int32_t* context_lens, int max_context_len, int B, int H, int E,
+                                              int V, int page_size, float scale, void* out, float* lse,
+                                              void* workspace, size_t workspace_bytes, void* stream);
+
+size_t indexer_latent_attention_shared_workspace_bytes(int B, int H, int E, int V, int prefix_len,
+                                                       int max_context_len);
+
+/*
  * topk_select -- the token selector on its own: top-k of each row of a score
  * matrix.
  *
