@@ -545,7 +545,7 @@ def latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim: int, sc
     dev, K = q.device, topk_idx.shape[1]
     out = torch.empty((T, H, v_dim), dtype=torch.bfloat16, device=dev)
     lse = torch.empty((T, H), dtype=torch.float32, device=dev) if want_lse else None
-    nws = lib.indexer_latent_attention_topk_workspace_bytes(T, H, E, v_dim, K)
+    nws = lib.indexer_latent_attention_topk_workspace_bytes(T, H, E, v_dim, K, dt)
     ws = workspace if workspace is not None and workspace.numel() >= nws else _workspace(nws, dev)
     with torch.cuda.device(dev):
         st = lib.indexer_latent_attention_topk(_ptr(q), BF16, _ptr(latent_cache), _ptr(latent_scale), dt,
@@ -583,7 +583,7 @@ def latent_attention_shared(q, latent_cache, prefix_table, prefix_len: int, bloc
     out = torch.empty((B, H, v_dim), dtype=torch.bfloat16, device=dev)
     lse = torch.empty((B, H), dtype=torch.float32, device=dev) if want_lse else None
     prefix_len = int(prefix_len)
-    nws = lib.indexer_latent_attention_shared_workspace_bytes(B, H, E, v_dim, prefix_len, mcl)
+    nws = lib.indexer_latent_attention_shared_workspace_bytes(B, H, E, v_dim, prefix_len, mcl, dt)
     ws = workspace if workspace is not None and workspace.numel() >= nws else _workspace(nws, dev)
     with torch.cuda.device(dev):
         st = lib.indexer_latent_attention_shared(_ptr(q), BF16, _ptr(latent_cache), _ptr(latent_scale), dt,

@@ -51,13 +51,13 @@ SIGNATURES = {
                                                _c_int, _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int,
                                                _c_int, _c_int, _c_int, _c_float, _c_void_p, _c_void_p, _c_void_p,
                                                _c_size_t, _c_void_p]),
-    "indexer_latent_attention_topk_workspace_bytes": (_c_size_t, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "indexer_latent_attention_topk_workspace_bytes": (_c_size_t, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
     "indexer_latent_attention_shared": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int,
                                                  _c_int, _c_void_p, _c_int, _c_int, _c_void_p, _c_int, _c_int,
                                                  _c_int, _c_int, _c_int, _c_int, _c_float, _c_void_p, _c_void_p,
                                                  _c_void_p, _c_size_t, _c_void_p]),
     "indexer_latent_attention_shared_workspace_bytes": (_c_size_t, [_c_int, _c_int, _c_int, _c_int, _c_int,
-                                                                    _c_int]),
+                                                                    _c_int, _c_int]),
     "dsaidx_probe_mfma": (_c_int, [_c_int, _c_int, _c_int, _c_void_p, _c_void_p]),
     "dsaidx_probe_page_read": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_void_p, _c_void_p]),
     "dsaidx_status_string": (ctypes.c_char_p, [_c_int]),

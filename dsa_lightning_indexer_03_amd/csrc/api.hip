@@ -293,10 +293,10 @@ dsaidx_status latent_run(dsaidx::LatentArgs& a, int latent_dtype, float scale, v
 
 extern "C" {
 
-size_t indexer_latent_attention_topk_workspace_bytes(int T, int H, int E, int V, int topk) {
-    (void)V;
+size_t indexer_latent_attention_topk_workspace_bytes(int T, int H, int E, int V, int topk, int latent_dtype) {
+    (void)E; (void)V;
     if (T < 1 || H < 1 || topk < 1) return 0;
-    return dsaidx::latent_topk_workspace_bytes(T, H, E, topk);
+    return dsaidx::latent_topk_workspace_bytes(T, H, topk, latent_dtype == DSAIDX_FP8_E4M3);
 }
 
 dsaidx_status indexer_latent_attention_topk(const void* q, int q_dtype, const void* latent_cache,
@@ -331,15 +331,15 @@ dsaidx_status indexer_latent_attention_topk(const void* q, int q_dtype, const vo
     a.num_pages = num_pages;
     a.K = topk;
     return latent_run(a, latent_dtype, scale, workspace, workspace_bytes,
-                      indexer_latent_attention_topk_workspace_bytes(T, H, E, V, topk),
+                      indexer_latent_attention_topk_workspace_bytes(T, H, E, V, topk, latent_dtype),
                       "indexer_latent_attention_topk", stream);
 }
 
 size_t indexer_latent_attention_shared_workspace_bytes(int B, int H, int E, int V, int prefix_len,
-                                                       int max_context_len) {
-    (void)V;
+                                                       int max_context_len, int latent_dtype) {
+    (void)E; (void)V;
     if (B < 1 || H < 1 || prefix_len < 0 || max_context_len < 0) return 0;
-    return dsaidx::latent_shared_workspace_bytes(B, H, E, prefix_len, max_context_len);
+    return dsaidx::latent_shared_workspace_bytes(B, H, prefix_len, max_context_len, latent_dtype == DSAIDX_FP8_E4M3);
 }
 
 dsaidx_status indexer_latent_attention_shared(const void* q, int q_dtype, const void* latent_cache,
@@ -381,7 +381,8 @@ dsaidx_status indexer_latent_attention_shared(const void* q, int q_dtype, const 
     a.prefix_len = prefix_len;
     a.max_ctx = max_context_len;
     return latent_run(a, latent_dtype, scale, workspace, workspace_bytes,
-                      indexer_latent_attention_shared_workspace_bytes(B, H, E, V, prefix_len, max_context_len),
+                      indexer_latent_attention_shared_workspace_bytes(B, H, E, V, prefix_len, max_context_len,
+                                                                      latent_dtype),
                       "indexer_latent_attention_shared", stream);
 }
 

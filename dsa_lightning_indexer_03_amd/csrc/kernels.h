@@ -172,8 +172,8 @@ hipError_t launch_kcache_append(const KcacheArgs& a, int dtype, hipStream_t stre
 hipError_t launch_topk_gather(const GatherArgs& a, hipStream_t stream);
 hipError_t launch_topk_gather_layers(const GatherLayersArgs& a, hipStream_t stream);
 hipError_t launch_cache_append_rope(const AppendRopeArgs& a, bool f32, bool fp8, hipStream_t stream);
-size_t latent_topk_workspace_bytes(int T, int H, int E, int K);
-size_t latent_shared_workspace_bytes(int B, int H, int E, int prefix_len, int max_ctx);
+size_t latent_topk_workspace_bytes(int T, int H, int K, bool fp8);
+size_t latent_shared_workspace_bytes(int B, int H, int prefix_len, int max_ctx, bool fp8);
 hipError_t launch_latent_attention(const LatentArgs& a, bool fp8, hipStream_t stream);
 // Measurement probes (csrc/probes.hip).
 hipError_t launch_probe_mfma(int kind, int blocks, int iters, float* out, hipStream_t stream);

@@ -6,130 +6,568 @@
 //
 // The keys of query t are the rows at its selected positions (topk), or the
 // rows of a prefix that the whole batch shares followed by the sequence's own
-// (shared).
+// (shared).  "Study MLA Indexer", the data-flow diagram's last step; "Lightning
+// Indexer explained", section 1.
 //
-// Layout: one wave per query and head.  Lane l holds columns 8l .. 8l+7 of
-// the query and of the sum, and column V + l of the query when E > V; the dot
-// product is a wave sum, the softmax is kept as a running maximum and sum.
+// One workgroup of four waves takes a block of up to 16*MT query rows (a
+// query's heads, or the stacked heads of several queries for the shared
+// prefix) and a run of 64-key tiles.  A tile is staged once in LDS and serves
+// both products:
+//   S^T (16 keys x rows) = K Q^T: wave w has keys 16w .. 16w+15, the queries
+//     sit in its registers;
+//   O^T (128 columns x rows) += V^T P^T: wave w has columns 128w .. 128w+127,
+//     the probabilities of all 64 keys come through LDS as bf16, the values
+//     are read transposed from the same tile.
+// Both leave a lane with one query row (lane % 16 of each 16-row block), so
+// the softmax's factors are per lane.  The exponent's reference m is common to
+// the four waves and only moves when a score exceeds it by more than
+// 2^kSlack (base 2): a flag in LDS, read behind the barrier that the exchange of P needs
+// anyway, sends all waves through a second pass that takes the tile's maximum,
+// rescales and rewrites P.  Sums are fp32; P is rounded to bf16 (the second
+// product's operand; its sum is taken before the rounding).
+// When the rows alone do not fill the GPU the key tiles are split over
+// workgroups, whose fp32 partial sums a second kernel joins by their maxima.
 #include "common.h"
+#include "device_once.h"
 #include "kernels.h"
 
 namespace dsaidx {
 namespace {
 
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
 constexpr int kPage = 64;
+constexpr int kTile = 64;      // keys of a tile
 constexpr int kThreads = 256;
 constexpr int kV = 512;
+constexpr float kSlack = 16.f;
 
-__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+// LDS: two tiles, P, the exchange of maxima and sums, flags.  A tile's row is
+// its 512 value columns padded by 16 bytes, so the 16 rows of an operand read
+// (and the 16 x 32-byte blocks of a transposed one) fall on all 64 banks; the
+// rotary columns lie behind, 128 bytes a row, their 16-byte pieces permuted
+// within the row.
+constexpr int kRowB = 2 * kV + 16;
+constexpr int kMainB = kTile * kRowB;
+constexpr int kRopeB = kTile * 128;
+constexpr int kTileB = kMainB + kRopeB;
+constexpr int kPOff = 2 * kTileB;
+__host__ __device__ constexpr int p_bytes(int mt) { return mt * 16 * 128; }
+__host__ __device__ constexpr int red_off(int mt) { return kPOff + p_bytes(mt); }   // [4][16 mt] floats
+__host__ __device__ constexpr int scale_off(int mt) { return red_off(mt) + 4 * 16 * mt * 4; }  // [2][64] floats
+__host__ __device__ constexpr int flag_off(int mt) { return scale_off(mt) + 512; }
+__host__ __device__ constexpr int lds_bytes(int mt) { return flag_off(mt) + 16; }
+static_assert(lds_bytes(4) <= 160 * 1024, "LDS budget");
 
-template <bool FP8>
-__device__ __forceinline__ void load_row(const LatentArgs& a, int64_t row, int lane, float (&x)[8], float& r) {
-    r = 0.f;
-    if constexpr (FP8) {
-        const uint8_t* p = reinterpret_cast<const uint8_t*>(a.cache) + row * a.E;
-        const float s = a.cache_scale[row];
-        const uint2 u = *reinterpret_cast<const uint2*>(p + 8 * lane);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)(j ? u.y : u.x), false);
-            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)(j ? u.y : u.x), true);
-            x[4 * j] = lo[0] * s;
-            x[4 * j + 1] = lo[1] * s;
-            x[4 * j + 2] = hi[0] * s;
-            x[4 * j + 3] = hi[1] * s;
+struct Plan {
+    int n_prefix, n_own;   // workgroups of each part (multiples of 8)
+    int rb;                // prefix: row blocks of all T * H rows
+    int sp, lp;            // prefix: splits, tiles of a split
+    int hb;                // own rows or selection: row blocks of one query's H rows
+    int so, lo;            //   splits, tiles of a split
+    int slots;             // partial results per row (1: written directly)
+    float* part_o;         // [slots][T * H][V]
+    float2* part_ml;       // [slots][T * H] (maximum, sum)
+};
+
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// 16 bytes per lane from base + off (off per lane) straight to LDS byte
+// address lds + 16 * lane.  Written as asm so that later LDS reads of the
+// other tile do not wait for it; it has no register result, and the kernel
+// waits for vmcnt itself before the tile is read.
+__device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void copy_to_lds(const void* p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
+}
+
+// Eight E4M3 codes -> eight bf16 (exact).
+__device__ __forceinline__ v4i widen8(uint2 c) {
+    return v4i{(int)fp8x2_to_bf16x2<false>((int)c.x), (int)fp8x2_to_bf16x2<true>((int)c.x),
+               (int)fp8x2_to_bf16x2<false>((int)c.y), (int)fp8x2_to_bf16x2<true>((int)c.y)};
+}
+
+template <int KD, int MT, bool TOPK, bool FP8>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_attention_kernel(LatentArgs a, Plan p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int E = 32 * KD;
+    constexpr int RB = FP8 ? E : 2 * E;   // bytes of a cached row
+    const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
+    const int n = lane & 15, g = lane >> 4;
+    const int total = a.T * a.H;
+
+    // ---- which rows, which keys ----
+    // Workgroups go to the 8 XCDs in turn; the ones that read the same keys
+    // follow each other on one XCD.
+    int r0, nrows, t0, t1, slot, len;
+    const int32_t* table;
+    const int32_t* idx = nullptr;
+    {
+        const int id = blockIdx.x;
+        if (!TOPK && id < p.n_prefix) {
+            const int w = (id & 7) * (p.n_prefix >> 3) + (id >> 3);
+            slot = w / p.rb;
+            if (slot >= p.sp) return;
+            r0 = (w % p.rb) * 16 * MT;
+            nrows = min(16 * MT, total - r0);
+            len = a.prefix_len;
+            table = a.prefix_table;
+            t0 = slot * p.lp;
+            t1 = min(t0 + p.lp, (len + kTile - 1) / kTile);
+        } else {
+            const int id2 = id - p.n_prefix;
+            const int w = (id2 & 7) * (p.n_own >> 3) + (id2 >> 3);
+            const int q = w / (p.hb * p.so), s = w / p.hb % p.so, h = w % p.hb * 16 * MT;
+            if (q >= a.T) return;
+            r0 = q * a.H + h;
+            nrows = min(16 * MT, a.H - h);
+            slot = p.sp + s;
+            t0 = s * p.lo;
+            if constexpr (TOPK) {
+                const int b = a.seq_ids ? a.seq_ids[q] : q;
+                const bool ok = b >= 0 && b < a.B;
+                table = a.block_table + (int64_t)(ok ? b : 0) * a.max_pages;
+                idx = a.idx + (int64_t)q * a.K;
+                len = ok ? a.K : 0;
+            } else {
+                table = a.block_table + (int64_t)q * a.max_pages;
+                len = min(max(a.context_lens[q], 0), a.max_ctx);
+            }
+            t1 = min(t0 + p.lo, (len + kTile - 1) / kTile);
         }
-        if (a.E > kV) r = __builtin_amdgcn_cvt_f32_fp8((int)p[kV + lane], 0) * s;
-    } else {
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(a.cache) + row * a.E;
-        const v4i u = *reinterpret_cast<const v4i*>(p + 8 * lane);
+    }
+
+    // ---- queries: B operand of 16 rows x 32 columns, in registers ----
+    v8bf Q[MT][KD];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = bf16_lo((uint32_t)u[j]);
-            x[2 * j + 1] = bf16_hi((uint32_t)u[j]);
+    for (int mt = 0; mt < MT; ++mt) {
+        const uint16_t* qp = a.q + (int64_t)(r0 + min(16 * mt + n, nrows - 1)) * E + 8 * g;
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks) Q[mt][ks] = *reinterpret_cast<const v8bf*>(qp + 32 * ks);
+    }
+    v4f O[8][MT];
+    float m[MT], l[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        m[mt] = -__builtin_inff();
+        l[mt] = 0.f;
+#pragma unroll
+        for (int ct = 0; ct < 8; ++ct) O[ct][mt] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+    int* flag = reinterpret_cast<int*>(smem + flag_off(MT));
+    float* red = reinterpret_cast<float*>(smem + red_off(MT));
+    if (threadIdx.x < 2) flag[threadIdx.x] = 0;
+
+    // ---- the rows of a tile: lane i holds entry i's row of the pool ----
+    auto entry = [&](int t) -> int {   // position (topk) of entry `lane`, -1: none
+        const int j = t * kTile + lane;
+        if constexpr (TOPK) return j < len ? idx[j] : -1;
+        return j < len ? j : -1;
+    };
+    auto page_of = [&](int s) -> int {
+        return s >= 0 && s / kPage < a.max_pages ? table[s / kPage] : -1;
+    };
+    auto page_of_tile = [&](int s, int t) -> int {
+        if constexpr (TOPK) return page_of(s);
+        return t < t1 ? table[t] : -1;
+    };
+    auto live = [&](int s, int page) { return s >= 0 && page >= 0 && page < a.num_pages; };
+
+    // The rows of tiles t+1, t+2, t+3 are found while tile t is computed: the
+    // entries (three tiles ahead) and their page ids (two ahead) are loads in
+    // flight, and the next tile's rows are copied from its ids.
+    int row = 0;          // the tile to copy: rows, and which entries have one
+    uint64_t mask = 0;
+    int s1, page1, s2;    // entries and page ids of the next tile, entries of the one behind it
+    auto resolve = [&](int s, int page) {
+        const bool ok = live(s, page);
+        mask = wave_ballot(ok);
+        row = ok ? page * kPage + (s & (kPage - 1)) : 0;
+    };
+    // first tile at or behind t with an entry, and the state from there
+    auto seek = [&](int t) -> int {
+        for (; t < t1; ++t) {
+            const int s = entry(t);
+            resolve(s, page_of_tile(s, t));
+            if (mask) break;
         }
-        if (a.E > kV) r = bf16_lo(p[kV + lane]);
+        s1 = entry(t + 1);
+        s2 = entry(t + 2);
+        page1 = page_of_tile(s1, t + 1);
+        return t;
+    };
+    auto advance = [&](int t) -> int {
+        resolve(s1, page1);
+        if (mask == 0) return seek(t + 2);
+        s1 = s2;
+        page1 = page_of_tile(s2, t + 2);
+        s2 = entry(t + 3);
+        return t + 1;
+    };
+
+    const int kb = 16 * wave;   // this wave's rows of a tile
+    uint2 main8[FP8 ? 16 : 1], rope8[FP8 ? 2 : 1];
+    float kscale = 0.f;
+    auto stage = [&](int buf) {
+        unsigned char* dst = smem + buf * kTileB;
+        const unsigned char* cache = reinterpret_cast<const unsigned char*>(a.cache);
+        const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)dst;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const uint32_t rid = (uint32_t)__builtin_amdgcn_readlane(row, kb + r);
+            const unsigned char* src = cache + (uint64_t)rid * RB;
+            if (mask >> (kb + r) & 1) {
+                if constexpr (FP8) main8[r] = *reinterpret_cast<const uint2*>(src + 8 * lane);
+                else copy_to_lds(src, 16 * lane, lds + (kb + r) * kRowB);
+            } else {   // no row: its probability is zero, and zero its values must be
+                if constexpr (FP8) main8[r] = uint2{0, 0};
+                else *reinterpret_cast<v4i*>(dst + (kb + r) * kRowB + 16 * lane) = v4i{0, 0, 0, 0};
+            }
+        }
+        if constexpr (KD > 16) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = kb + 8 * j + (lane >> 3);
+                const int piece = (lane & 7) ^ ((r >> 1) & 7);
+                const uint32_t rid = (uint32_t)__shfl(row, r);
+                if constexpr (FP8)
+                    rope8[j] = *reinterpret_cast<const uint2*>(cache + (uint64_t)rid * RB + kV + 8 * piece);
+                else
+                    copy_to_lds(cache + (uint64_t)rid * RB + 2 * kV + 16 * piece,
+                                lds + kMainB + (kb + 8 * j) * 128);
+            }
+        }
+        if constexpr (FP8) kscale = mask >> lane & 1 ? a.cache_scale[row] : 0.f;
+    };
+    // fp8 rows: widened on their way into the tile
+    auto stage_store = [&](int buf) {
+        if constexpr (FP8) {
+            unsigned char* dst = smem + buf * kTileB;
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                *reinterpret_cast<v4i*>(dst + (kb + r) * kRowB + 16 * lane) = widen8(main8[r]);
+            if constexpr (KD > 16)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    *reinterpret_cast<v4i*>(dst + kMainB + (kb + 8 * j) * 128 + 16 * lane) = widen8(rope8[j]);
+            if ((lane >> 4) == wave) reinterpret_cast<float*>(smem + scale_off(MT))[64 * buf + lane] = kscale;
+        }
+    };
+
+    int t = seek(t0);
+    int buf = 0;
+    if (t < t1) {
+        stage(0);
+        stage_store(0);
+    }
+    while (t < t1) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the tile
+        lds_barrier();
+        const uint32_t live4 = (uint32_t)(mask >> (kb + 4 * g)) & 15u;
+        const int t_next = t + 1 < t1 ? advance(t) : t1;
+        if (t_next < t1) stage(buf ^ 1);
+
+        const unsigned char* tile = smem + buf * kTileB;
+        // ---- scores: S^T, keys 4g .. 4g+3 of this wave's 16, row n of each block ----
+        v4f S[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) S[mt] = v4f{0.f, 0.f, 0.f, 0.f};
+        {
+            const unsigned char* kp = tile + (kb + n) * kRowB + 16 * g;
+#pragma unroll
+            for (int ks = 0; ks < KD; ++ks) {
+                const unsigned char* at =
+                    ks < 16 ? kp + 64 * ks
+                            : tile + kMainB + (kb + n) * 128 + 16 * ((4 * (ks - 16) + g) ^ ((n >> 1) & 7));
+                const v8bf K = *reinterpret_cast<const v8bf*>(at);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    S[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(K, Q[mt][ks], S[mt], 0, 0, 0);
+            }
+        }
+        // ---- softmax against the common reference ----
+        float ks4[4] = {1.f, 1.f, 1.f, 1.f};
+        if constexpr (FP8) {
+            const v4f s4 = *reinterpret_cast<const v4f*>(smem + scale_off(MT) + 256 * buf + 4 * (kb + 4 * g));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ks4[i] = s4[i];
+        }
+        float top[MT], sum[MT];
+        bool rise = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = S[mt][i] * (FP8 ? ks4[i] * a.scale_log2 : a.scale_log2);
+                S[mt][i] = live4 >> i & 1 ? x : -__builtin_inff();
+            }
+            top[mt] = fmaxf(fmaxf(S[mt][0], S[mt][1]), fmaxf(S[mt][2], S[mt][3]));
+            rise |= top[mt] > m[mt] + kSlack;
+        }
+        auto write_p = [&]() {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const float ref = m[mt] == -__builtin_inff() ? 0.f : m[mt];
+                float pr[4];
+                sum[mt] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    pr[i] = __builtin_amdgcn_exp2f(S[mt][i] - ref);
+                    sum[mt] += pr[i];
+                    if (FP8) pr[i] *= ks4[i];
+                }
+                // P[row][key], 128 bytes a row; 16-byte piece 4(w/2) + g holds the keys 4g .. 4g+3
+                // of waves 2(w/2) and 2(w/2) + 1; pieces permuted by the row
+                const v2bf lo = v2bf{(__bf16)pr[0], (__bf16)pr[1]}, hi = v2bf{(__bf16)pr[2], (__bf16)pr[3]};
+                *reinterpret_cast<uint2*>(smem + kPOff + (16 * mt + n) * 128 +
+                                          16 * ((4 * (wave >> 1) + g) ^ ((n >> 1) & 7)) + 8 * (wave & 1)) =
+                    uint2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+            }
+        };
+        write_p();
+        if (wave_ballot(rise) && lane == 0) flag[buf] = 1;
+        if (threadIdx.x == 0) flag[buf ^ 1] = 0;
+        lds_barrier();
+        if (uniform(flag[buf])) {
+            // the reference moves to the tile's maximum where that is above it
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float x = top[mt];
+                x = fmaxf(x, __shfl_xor(x, 16, kWave));
+                x = fmaxf(x, __shfl_xor(x, 32, kWave));
+                if (g == 0) red[wave * 16 * MT + 16 * mt + n] = x;
+            }
+            lds_barrier();
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float x = m[mt];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) x = fmaxf(x, red[w * 16 * MT + 16 * mt + n]);
+                const float f = m[mt] == x ? 1.f : __builtin_amdgcn_exp2f(m[mt] - x);
+                m[mt] = x;
+                l[mt] *= f;
+#pragma unroll
+                for (int ct = 0; ct < 8; ++ct) O[ct][mt] *= f;
+            }
+            write_p();
+            lds_barrier();
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) l[mt] += sum[mt];
+
+        // ---- O^T += V^T P^T ----
+        v8bf P[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+                P[mt][kk] = *reinterpret_cast<const v8bf*>(smem + kPOff + (16 * mt + n) * 128 +
+                                                           16 * ((4 * kk + g) ^ ((n >> 1) & 7)));
+        const unsigned char* vp = tile + (4 * g + (n >> 2)) * kRowB + 8 * (n & 3) + 256 * wave;
+#pragma unroll
+        for (int ct = 0; ct < 8; ++ct)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                // columns 16ct .. 16ct+15 of keys 4g .. 4g+3 of two 16-key groups
+                const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vp + 32 * ct + 32 * kk * kRowB));
+                const v4s hi =
+                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vp + 32 * ct + (32 * kk + 16) * kRowB));
+                const v8bf W = __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    O[ct][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(W, P[mt][kk], O[ct][mt], 0, 0, 0);
+            }
+        if (t_next < t1) stage_store(buf ^ 1);
+        t = t_next;
+        buf ^= 1;
+    }
+
+    // ---- join the waves' sums, write ----
+    lds_barrier();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        float x = l[mt];
+        x += __shfl_xor(x, 16, kWave);
+        x += __shfl_xor(x, 32, kWave);
+        if (g == 0) red[wave * 16 * MT + 16 * mt + n] = x;
+    }
+    lds_barrier();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) x += red[w * 16 * MT + 16 * mt + n];
+        if (16 * mt + n >= nrows) continue;
+        const int64_t r = r0 + 16 * mt + n;
+        if (p.slots == 1) {
+            const float inv = x > 0.f ? 1.f / x : 0.f;
+#pragma unroll
+            for (int ct = 0; ct < 8; ++ct) {
+                const v4f o = O[ct][mt] * inv;
+                const v2bf lo = v2bf{(__bf16)o[0], (__bf16)o[1]}, hi = v2bf{(__bf16)o[2], (__bf16)o[3]};
+                *reinterpret_cast<uint2*>(a.out + r * kV + 128 * wave + 16 * ct + 4 * g) =
+                    uint2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+            }
+            if (a.lse && wave == 0 && g == 0)
+                a.lse[r] = x > 0.f ? (m[mt] + log2f(x)) * 0.693147180559945f : -__builtin_inff();
+        } else {
+            const int64_t at = (int64_t)slot * total + r;
+            if (x != 0.f)   // (NaN too)
+#pragma unroll
+                for (int ct = 0; ct < 8; ++ct)
+                    *reinterpret_cast<v4f*>(p.part_o + at * kV + 128 * wave + 16 * ct + 4 * g) = O[ct][mt];
+            if (wave == 0 && g == 0) p.part_ml[at] = float2{m[mt], x};
+        }
     }
 }
 
-template <bool FP8>
+// Joins the slots' partial results of a row: one wave per row, 8 columns a lane.
 __global__ void __launch_bounds__(kThreads)
-latent_attention_kernel(LatentArgs a) {
+latent_join_kernel(LatentArgs a, Plan p) {
     const int lane = threadIdx.x & 63;
-    const int64_t w = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 6;
-    if (w >= (int64_t)a.T * a.H) return;
-    const int t = (int)(w / a.H);
-    const uint16_t* qp = a.q + w * a.E;
-    float q[8], qr = 0.f;
-    {
-        const v4i u = *reinterpret_cast<const v4i*>(qp + 8 * lane);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            q[2 * j] = bf16_lo((uint32_t)u[j]);
-            q[2 * j + 1] = bf16_hi((uint32_t)u[j]);
-        }
-        if (a.E > kV) qr = bf16_lo(qp[kV + lane]);
+    const int total = a.T * a.H;
+    const int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 6;
+    if (r >= total) return;
+    float top = -__builtin_inff();
+    for (int s = 0; s < p.slots; ++s) {
+        const float2 ml = p.part_ml[(int64_t)s * total + r];
+        if (ml.y != 0.f) top = fmaxf(top, ml.x);
     }
-    float m = -__builtin_inff(), l = 0.f, o[8];
+    float l = 0.f, o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = 0.f;
-
-    auto key = [&](int64_t row) {
-        float x[8], r;
-        load_row<FP8>(a, row, lane, x, r);
-        float d = qr * r;
+    for (int s = 0; s < p.slots; ++s) {
+        const int64_t at = (int64_t)s * total + r;
+        const float2 ml = p.part_ml[at];
+        if (ml.y == 0.f) continue;
+        const float w = __builtin_amdgcn_exp2f(ml.x - top);
+        l += w * ml.y;
+        const v4f x = *reinterpret_cast<const v4f*>(p.part_o + at * kV + 8 * lane);
+        const v4f y = *reinterpret_cast<const v4f*>(p.part_o + at * kV + 8 * lane + 4);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d = fmaf(q[j], x[j], d);
-#pragma unroll
-        for (int i = 32; i >= 1; i >>= 1) d += __shfl_xor(d, i, kWave);
-        d *= a.scale_log2;
-        if (d == -__builtin_inff()) return;
-        const float m2 = fmaxf(m, d);
-        const float f = exp2f(m - m2), p = exp2f(d - m2);
-        m = m2;
-        l = l * f + p;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = o[j] * f + p * x[j];
-    };
-    auto paged = [&](const int32_t* table, int n) {
-        for (int j = 0; j < n; ++j) {
-            const int page = table[j / kPage];
-            if (page >= 0 && page < a.num_pages) key((int64_t)page * kPage + j % kPage);
+        for (int j = 0; j < 4; ++j) {
+            o[j] += w * x[j];
+            o[4 + j] += w * y[j];
         }
-    };
-    if (a.idx) {
-        const int b = a.seq_ids ? a.seq_ids[t] : t;
-        if (b >= 0 && b < a.B) {
-            const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
-            for (int j = 0; j < a.K; ++j) {
-                const int s = a.idx[(int64_t)t * a.K + j];
-                if (s < 0 || s / kPage >= a.max_pages) continue;
-                const int page = table[s / kPage];
-                if (page >= 0 && page < a.num_pages) key((int64_t)page * kPage + s % kPage);
-            }
-        }
-    } else {
-        paged(a.prefix_table, a.prefix_len);
-        paged(a.block_table + (int64_t)t * a.max_pages, min(max(a.context_lens[t], 0), a.max_ctx));
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
     v8bf y;
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = (__bf16)(o[j] * inv);
-    *reinterpret_cast<v8bf*>(a.out + w * kV + 8 * lane) = y;
-    if (a.lse && lane == 0) a.lse[w] = l > 0.f ? (m + log2f(l)) * 0.693147180559945f : -__builtin_inff();
+    *reinterpret_cast<v8bf*>(a.out + r * kV + 8 * lane) = y;
+    if (a.lse && lane == 0) a.lse[r] = l != 0.f ? (top + log2f(l)) * 0.693147180559945f : -__builtin_inff();
+}
+
+constexpr int kCUs = 256;
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+int pad8(int n) { return (n + 7) / 8 * 8; }
+
+// Row blocks of 64 where the rows fill them; fp8 tiles pass through registers,
+// which leaves room for 32.
+int blocks_of_16(int64_t rows, bool fp8) { return rows <= 16 ? 1 : rows <= 32 || fp8 ? 2 : 4; }
+
+// Tiles per workgroup that finish first: a workgroup costs its tiles and a
+// fixed part (queries, first tile, results) of about three tiles, the GPU runs
+// one per CU at a time, and joining costs about a tile per 16 slots.
+void split(int64_t rows_p, int tiles_p, int64_t rows_o, int tiles_o, Plan& p) {
+    double best = 1e30;
+    const int most = tiles_p > tiles_o ? tiles_p : tiles_o;
+    for (int len = 1;; len = len < 16 ? len + 1 : len + len / 8) {
+        if (len > most) len = most;
+        const int sp = ceil_div(tiles_p, len), so = ceil_div(tiles_o, len);
+        if (sp + so <= 64 || len == most) {
+            const int64_t n = rows_p * sp + rows_o * so;
+            const double cost = (double)ceil_div(n, kCUs) * (len + 3) + (sp + so > 1 ? 2 + (sp + so) / 16.0 : 0);
+            if (cost < best) {
+                best = cost;
+                p.sp = sp;
+                p.so = so;
+                p.lp = p.lo = len;
+            }
+        }
+        if (len >= most) break;
+    }
+}
+
+Plan make_plan(int T, int H, bool topk, int K, int prefix_len, int max_ctx, bool fp8, int* mt) {
+    Plan p{};
+    const int tiles_p = topk ? 0 : ceil_div(prefix_len, kTile);
+    int tiles_o = ceil_div(topk ? K : max_ctx, kTile);
+    if (tiles_p + tiles_o == 0) tiles_o = 1;   // nothing to see: one workgroup a row block writes that
+    *mt = blocks_of_16(tiles_p > 0 ? (int64_t)T * H : H, fp8);
+    p.rb = ceil_div((int64_t)T * H, 16 * *mt);
+    p.hb = ceil_div(H, 16 * *mt);
+    split(tiles_p ? p.rb : 0, tiles_p, tiles_o ? (int64_t)T * p.hb : 0, tiles_o, p);
+    p.n_prefix = pad8(p.rb * p.sp);
+    p.n_own = pad8(T * p.hb * p.so);
+    p.slots = p.sp + p.so;
+    return p;
+}
+
+size_t plan_bytes(const Plan& p, int T, int H) {
+    return p.slots == 1 ? 0 : (size_t)p.slots * T * H * (kV + 2) * sizeof(float);
+}
+
+template <int KD, int MT, bool TOPK, bool FP8>
+hipError_t run(const LatentArgs& a, const Plan& p, hipStream_t stream) {
+    static PerDevice<int> once;
+    const hipError_t e = set_lds_limit(once, (const void*)latent_attention_kernel<KD, MT, TOPK, FP8>, lds_bytes(MT));
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((latent_attention_kernel<KD, MT, TOPK, FP8>), dim3((unsigned)(p.n_prefix + p.n_own)),
+                       dim3(kThreads), lds_bytes(MT), stream, a, p);
+    return hipGetLastError();
+}
+
+template <int KD, int MT, bool TOPK>
+hipError_t run(const LatentArgs& a, const Plan& p, bool fp8, hipStream_t stream) {
+    if constexpr (MT <= 2)
+        if (fp8) return run<KD, MT, TOPK, true>(a, p, stream);
+    return run<KD, MT, TOPK, false>(a, p, stream);
+}
+
+template <int KD, int MT>
+hipError_t run(const LatentArgs& a, const Plan& p, bool fp8, hipStream_t stream) {
+    return a.idx ? run<KD, MT, true>(a, p, fp8, stream) : run<KD, MT, false>(a, p, fp8, stream);
+}
+
+template <int KD>
+hipError_t run(const LatentArgs& a, const Plan& p, int mt, bool fp8, hipStream_t stream) {
+    return mt == 1 ? run<KD, 1>(a, p, fp8, stream) : mt == 2 ? run<KD, 2>(a, p, fp8, stream)
+                                                             : run<KD, 4>(a, p, fp8, stream);
 }
 
 }  // namespace
 
-size_t latent_topk_workspace_bytes(int T, int H, int E, int K) { return 0; }
-size_t latent_shared_workspace_bytes(int B, int H, int E, int prefix_len, int max_ctx) { return 0; }
+// The caller's workspace holds the partial sums, then the (maximum, sum) pairs.
+size_t latent_topk_workspace_bytes(int T, int H, int K, bool fp8) {
+    int mt;
+    return plan_bytes(make_plan(T, H, true, K, 0, 0, fp8, &mt), T, H);
+}
+size_t latent_shared_workspace_bytes(int B, int H, int prefix_len, int max_ctx, bool fp8) {
+    int mt;
+    return plan_bytes(make_plan(B, H, false, 0, prefix_len, max_ctx, fp8, &mt), B, H);
+}
 
 hipError_t launch_latent_attention(const LatentArgs& a, bool fp8, hipStream_t stream) {
+    int mt;
+    Plan p = make_plan(a.T, a.H, a.idx != nullptr, a.K, a.prefix_len, a.max_ctx, fp8, &mt);
+    p.part_o = reinterpret_cast<float*>(a.workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)p.slots * a.T * a.H * kV);
+    hipError_t e = a.E == 576 ? run<18>(a, p, mt, fp8, stream) : run<16>(a, p, mt, fp8, stream);
+    if (e != hipSuccess || p.slots == 1) return e;
     const int64_t blocks = ((int64_t)a.T * a.H * 64 + kThreads - 1) / kThreads;
-    if (fp8) hipLaunchKernelGGL(latent_attention_kernel<true>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL(latent_attention_kernel<false>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a, p);
     return hipGetLastError();
 }
 

@@ -419,7 +419,7 @@ dsaidx_status indexer_cache_append_rope(const void* kv, int64_t kv_stride, int k
  *                a query without a row), or NULL: query t uses row t (T <= B)
  *   out          out [T][H][V] bf16;  lse  out [T][H] fp32 or NULL
  *   workspace    indexer_latent_attention_topk_workspace_bytes(T, H, E, V,
- *                topk) bytes of caller-owned device memory, 16-byte aligned,
+ *                topk, latent_dtype) bytes of caller-owned device memory, 16-byte aligned,
  *                scratch (its contents on entry do not matter; two calls in
  *                flight on one workspace race)
  * T = 0 is a no-op.
@@ -434,7 +434,7 @@ dsaidx_status indexer_latent_attention_topk(const void* q, int q_dtype, const vo
                                             int topk, float scale, void* out, float* lse, void* workspace,
                                             size_t workspace_bytes, void* stream);
 
-size_t indexer_latent_attention_topk_workspace_bytes(int T, int H, int E, int V, int topk);
+size_t indexer_latent_attention_topk_workspace_bytes(int T, int H, int E, int V, int topk, int latent_dtype);
 
 /*
  * indexer_latent_attention_shared -- one decode step of B queries that share
@@ -459,7 +459,7 @@ size_t indexer_latent_attention_topk_workspace_bytes(int T, int H, int E, int V,
  * A page id outside [0, num_pages) is a page without rows.  A query without
  * a row gives out = 0 and lse = -inf.  B = 0 is a no-op.
  *   workspace    indexer_latent_attention_shared_workspace_bytes(B, H, E, V,
- *                prefix_len, max_context_len) bytes, as for topk
+ *                prefix_len, max_context_len, latent_dtype) bytes, as for topk
  *
  * Supported: as indexer_latent_attention_topk; prefix_len <= 2^27.
  */
@@ -472,7 +472,7 @@ dsaidx_status indexer_latent_attention_shared(const void* q, int q_dtype, const 
                                               void* workspace, size_t workspace_bytes, void* stream);
 
 size_t indexer_latent_attention_shared_workspace_bytes(int B, int H, int E, int V, int prefix_len,
-                                                       int max_context_len);
+                                                       int max_context_len, int latent_dtype);
 
 /*
  * topk_select -- the token selector on its own: top-k of each row of a score

@@ -43,7 +43,7 @@ def test_append_rope_rejects_before_launch(lib, kw, status):
 def topk(lib, q=P, qd=1, lc=P, ls=None, ldt=1, bt=P, mpp=4, npg=4, idx=P, seq=None, B=2, T=2, H=16, E=576, V=512,
          ps=64, K=100, scale=0.1, out=P, ws=P, nws=None):
     if nws is None:
-        nws = lib.indexer_latent_attention_topk_workspace_bytes(T, H, E, V, K)
+        nws = lib.indexer_latent_attention_topk_workspace_bytes(T, H, E, V, K, ldt)
     return lib.indexer_latent_attention_topk(q, qd, lc, ls, ldt, bt, mpp, npg, idx, seq, B, T, H, E, V, ps, K, scale,
                                              out, None, ws, nws, None)
 
@@ -51,7 +51,7 @@ def topk(lib, q=P, qd=1, lc=P, ls=None, ldt=1, bt=P, mpp=4, npg=4, idx=P, seq=No
 def shared(lib, q=P, qd=1, lc=P, ls=None, ldt=1, pt=P, np_=2, pl=100, bt=P, mpp=4, npg=4, cl=P, mcl=256, B=2, H=16,
            E=576, V=512, ps=64, scale=0.1, out=P, ws=P, nws=None):
     if nws is None:
-        nws = lib.indexer_latent_attention_shared_workspace_bytes(B, H, E, V, pl, mcl)
+        nws = lib.indexer_latent_attention_shared_workspace_bytes(B, H, E, V, pl, mcl, ldt)
     return lib.indexer_latent_attention_shared(q, qd, lc, ls, ldt, pt, np_, pl, bt, mpp, npg, cl, mcl, B, H, E, V, ps,
                                                scale, out, None, ws, nws, None)
 
@@ -67,7 +67,8 @@ COMMON = [
 
 @pytest.mark.parametrize("kw,status", COMMON + [
     (dict(idx=None), NULL), (dict(K=0), SHAPE), (dict(K=131073), UNSUP), (dict(T=3), SHAPE), (dict(T=-1), SHAPE),
-    (dict(T=1 << 21, seq=P), UNSUP), (dict(T=0), OK), (dict(T=0, idx=None, q=None), OK), (dict(B=0), SHAPE)])
+    (dict(T=1 << 21, seq=P), UNSUP), (dict(K=2048, ws=None), WS), (dict(K=2048, nws=8), WS),
+    (dict(K=2048, ws=P + 8), UNSUP), (dict(T=0), OK), (dict(T=0, idx=None, q=None), OK), (dict(B=0), SHAPE)])
 def test_topk_rejects_before_launch(lib, kw, status):
     assert topk(lib, **kw) == status
     assert status == OK or lib.dsaidx_last_error()
@@ -75,7 +76,8 @@ def test_topk_rejects_before_launch(lib, kw, status):
 
 @pytest.mark.parametrize("kw,status", COMMON + [
     (dict(pt=None), NULL), (dict(cl=None), NULL), (dict(pl=129), SHAPE), (dict(pl=-1), SHAPE), (dict(np_=-1), SHAPE),
-    (dict(mcl=257), SHAPE), (dict(mcl=-1), SHAPE), (dict(B=0), OK), (dict(B=-1), SHAPE)])
+    (dict(mcl=257), SHAPE), (dict(mcl=-1), SHAPE), (dict(B=0), OK), (dict(B=-1), SHAPE), (dict(ws=None), WS), (dict(nws=8), WS),
+    (dict(ws=P + 8), UNSUP)])
 def test_shared_rejects_before_launch(lib, kw, status):
     assert shared(lib, **kw) == status
     assert status == OK or lib.dsaidx_last_error()
