@@ -43,23 +43,32 @@ constexpr int kTile = 64;      // keys of a tile
 constexpr int kThreads = 256;
 constexpr int kV = 512;
 constexpr float kSlack = 16.f;
+constexpr int kAhead = 3;      // operand reads in flight
 
-// LDS: two tiles, P, the exchange of maxima and sums, flags.  A tile's row is
-// its 512 value columns padded by 16 bytes, so the 16 rows of an operand read
-// (and the 16 x 32-byte blocks of a transposed one) fall on all 64 banks; the
-// rotary columns lie behind, 128 bytes a row, their 16-byte pieces permuted
-// within the row.
-constexpr int kRowB = 2 * kV + 16;
+// LDS: two tiles, P, the exchange of maxima and sums, flags.  The 64 banks
+// serve 16 lanes of a 16-byte read at once (lanes 0-3, 12-15 and 20-27 are one
+// such group, 4-11, 16-19 and 28-31 the next), 32 lanes of an 8-byte one.  A
+// tile's row is its 512 value columns padded by 32 bytes: consecutive rows
+// start 8 banks apart, and both an operand read (16 rows, lane groups 16 bytes
+// apart) and a transposed one (8 rows of 32 bytes) use every bank once: 235
+// bytes a clock and CU against 127 with a padding of 16.  P's rows are padded
+// alike.  The rotary columns lie behind, 128 bytes a row, their 16-byte pieces
+// permuted within the row.
+constexpr int kRowB = 2 * kV + 32;
+constexpr int kPRowB = 2 * kTile + 32;
 constexpr int kMainB = kTile * kRowB;
 constexpr int kRopeB = kTile * 128;
 constexpr int kTileB = kMainB + kRopeB;
 constexpr int kPOff = 2 * kTileB;
-__host__ __device__ constexpr int p_bytes(int mt) { return mt * 16 * 128; }
+__host__ __device__ constexpr int p_bytes(int mt) { return mt * 16 * kPRowB; }
 __host__ __device__ constexpr int red_off(int mt) { return kPOff + p_bytes(mt); }   // [4][16 mt] floats
 __host__ __device__ constexpr int scale_off(int mt) { return red_off(mt) + 4 * 16 * mt * 4; }  // [2][64] floats
 __host__ __device__ constexpr int flag_off(int mt) { return scale_off(mt) + 512; }
 __host__ __device__ constexpr int lds_bytes(int mt) { return flag_off(mt) + 16; }
 static_assert(lds_bytes(4) <= 160 * 1024, "LDS budget");
+
+// What an entry without a row is copied from.
+__device__ __align__(16) const unsigned char kZeroRow[1152] = {};
 
 struct Plan {
     int n_prefix, n_own;   // workgroups of each part (multiples of 8)
@@ -82,9 +91,10 @@ __device__ __forceinline__ void lds_barrier() {
 // 16 bytes per lane from base + off (off per lane) straight to LDS byte
 // address lds + 16 * lane.  Written as asm so that later LDS reads of the
 // other tile do not wait for it; it has no register result, and the kernel
-// waits for vmcnt itself before the tile is read.
+// waits for vmcnt itself before the tile is read.  The copy may follow the
+// lane read that made its scalar base: five wait states, one for M0.
 __device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
                  ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void copy_to_lds(const void* p, uint32_t lds) {
@@ -156,6 +166,11 @@ latent_attention_kernel(LatentArgs a, Plan p) {
 #pragma unroll
         for (int ks = 0; ks < KD; ++ks) Q[mt][ks] = *reinterpret_cast<const v8bf*>(qp + 32 * ks);
     }
+    // 64 rows' queries fill most of the accumulation registers, which an
+    // operand may be read from as well
+    if constexpr (MT == 4)
+#pragma unroll
+        for (int i = 0; i < MT * KD && i < 60; ++i) asm volatile("" : "+a"(Q[i / KD][i % KD]));
     v4f O[8][MT];
     float m[MT], l[MT];
 #pragma unroll
@@ -168,6 +183,8 @@ latent_attention_kernel(LatentArgs a, Plan p) {
     int* flag = reinterpret_cast<int*>(smem + flag_off(MT));
     float* red = reinterpret_cast<float*>(smem + red_off(MT));
     if (threadIdx.x < 2) flag[threadIdx.x] = 0;
+
+    const int kb = 16 * wave;   // this wave's rows of a tile
 
     // ---- the rows of a tile: lane i holds entry i's row of the pool ----
     auto entry = [&](int t) -> int {   // position (topk) of entry `lane`, -1: none
@@ -187,13 +204,26 @@ latent_attention_kernel(LatentArgs a, Plan p) {
     // The rows of tiles t+1, t+2, t+3 are found while tile t is computed: the
     // entries (three tiles ahead) and their page ids (two ahead) are loads in
     // flight, and the next tile's rows are copied from its ids.
-    int row = 0;          // the tile to copy: rows, and which entries have one
-    uint64_t mask = 0;
+    // An entry without a row takes a row of zeros: its probability is zero,
+    // and zero its values must be.
+    int row = 0;                      // the tile to copy: rows,
+    uint64_t mask = 0;                // which entries have one,
+    uint64_t src = 0;                 // their addresses,
+    uint64_t rope_src[2] = {0, 0};    // and this lane's pieces of the rotary columns
     int s1, page1, s2;    // entries and page ids of the next tile, entries of the one behind it
     auto resolve = [&](int s, int page) {
         const bool ok = live(s, page);
         mask = wave_ballot(ok);
         row = ok ? page * kPage + (s & (kPage - 1)) : 0;
+        src = ok ? (uint64_t)a.cache + (uint64_t)(uint32_t)row * RB : (uint64_t)kZeroRow;
+        if constexpr (KD > 16)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = kb + 8 * j + (lane >> 3);
+                const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)src, r);
+                const uint32_t hi = (uint32_t)__shfl((int)(uint32_t)(src >> 32), r);
+                rope_src[j] = ((uint64_t)hi << 32 | lo) + (RB / E) * (kV + 8 * ((lane & 7) ^ ((r >> 1) & 7)));
+            }
     };
     // first tile at or behind t with an entry, and the state from there
     auto seek = [&](int t) -> int {
@@ -216,39 +246,24 @@ latent_attention_kernel(LatentArgs a, Plan p) {
         return t + 1;
     };
 
-    const int kb = 16 * wave;   // this wave's rows of a tile
     uint2 main8[FP8 ? 16 : 1], rope8[FP8 ? 2 : 1];
     float kscale = 0.f;
-    auto stage = [&](int buf) {
-        unsigned char* dst = smem + buf * kTileB;
-        const unsigned char* cache = reinterpret_cast<const unsigned char*>(a.cache);
-        const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)dst;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const uint32_t rid = (uint32_t)__builtin_amdgcn_readlane(row, kb + r);
-            const unsigned char* src = cache + (uint64_t)rid * RB;
-            if (mask >> (kb + r) & 1) {
-                if constexpr (FP8) main8[r] = *reinterpret_cast<const uint2*>(src + 8 * lane);
-                else copy_to_lds(src, 16 * lane, lds + (kb + r) * kRowB);
-            } else {   // no row: its probability is zero, and zero its values must be
-                if constexpr (FP8) main8[r] = uint2{0, 0};
-                else *reinterpret_cast<v4i*>(dst + (kb + r) * kRowB + 16 * lane) = v4i{0, 0, 0, 0};
-            }
+    // Part i of a tile's copy: row kb + i, then (i = 16, 17) 8 rows' rotary columns.
+    auto stage = [&](int buf, int i) {
+        const uint32_t lds =
+            (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)(smem + buf * kTileB);
+        if (i < 16) {
+            const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)src, kb + i);
+            const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(src >> 32), kb + i);
+            const unsigned char* from = reinterpret_cast<const unsigned char*>((uint64_t)hi << 32 | lo);
+            if constexpr (FP8) main8[i] = *reinterpret_cast<const uint2*>(from + 8 * lane);
+            else copy_to_lds(from, 16 * lane, lds + (kb + i) * kRowB);
+        } else {
+            if constexpr (FP8) rope8[i - 16] = *reinterpret_cast<const uint2*>(rope_src[i - 16]);
+            else
+                copy_to_lds(reinterpret_cast<const void*>(rope_src[i - 16]),
+                            lds + kMainB + (kb + 8 * (i - 16)) * 128);
         }
-        if constexpr (KD > 16) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = kb + 8 * j + (lane >> 3);
-                const int piece = (lane & 7) ^ ((r >> 1) & 7);
-                const uint32_t rid = (uint32_t)__shfl(row, r);
-                if constexpr (FP8)
-                    rope8[j] = *reinterpret_cast<const uint2*>(cache + (uint64_t)rid * RB + kV + 8 * piece);
-                else
-                    copy_to_lds(cache + (uint64_t)rid * RB + 2 * kV + 16 * piece,
-                                lds + kMainB + (kb + 8 * j) * 128);
-            }
-        }
-        if constexpr (FP8) kscale = mask >> lane & 1 ? a.cache_scale[row] : 0.f;
     };
     // fp8 rows: widened on their way into the tile
     auto stage_store = [&](int buf) {
@@ -268,15 +283,20 @@ latent_attention_kernel(LatentArgs a, Plan p) {
     int t = seek(t0);
     int buf = 0;
     if (t < t1) {
-        stage(0);
+#pragma unroll
+        for (int i = 0; i < KD; ++i) stage(0, i);
+        if constexpr (FP8) kscale = mask >> lane & 1 ? a.cache_scale[row] : 0.f;
         stage_store(0);
     }
     while (t < t1) {
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the tile
         lds_barrier();
         const uint32_t live4 = (uint32_t)(mask >> (kb + 4 * g)) & 15u;
-        const int t_next = t + 1 < t1 ? advance(t) : t1;
-        if (t_next < t1) stage(buf ^ 1);
+        // the next tile; behind the last one, zeros that nobody reads
+        int t_next = t1;
+        if (t + 1 < t1) t_next = advance(t);
+        if (t_next >= t1) resolve(-1, -1);
+        if constexpr (FP8) kscale = mask >> lane & 1 ? a.cache_scale[row] : 0.f;
 
         const unsigned char* tile = smem + buf * kTileB;
         // ---- scores: S^T, keys 4g .. 4g+3 of this wave's 16, row n of each block ----
@@ -285,15 +305,22 @@ latent_attention_kernel(LatentArgs a, Plan p) {
         for (int mt = 0; mt < MT; ++mt) S[mt] = v4f{0.f, 0.f, 0.f, 0.f};
         {
             const unsigned char* kp = tile + (kb + n) * kRowB + 16 * g;
+            auto read_k = [&](int ks) {
+                return *reinterpret_cast<const v8bf*>(
+                    ks < 16 ? kp + 64 * ks
+                            : tile + kMainB + (kb + n) * 128 + 16 * ((4 * (ks - 16) + g) ^ ((n >> 1) & 7)));
+            };
+            v8bf K[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) K[i] = read_k(i);
 #pragma unroll
             for (int ks = 0; ks < KD; ++ks) {
-                const unsigned char* at =
-                    ks < 16 ? kp + 64 * ks
-                            : tile + kMainB + (kb + n) * 128 + 16 * ((4 * (ks - 16) + g) ^ ((n >> 1) & 7));
-                const v8bf K = *reinterpret_cast<const v8bf*>(at);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                    S[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(K, Q[mt][ks], S[mt], 0, 0, 0);
+                    S[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(K[ks % kAhead], Q[mt][ks], S[mt], 0, 0, 0);
+                if (ks + kAhead < KD) K[ks % kAhead] = read_k(ks + kAhead);
+                stage(buf ^ 1, ks);
             }
         }
         // ---- softmax against the common reference ----
@@ -327,11 +354,11 @@ latent_attention_kernel(LatentArgs a, Plan p) {
                     sum[mt] += pr[i];
                     if (FP8) pr[i] *= ks4[i];
                 }
-                // P[row][key], 128 bytes a row; 16-byte piece 4(w/2) + g holds the keys 4g .. 4g+3
-                // of waves 2(w/2) and 2(w/2) + 1; pieces permuted by the row
+                // P[row][key]: 16-byte piece 4(w/2) + g holds the keys 4g .. 4g+3 of waves
+                // 2(w/2) and 2(w/2) + 1
                 const v2bf lo = v2bf{(__bf16)pr[0], (__bf16)pr[1]}, hi = v2bf{(__bf16)pr[2], (__bf16)pr[3]};
-                *reinterpret_cast<uint2*>(smem + kPOff + (16 * mt + n) * 128 +
-                                          16 * ((4 * (wave >> 1) + g) ^ ((n >> 1) & 7)) + 8 * (wave & 1)) =
+                *reinterpret_cast<uint2*>(smem + kPOff + (16 * mt + n) * kPRowB + 16 * (4 * (wave >> 1) + g) +
+                                          8 * (wave & 1)) =
                     uint2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
             }
         };
@@ -372,28 +399,34 @@ latent_attention_kernel(LatentArgs a, Plan p) {
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
-                P[mt][kk] = *reinterpret_cast<const v8bf*>(smem + kPOff + (16 * mt + n) * 128 +
-                                                           16 * ((4 * kk + g) ^ ((n >> 1) & 7)));
+                P[mt][kk] = *reinterpret_cast<const v8bf*>(smem + kPOff + (16 * mt + n) * kPRowB +
+                                                           16 * (4 * kk + g));
         const unsigned char* vp = tile + (4 * g + (n >> 2)) * kRowB + 8 * (n & 3) + 256 * wave;
+        // columns 16ct .. 16ct+15 of keys 4g .. 4g+3 of two 16-key groups; step i: ct = i / 2, kk = i % 2
+        auto read_v = [&](int i) {
+            const unsigned char* at = vp + 32 * (i >> 1) + 32 * (i & 1) * kRowB;
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
+            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 16 * kRowB));
+            return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        v8bf W[kAhead];
 #pragma unroll
-        for (int ct = 0; ct < 8; ++ct)
+        for (int i = 0; i < kAhead; ++i) W[i] = read_v(i);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                // columns 16ct .. 16ct+15 of keys 4g .. 4g+3 of two 16-key groups
-                const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vp + 32 * ct + 32 * kk * kRowB));
-                const v4s hi =
-                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vp + 32 * ct + (32 * kk + 16) * kRowB));
-                const v8bf W = __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        for (int i = 0; i < 16; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    O[ct][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(W, P[mt][kk], O[ct][mt], 0, 0, 0);
-            }
-        if (t_next < t1) stage_store(buf ^ 1);
+            for (int mt = 0; mt < MT; ++mt)
+                O[i >> 1][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(W[i % kAhead], P[mt][i & 1], O[i >> 1][mt], 0, 0, 0);
+            if (i + kAhead < 16) W[i % kAhead] = read_v(i + kAhead);
+        }
+        stage_store(buf ^ 1);
         t = t_next;
         buf ^= 1;
     }
 
     // ---- join the waves' sums, write ----
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // no copy may still be in flight
     lds_barrier();
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
