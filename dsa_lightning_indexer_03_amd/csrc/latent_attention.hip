@@ -91,11 +91,13 @@ __device__ __forceinline__ void lds_barrier() {
 // 16 bytes per lane from base + off (off per lane) straight to LDS byte
 // address lds + 16 * lane.  Written as asm so that later LDS reads of the
 // other tile do not wait for it; it has no register result, and the kernel
-// waits for vmcnt itself before the tile is read.  The copy may follow the
-// lane read that made its scalar base: five wait states, one for M0.
+// waits for vmcnt itself before the tile is read.  The base often comes from a
+// lane read: the scalar move in between makes it safe to address with at once,
+// and is the wait state that M0 needs.
 __device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
-                 ::"s"(lds), "v"(off), "s"(base) : "memory");
+    uint64_t b;
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+                 : "=&s"(b) : "s"(lds), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void copy_to_lds(const void* p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
@@ -158,19 +160,27 @@ latent_attention_kernel(LatentArgs a, Plan p) {
         }
     }
 
-    // ---- queries: B operand of 16 rows x 32 columns, in registers ----
-    v8bf Q[MT][KD];
+    // ---- queries: copied to the second tile's place in a tile's layout ----
+    const int kb = 16 * wave;   // this wave's rows of a tile
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
+    {
+        const uint16_t* q = a.q + (int64_t)r0 * E;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const uint16_t* qp = a.q + (int64_t)(r0 + min(16 * mt + n, nrows - 1)) * E + 8 * g;
+        for (int i = 0; i < 4 * MT; ++i) {
+            const int r = 4 * MT * wave + i;
+            copy_to_lds(q + (int64_t)min(r, nrows - 1) * E, 16 * lane, lds0 + kTileB + r * kRowB);
+        }
+        if constexpr (KD > 16)
 #pragma unroll
-        for (int ks = 0; ks < KD; ++ks) Q[mt][ks] = *reinterpret_cast<const v8bf*>(qp + 32 * ks);
+            for (int j = 0; j < (MT + 1) / 2; ++j) {
+                const int r8 = 8 * (wave + 4 * j);
+                if (r8 < 16 * MT) {
+                    const int r = r8 + (lane >> 3);
+                    copy_to_lds(q + (int64_t)min(r, nrows - 1) * E + kV + 8 * ((lane & 7) ^ ((r >> 1) & 7)),
+                                lds0 + kTileB + kMainB + r8 * 128);
+                }
+            }
     }
-    // 64 rows' queries fill most of the accumulation registers, which an
-    // operand may be read from as well
-    if constexpr (MT == 4)
-#pragma unroll
-        for (int i = 0; i < MT * KD && i < 60; ++i) asm volatile("" : "+a"(Q[i / KD][i % KD]));
     v4f O[8][MT];
     float m[MT], l[MT];
 #pragma unroll
@@ -184,8 +194,6 @@ latent_attention_kernel(LatentArgs a, Plan p) {
     float* red = reinterpret_cast<float*>(smem + red_off(MT));
     if (threadIdx.x < 2) flag[threadIdx.x] = 0;
 
-    const int kb = 16 * wave;   // this wave's rows of a tile
-
     // ---- the rows of a tile: lane i holds entry i's row of the pool ----
     auto entry = [&](int t) -> int {   // position (topk) of entry `lane`, -1: none
         const int j = t * kTile + lane;
@@ -195,63 +203,60 @@ latent_attention_kernel(LatentArgs a, Plan p) {
     auto page_of = [&](int s) -> int {
         return s >= 0 && s / kPage < a.max_pages ? table[s / kPage] : -1;
     };
+    int zero;   // keeps the loads of page ids among the vector loads
+    asm volatile("v_mov_b32 %0, 0" : "=v"(zero));
     auto page_of_tile = [&](int s, int t) -> int {
         if constexpr (TOPK) return page_of(s);
-        return t < t1 ? table[t] : -1;
+        return t < t1 ? table[t + zero] : -1;
     };
     auto live = [&](int s, int page) { return s >= 0 && page >= 0 && page < a.num_pages; };
 
-    // The rows of tiles t+1, t+2, t+3 are found while tile t is computed: the
-    // entries (three tiles ahead) and their page ids (two ahead) are loads in
-    // flight, and the next tile's rows are copied from its ids.
-    // An entry without a row takes a row of zeros: its probability is zero,
-    // and zero its values must be.
-    int row = 0;                      // the tile to copy: rows,
+    // While a tile is computed the next one is copied, the addresses of the one
+    // behind it are made, and page ids and entries of the next two are loads in
+    // flight.  An entry without a row takes a row of zeros: its probability is
+    // zero, and zero its values must be.
+    int row = 0;                      // the next tile: rows,
     uint64_t mask = 0;                // which entries have one,
     uint64_t src = 0;                 // their addresses,
     uint64_t rope_src[2] = {0, 0};    // and this lane's pieces of the rotary columns
-    int s1, page1, s2;    // entries and page ids of the next tile, entries of the one behind it
+    int s2, page2, s3;                // entries and page ids of the tile behind it, entries of the next
+    auto address = [&](int r) {
+        return r >= 0 ? (uint64_t)a.cache + (uint64_t)(uint32_t)r * RB : (uint64_t)kZeroRow;
+    };
     auto resolve = [&](int s, int page) {
         const bool ok = live(s, page);
         mask = wave_ballot(ok);
-        row = ok ? page * kPage + (s & (kPage - 1)) : 0;
-        src = ok ? (uint64_t)a.cache + (uint64_t)(uint32_t)row * RB : (uint64_t)kZeroRow;
+        row = ok ? page * kPage + (s & (kPage - 1)) : -1;
+        src = address(row);
         if constexpr (KD > 16)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int r = kb + 8 * j + (lane >> 3);
-                const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)src, r);
-                const uint32_t hi = (uint32_t)__shfl((int)(uint32_t)(src >> 32), r);
-                rope_src[j] = ((uint64_t)hi << 32 | lo) + (RB / E) * (kV + 8 * ((lane & 7) ^ ((r >> 1) & 7)));
+                rope_src[j] = address(__shfl(row, r)) + (RB / E) * (kV + 8 * ((lane & 7) ^ ((r >> 1) & 7)));
             }
     };
-    // first tile at or behind t with an entry, and the state from there
+    // First tile at or behind t with an entry, resolved, and the loads behind it.
     auto seek = [&](int t) -> int {
         for (; t < t1; ++t) {
             const int s = entry(t);
             resolve(s, page_of_tile(s, t));
             if (mask) break;
         }
-        s1 = entry(t + 1);
-        s2 = entry(t + 2);
-        page1 = page_of_tile(s1, t + 1);
+        if (t >= t1) {
+            resolve(-1, -1);
+            return t1;
+        }
+        s2 = entry(t + 1);
+        s3 = entry(t + 2);
+        page2 = page_of_tile(s2, t + 1);
         return t;
-    };
-    auto advance = [&](int t) -> int {
-        resolve(s1, page1);
-        if (mask == 0) return seek(t + 2);
-        s1 = s2;
-        page1 = page_of_tile(s2, t + 2);
-        s2 = entry(t + 3);
-        return t + 1;
     };
 
     uint2 main8[FP8 ? 16 : 1], rope8[FP8 ? 2 : 1];
     float kscale = 0.f;
     // Part i of a tile's copy: row kb + i, then (i = 16, 17) 8 rows' rotary columns.
     auto stage = [&](int buf, int i) {
-        const uint32_t lds =
-            (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)(smem + buf * kTileB);
+        const uint32_t lds = lds0 + buf * kTileB;
         if (i < 16) {
             const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)src, kb + i);
             const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(src >> 32), kb + i);
@@ -281,22 +286,67 @@ latent_attention_kernel(LatentArgs a, Plan p) {
     };
 
     int t = seek(t0);
-    int buf = 0;
-    if (t < t1) {
+    uint64_t here = mask;   // the entries of the tile that is computed
+    auto stage_scale = [&]() {
+        if constexpr (FP8) kscale = row >= 0 ? a.cache_scale[row] : 0.f;
+    };
 #pragma unroll
-        for (int i = 0; i < KD; ++i) stage(0, i);
-        if constexpr (FP8) kscale = mask >> lane & 1 ? a.cache_scale[row] : 0.f;
-        stage_store(0);
+    for (int i = 0; i < KD; ++i) stage(0, i);
+    stage_scale();
+    stage_store(0);
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    lds_barrier();
+    // B operand of 16 rows x 32 columns: row n, columns 8g .. 8g+7 of each 32
+    v8bf Q[MT][KD];
+    auto operand = [&](const unsigned char* tile, int r, int ks) {   // row r: r % 16 == n
+        return *reinterpret_cast<const v8bf*>(
+            tile + (ks < 16 ? r * kRowB + 16 * g + 64 * ks
+                            : kMainB + r * 128 + 16 * ((4 * (ks - 16) + g) ^ ((n >> 1) & 7))));
+    };
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks) {
+            v8bf q = operand(smem + kTileB, 16 * mt + n, ks);
+            if (a.scale_log2 < 0.f) {   // the products then take the scale's magnitude
+                v4i u = __builtin_bit_cast(v4i, q);
+                u ^= (int)0x80008000;
+                q = __builtin_bit_cast(v8bf, u);
+            }
+            Q[mt][ks] = q;
+        }
+    // 64 rows' queries fill most of the accumulation registers, which an
+    // operand may be read from as well
+    if constexpr (MT == 4)
+#pragma unroll
+        for (int i = 0; i < MT * KD && i < 60; ++i) asm volatile("" : "+a"(Q[i / KD][i % KD]));
+    // (never 0: a score of -inf, an entry without a row, has to stay one)
+    const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
+
+    int t_next = t1, buf = 0;
+    if (t < t1) {
+        if (t + 1 < t1) {
+            resolve(s2, page2);
+            if (mask == 0) {
+                t_next = seek(t + 2);
+            } else {
+                t_next = t + 1;
+                s2 = s3;
+                page2 = page_of_tile(s2, t + 2);
+                s3 = entry(t + 3);
+            }
+        } else {
+            resolve(-1, -1);
+        }
     }
     while (t < t1) {
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the tile
         lds_barrier();
-        const uint32_t live4 = (uint32_t)(mask >> (kb + 4 * g)) & 15u;
-        // the next tile; behind the last one, zeros that nobody reads
-        int t_next = t1;
-        if (t + 1 < t1) t_next = advance(t);
-        if (t_next >= t1) resolve(-1, -1);
-        if constexpr (FP8) kscale = mask >> lane & 1 ? a.cache_scale[row] : 0.f;
+        const uint32_t live4 = (uint32_t)(here >> (kb + 4 * g)) & 15u;
+        // loads for the tiles behind the next one
+        const int page3 = page_of_tile(s3, t_next + 2);
+        const int s4 = entry(t_next + 3);
+        stage_scale();
 
         const unsigned char* tile = smem + buf * kTileB;
         // ---- scores: S^T, keys 4g .. 4g+3 of this wave's 16, row n of each block ----
@@ -304,24 +354,19 @@ latent_attention_kernel(LatentArgs a, Plan p) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) S[mt] = v4f{0.f, 0.f, 0.f, 0.f};
         {
-            const unsigned char* kp = tile + (kb + n) * kRowB + 16 * g;
-            auto read_k = [&](int ks) {
-                return *reinterpret_cast<const v8bf*>(
-                    ks < 16 ? kp + 64 * ks
-                            : tile + kMainB + (kb + n) * 128 + 16 * ((4 * (ks - 16) + g) ^ ((n >> 1) & 7)));
-            };
             v8bf K[kAhead];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) K[i] = read_k(i);
+            for (int i = 0; i < kAhead; ++i) K[i] = operand(tile, kb + n, i);
 #pragma unroll
             for (int ks = 0; ks < KD; ++ks) {
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
                     S[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(K[ks % kAhead], Q[mt][ks], S[mt], 0, 0, 0);
-                if (ks + kAhead < KD) K[ks % kAhead] = read_k(ks + kAhead);
-                stage(buf ^ 1, ks);
+                if (ks + kAhead < KD) K[ks % kAhead] = operand(tile, kb + n, ks + kAhead);
+                stage(buf ^ 1, ks);   // behind the last tile: zeros that nobody reads
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         // ---- softmax against the common reference ----
         float ks4[4] = {1.f, 1.f, 1.f, 1.f};
@@ -329,17 +374,21 @@ latent_attention_kernel(LatentArgs a, Plan p) {
             const v4f s4 = *reinterpret_cast<const v4f*>(smem + scale_off(MT) + 256 * buf + 4 * (kb + 4 * g));
 #pragma unroll
             for (int i = 0; i < 4; ++i) ks4[i] = s4[i];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[mt][i] *= ks4[i];
         }
+        if (here != ~0ull)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[mt][i] = live4 >> i & 1 ? S[mt][i] : -__builtin_inff();
         float top[MT], sum[MT];
         bool rise = false;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = S[mt][i] * (FP8 ? ks4[i] * a.scale_log2 : a.scale_log2);
-                S[mt][i] = live4 >> i & 1 ? x : -__builtin_inff();
-            }
-            top[mt] = fmaxf(fmaxf(S[mt][0], S[mt][1]), fmaxf(S[mt][2], S[mt][3]));
+            top[mt] = scale * fmaxf(fmaxf(S[mt][0], S[mt][1]), fmaxf(S[mt][2], S[mt][3]));
             rise |= top[mt] > m[mt] + kSlack;
         }
         auto write_p = [&]() {
@@ -350,7 +399,7 @@ latent_attention_kernel(LatentArgs a, Plan p) {
                 sum[mt] = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    pr[i] = __builtin_amdgcn_exp2f(S[mt][i] - ref);
+                    pr[i] = __builtin_amdgcn_exp2f(fmaf(S[mt][i], scale, -ref));
                     sum[mt] += pr[i];
                     if (FP8) pr[i] *= ks4[i];
                 }
@@ -365,8 +414,29 @@ latent_attention_kernel(LatentArgs a, Plan p) {
         write_p();
         if (wave_ballot(rise) && lane == 0) flag[buf] = 1;
         if (threadIdx.x == 0) flag[buf ^ 1] = 0;
+        // the values: columns 16ct .. 16ct+15 of keys 4g .. 4g+3 of two 16-key groups; step i: ct = i / 2, kk = i % 2
+        const unsigned char* vp = tile + (4 * g + (n >> 2)) * kRowB + 8 * (n & 3) + 256 * wave;
+        auto read_v = [&](int i) {
+            const unsigned char* at = vp + 32 * (i >> 1) + 32 * (i & 1) * kRowB;
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
+            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 16 * kRowB));
+            return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        v8bf P[MT][2], W[kAhead];
+        auto read_p = [&]() {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+                    P[mt][kk] = *reinterpret_cast<const v8bf*>(smem + kPOff + (16 * mt + n) * kPRowB +
+                                                               16 * (4 * kk + g));
+        };
         lds_barrier();
-        if (uniform(flag[buf])) {
+        const int risen = flag[buf];
+        read_p();
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) W[i] = read_v(i);
+        if (uniform(risen)) {
             // the reference moves to the tile's maximum where that is above it
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -389,29 +459,14 @@ latent_attention_kernel(LatentArgs a, Plan p) {
             }
             write_p();
             lds_barrier();
+            read_p();
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) l[mt] += sum[mt];
 
-        // ---- O^T += V^T P^T ----
-        v8bf P[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-                P[mt][kk] = *reinterpret_cast<const v8bf*>(smem + kPOff + (16 * mt + n) * kPRowB +
-                                                           16 * (4 * kk + g));
-        const unsigned char* vp = tile + (4 * g + (n >> 2)) * kRowB + 8 * (n & 3) + 256 * wave;
-        // columns 16ct .. 16ct+15 of keys 4g .. 4g+3 of two 16-key groups; step i: ct = i / 2, kk = i % 2
-        auto read_v = [&](int i) {
-            const unsigned char* at = vp + 32 * (i >> 1) + 32 * (i & 1) * kRowB;
-            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
-            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 16 * kRowB));
-            return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        };
-        v8bf W[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) W[i] = read_v(i);
+        // ---- O^T += V^T P^T; beside it, the addresses of the tile behind the next one ----
+        const int t_now = t_next;
+        here = mask;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             __builtin_amdgcn_sched_barrier(0);
@@ -419,10 +474,20 @@ latent_attention_kernel(LatentArgs a, Plan p) {
             for (int mt = 0; mt < MT; ++mt)
                 O[i >> 1][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(W[i % kAhead], P[mt][i & 1], O[i >> 1][mt], 0, 0, 0);
             if (i + kAhead < 16) W[i % kAhead] = read_v(i + kAhead);
+            if (i == 2) {
+                if (t_now + 1 >= t1) s2 = -1;
+                resolve(s2, page2);
+            }
         }
+        __builtin_amdgcn_sched_barrier(0);
         stage_store(buf ^ 1);
-        t = t_next;
         buf ^= 1;
+        t = t_now;
+        t_next = t_now + 1;
+        s2 = s3;
+        page2 = page3;
+        s3 = s4;
+        if (mask == 0 && t_next < t1) t_next = seek(t_next + 1);
     }
 
     // ---- join the waves' sums, write ----
@@ -465,41 +530,62 @@ latent_attention_kernel(LatentArgs a, Plan p) {
     }
 }
 
-// Joins the slots' partial results of a row: one wave per row, 8 columns a lane.
+// Joins the slots' partial results of a row: one workgroup per row, a wave
+// takes every fourth slot (8 columns a lane), the waves' sums meet in LDS.
+// Slots are at most 64, one per lane for the weights.  Bound by reading the
+// partial sums; with few rows by latency, so a wave has four slots in flight.
 __global__ void __launch_bounds__(kThreads)
 latent_join_kernel(LatentArgs a, Plan p) {
-    const int lane = threadIdx.x & 63;
+    __shared__ float sums[4][kV];
+    const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int total = a.T * a.H;
-    const int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 6;
-    if (r >= total) return;
-    float top = -__builtin_inff();
-    for (int s = 0; s < p.slots; ++s) {
-        const float2 ml = p.part_ml[(int64_t)s * total + r];
-        if (ml.y != 0.f) top = fmaxf(top, ml.x);
-    }
-    float l = 0.f, o[8];
+    const int64_t r = blockIdx.x;
+    const float2 ml = lane < p.slots ? p.part_ml[(int64_t)lane * total + r] : float2{0.f, 0.f};
+    const bool some = ml.y != 0.f;
+    float top = some ? ml.x : -__builtin_inff();
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
+    const float w = some ? __builtin_amdgcn_exp2f(ml.x - top) : 0.f;
+    float l = w * ml.y;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) l += __shfl_xor(l, d, kWave);
+    const uint64_t filled = wave_ballot(some);
+    const int any = filled ? __builtin_ctzll(filled) : 0;
+    float o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = 0.f;
-    for (int s = 0; s < p.slots; ++s) {
-        const int64_t at = (int64_t)s * total + r;
-        const float2 ml = p.part_ml[at];
-        if (ml.y == 0.f) continue;
-        const float w = __builtin_amdgcn_exp2f(ml.x - top);
-        l += w * ml.y;
-        const v4f x = *reinterpret_cast<const v4f*>(p.part_o + at * kV + 8 * lane);
-        const v4f y = *reinterpret_cast<const v4f*>(p.part_o + at * kV + 8 * lane + 4);
+    if (filled)
+        for (int s0 = wave; s0 < p.slots; s0 += 16) {
+            v4f x[4], y[4];
+            float f[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            o[j] += w * x[j];
-            o[4 + j] += w * y[j];
+            for (int u = 0; u < 4; ++u) {   // a slot that holds nothing was not written: another's place, weight 0
+                const int s = s0 + 4 * u < p.slots ? s0 + 4 * u : any;
+                const bool ok = s0 + 4 * u < p.slots && filled >> s & 1;
+                f[u] = ok ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), s)) : 0.f;
+                const float* at = p.part_o + ((int64_t)(ok ? s : any) * total + r) * kV + 8 * lane;
+                x[u] = *reinterpret_cast<const v4f*>(at);
+                y[u] = *reinterpret_cast<const v4f*>(at + 4);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    o[j] += f[u] * x[u][j];
+                    o[4 + j] += f[u] * y[u][j];
+                }
         }
-    }
+    *reinterpret_cast<v4f*>(&sums[wave][8 * lane]) = v4f{o[0], o[1], o[2], o[3]};
+    *reinterpret_cast<v4f*>(&sums[wave][8 * lane + 4]) = v4f{o[4], o[5], o[6], o[7]};
+    __syncthreads();
     const float inv = l != 0.f ? 1.f / l : 0.f;
-    v8bf y;
+    const int c = 2 * threadIdx.x;
+    v2bf out;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = (__bf16)(o[j] * inv);
-    *reinterpret_cast<v8bf*>(a.out + r * kV + 8 * lane) = y;
-    if (a.lse && lane == 0) a.lse[r] = l != 0.f ? (top + log2f(l)) * 0.693147180559945f : -__builtin_inff();
+    for (int j = 0; j < 2; ++j)
+        out[j] = (__bf16)(((sums[0][c + j] + sums[1][c + j]) + (sums[2][c + j] + sums[3][c + j])) * inv);
+    *reinterpret_cast<v2bf*>(a.out + r * kV + c) = out;
+    if (a.lse && threadIdx.x == 0) a.lse[r] = l != 0.f ? (top + log2f(l)) * 0.693147180559945f : -__builtin_inff();
 }
 
 constexpr int kCUs = 256;
@@ -510,26 +596,42 @@ int pad8(int n) { return (n + 7) / 8 * 8; }
 // which leaves room for 32.
 int blocks_of_16(int64_t rows, bool fp8) { return rows <= 16 ? 1 : rows <= 32 || fp8 ? 2 : 4; }
 
-// Tiles per workgroup that finish first: a workgroup costs its tiles and a
-// fixed part (queries, first tile, results) of about three tiles, the GPU runs
-// one per CU at a time, and joining costs about a tile per 16 slots.
-void split(int64_t rows_p, int tiles_p, int64_t rows_o, int tiles_o, Plan& p) {
+// Splits that finish first, in us: a workgroup takes 5 and 1.4 a tile, the GPU
+// runs one per CU, prefix parts first; joining takes 4 and reads and writes
+// every slot's sums.  A run of own tiles is as long as one of the prefix.
+void split(int tiles_p, int64_t blocks_o, int tiles_o, int64_t rows, Plan& p) {
+    static const int kSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32};
+    const int tiles = tiles_p > 0 ? tiles_p : tiles_o;
     double best = 1e30;
-    const int most = tiles_p > tiles_o ? tiles_p : tiles_o;
-    for (int len = 1;; len = len < 16 ? len + 1 : len + len / 8) {
-        if (len > most) len = most;
-        const int sp = ceil_div(tiles_p, len), so = ceil_div(tiles_o, len);
-        if (sp + so <= 64 || len == most) {
-            const int64_t n = rows_p * sp + rows_o * so;
-            const double cost = (double)ceil_div(n, kCUs) * (len + 3) + (sp + so > 1 ? 2 + (sp + so) / 16.0 : 0);
-            if (cost < best) {
-                best = cost;
-                p.sp = sp;
-                p.so = so;
-                p.lp = p.lo = len;
-            }
+    for (int n : kSplits) {
+        if (n > tiles) break;
+        const int len = ceil_div(tiles, n);
+        const int sp = tiles_p > 0 ? ceil_div(tiles_p, len) : 0;
+        int lo = tiles_p > 0 ? (len < tiles_o ? len : tiles_o) : len;
+        if (lo < ceil_div(tiles_o, 32)) lo = ceil_div(tiles_o, 32);
+        const int so = tiles_o > 0 ? ceil_div(tiles_o, lo) : 0;
+        const int64_t np = tiles_p > 0 ? (int64_t)p.rb * sp : 0, no = blocks_o * so;
+        const double cp = 5 + 1.4 * len, co = 5 + 1.4 * lo;
+        // whole rounds of prefix parts; the rest of them beside the own parts
+        const int64_t rest = np % kCUs;
+        int64_t k = no / kCUs;   // own parts one after another on a CU
+        auto room = [&](int64_t k) {
+            const int64_t behind = k * co > cp ? (int64_t)((k * co - cp) / co) : 0;
+            return (kCUs - rest) * k + rest * behind;
+        };
+        while (room(k) < no) ++k;
+        double us = k * co;
+        if (rest > 0 && us < cp) us = cp;
+        us += (double)(np / kCUs) * cp;
+        const int slots = sp + so;
+        if (slots > 1) us += 4 + 1e-3 * (double)rows * slots;
+        if (us < best) {
+            best = us;
+            p.sp = sp;
+            p.so = so;
+            p.lp = len;
+            p.lo = lo;
         }
-        if (len >= most) break;
     }
 }
 
@@ -541,7 +643,7 @@ Plan make_plan(int T, int H, bool topk, int K, int prefix_len, int max_ctx, bool
     *mt = blocks_of_16(tiles_p > 0 ? (int64_t)T * H : H, fp8);
     p.rb = ceil_div((int64_t)T * H, 16 * *mt);
     p.hb = ceil_div(H, 16 * *mt);
-    split(tiles_p ? p.rb : 0, tiles_p, tiles_o ? (int64_t)T * p.hb : 0, tiles_o, p);
+    split(tiles_p, tiles_o ? (int64_t)T * p.hb : 0, tiles_o, (int64_t)T * H, p);
     p.n_prefix = pad8(p.rb * p.sp);
     p.n_own = pad8(T * p.hb * p.so);
     p.slots = p.sp + p.so;
@@ -599,8 +701,7 @@ hipError_t launch_latent_attention(const LatentArgs& a, bool fp8, hipStream_t st
     p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)p.slots * a.T * a.H * kV);
     hipError_t e = a.E == 576 ? run<18>(a, p, mt, fp8, stream) : run<16>(a, p, mt, fp8, stream);
     if (e != hipSuccess || p.slots == 1) return e;
-    const int64_t blocks = ((int64_t)a.T * a.H * 64 + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a, p);
+    hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)(a.T * a.H)), dim3(kThreads), 0, stream, a, p);
     return hipGetLastError();
 }
 
