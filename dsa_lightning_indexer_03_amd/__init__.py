@@ -68,6 +68,10 @@ def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+# the same handle without the Python stream object (1.8 us a call) where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
+
+
 def _workspace(nbytes: int, device) -> torch.Tensor | None:
     if nbytes == 0:
         return None
@@ -408,9 +412,15 @@ def prefill_chunk_paged(q, q_scale, w, k_cache, k_scale, block_table, q0: int, t
     return idx.view(B, Lq, topk), None if val is None else val.view(B, Lq, topk)
 
 
-def _same_device(dev, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
+def _all(dev, *checks) -> None:
+    """(name, tensor or None, element types): each tensor of one of its types,
+    contiguous, on `dev`, a GPU."""
+    for name, t, dtypes in checks:
+        if t is not None and t.dtype not in dtypes:
+            _need(t, name, *dtypes)
+    for name, t, _ in checks:
+        if t is not None and (t.device != dev or not t.is_contiguous() or dev.type != "cuda"):
+            _dev(t, name)
             raise ValueError(f"{name} must be on {dev}, the device of the other tensors")
 
 
@@ -424,10 +434,25 @@ def _rows(t, name: str) -> int:
 
 
 def _inference_only(where: str, *tensors) -> None:
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError(f"{where} has no backward: call it under torch.no_grad() or detach its inputs")
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{where} has no backward: call it under torch.no_grad() or detach its inputs")
+
+
+def _on_device(dev, fn, *args):
+    """fn(*args, stream) with `dev` current, on its current stream."""
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        return fn(*args, _raw_stream(index))
+    with torch.cuda.device(index):
+        return fn(*args, _raw_stream(index))
+
+
+_BF16 = (torch.bfloat16,)
+_NEW = (torch.bfloat16, torch.float32)
+_LATENT = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
+_FLOATS = (torch.float32,)
+_INTS = (torch.int32,)
 
 
 def cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin, latent_scale=None,
@@ -447,24 +472,22 @@ def cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin
     i is columns (2i, 2i+1), else (i, i + R/2).  Returns nothing."""
     lib = _lib.load()
     dev = kv.device
+    if kv.dtype not in _NEW:
+        _need(kv, "kv", *_NEW)
     kv_stride = _rows(kv, "kv")
     T, E = kv.shape
-    _need(kv, "kv", torch.bfloat16, _F32)
-    _need(latent_cache, "latent_cache", torch.bfloat16, *_CODES)
-    _need(latent_scale, "latent_scale", _F32)
-    _need(cos_sin, "cos_sin", _F32)
-    _need(seq_ids, "seq_ids", _I32)
-    _need(positions, "positions", _I32)
-    _need(block_table, "block_table", _I32)
+    _all(dev, ("latent_cache", latent_cache, _LATENT), ("latent_scale", latent_scale, _FLOATS),
+         ("cos_sin", cos_sin, _FLOATS), ("seq_ids", seq_ids, _INTS), ("positions", positions, _INTS),
+         ("block_table", block_table, _INTS), ("k_cache", k_cache, _CODES), ("k_scale", k_scale, _FLOATS))
     if latent_cache.dim() != 3 or latent_cache.shape[2] != E:
         raise ValueError("latent_cache must be [P, page, E] with the E of kv")
-    P, page = latent_cache.shape[:2]
+    P, page, _ = latent_cache.shape
     fp8 = latent_cache.dtype != torch.bfloat16
-    if fp8 != (latent_scale is not None) or (fp8 and tuple(latent_scale.shape) != (P, page)):
+    if fp8 != (latent_scale is not None) or (fp8 and latent_scale.shape != (P, page)):
         raise ValueError("latent_scale [P, page] goes with fp8 latent rows, None with bf16 rows")
     if cos_sin.dim() != 2 or block_table.dim() != 2:
         raise ValueError("cos_sin must be [rope_len, R] and block_table [B, max_pages]")
-    if tuple(seq_ids.shape) != (T,) or tuple(positions.shape) != (T,):
+    if seq_ids.shape != (T,) or positions.shape != (T,):
         raise ValueError("seq_ids / positions must have one entry per token")
     index_stride, D = 0, 128
     if (index_k is None) != (k_cache is None) or (index_k is None) != (k_scale is None):
@@ -472,52 +495,49 @@ def cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin
     if index_k is not None:
         index_stride = _rows(index_k, "index_k")
         D = index_k.shape[1]
-        if index_k.dtype != kv.dtype or index_k.shape[0] != T:
-            raise ValueError("index_k must be [T, D] of kv's type")
-        _need(k_cache, "k_cache", *_CODES)
-        _need(k_scale, "k_scale", _F32)
-        if tuple(k_cache.shape) != (P, page, D) or tuple(k_scale.shape) != (P, page):
+        if index_k.dtype != kv.dtype or index_k.shape[0] != T or index_k.device != dev:
+            raise ValueError("index_k must be [T, D] of kv's type, on its device")
+        if k_cache.shape != (P, page, D) or k_scale.shape != (P, page):
             raise ValueError("k_cache [P, page, D] / k_scale [P, page] shape mismatch")
-    for name, t in (("seq_ids", seq_ids), ("positions", positions), ("block_table", block_table),
-                    ("latent_cache", latent_cache), ("cos_sin", cos_sin), ("latent_scale", latent_scale),
-                    ("k_cache", k_cache), ("k_scale", k_scale)):
-        if t is not None:
-            _dev(t, name)
-    _same_device(dev, seq_ids=seq_ids, positions=positions, block_table=block_table, latent_cache=latent_cache,
-                 cos_sin=cos_sin, latent_scale=latent_scale, index_k=index_k, k_cache=k_cache, k_scale=k_scale)
     _inference_only("cache_append_rope", kv, index_k)
-    with torch.cuda.device(dev):
-        st = lib.indexer_cache_append_rope(_ptr(kv), kv_stride, int(kv_interleaved), _ptr(index_k), index_stride,
-                                           int(index_interleaved), dtype_code(kv), _ptr(cos_sin), cos_sin.shape[0],
-                                           cos_sin.shape[1], _ptr(seq_ids), _ptr(positions), _ptr(block_table),
-                                           block_table.shape[0], block_table.shape[1], _ptr(latent_cache),
-                                           _ptr(latent_scale), FP8_E4M3 if fp8 else BF16, _ptr(k_cache),
-                                           _ptr(k_scale), P, T, E, D, page, _stream(dev))
-    _lib.check(st, "indexer_cache_append_rope")
+    B, max_pages = block_table.shape
+    rope_len, R = cos_sin.shape
+    st = _on_device(dev, lib.indexer_cache_append_rope, kv.data_ptr(), kv_stride, 1 if kv_interleaved else 0,
+                    _ptr(index_k), index_stride, 1 if index_interleaved else 0,
+                    BF16 if kv.dtype == torch.bfloat16 else F32, cos_sin.data_ptr(), rope_len, R,
+                    seq_ids.data_ptr(), positions.data_ptr(), block_table.data_ptr(), B, max_pages,
+                    latent_cache.data_ptr(), _ptr(latent_scale), FP8_E4M3 if fp8 else BF16, _ptr(k_cache),
+                    _ptr(k_scale), P, T, E, D, page)
+    if st:
+        _lib.check(st, "indexer_cache_append_rope")
 
 
-def _latent_inputs(q, latent_cache, latent_scale, block_table, where: str, **others):
+def _latent_inputs(q, latent_cache, latent_scale, block_table, where: str, *others):
     """Checks that the latent-attention calls share; returns (P, page, dtype code of the rows)."""
-    _need(q, "q", torch.bfloat16)
-    _need(latent_cache, "latent_cache", torch.bfloat16, *_CODES)
-    _need(latent_scale, "latent_scale", _F32)
+    _all(q.device, ("q", q, _BF16), ("latent_cache", latent_cache, _LATENT), ("latent_scale", latent_scale, _FLOATS),
+         ("block_table", block_table, _INTS), *others)
     if q.dim() != 3 or latent_cache.dim() != 3 or latent_cache.shape[2] != q.shape[2]:
         raise ValueError("q must be [rows, H, E] and latent_cache [P, page, E]")
-    P, page = latent_cache.shape[:2]
+    P, page, _ = latent_cache.shape
     fp8 = latent_cache.dtype != torch.bfloat16
-    if fp8 != (latent_scale is not None) or (fp8 and tuple(latent_scale.shape) != (P, page)):
+    if fp8 != (latent_scale is not None) or (fp8 and latent_scale.shape != (P, page)):
         raise ValueError("latent_scale [P, page] goes with fp8 latent rows, None with bf16 rows")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
-    tensors = dict(q=q, latent_cache=latent_cache, latent_scale=latent_scale, block_table=block_table, **others)
-    for name, t in tensors.items():
-        if t is not None:
-            if name not in ("q", "latent_cache", "latent_scale"):
-                _need(t, name, _I32)
-            _dev(t, name)
-    _same_device(q.device, **tensors)
     _inference_only(where, q, latent_cache)
     return P, page, FP8_E4M3 if fp8 else BF16
+
+
+def _scratch(workspace, nbytes: int, dev):
+    """The caller's workspace where it is one (enough bytes, on `dev`), else a new one; None where none is needed."""
+    if nbytes == 0:
+        return None
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        if workspace.numel() * workspace.element_size() >= nbytes:
+            return workspace.data_ptr()
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
 def latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim: int, scale: float, latent_scale=None,
@@ -534,25 +554,26 @@ def latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim: int, sc
     row gives zeros and -inf."""
     lib = _lib.load()
     P, page, dt = _latent_inputs(q, latent_cache, latent_scale, block_table, "latent_attention_topk",
-                                 topk_idx=topk_idx, seq_ids=seq_ids)
+                                 ("topk_idx", topk_idx, _INTS), ("seq_ids", seq_ids, _INTS))
     T, H, E = q.shape
     if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
         raise ValueError("topk_idx must be [T, K]")
-    if seq_ids is not None and tuple(seq_ids.shape) != (T,):
+    if seq_ids is not None and seq_ids.shape != (T,):
         raise ValueError("seq_ids must have one entry per query")
-    if seq_ids is None and block_table.shape[0] != T:
+    B, max_pages = block_table.shape
+    if seq_ids is None and B != T:
         raise ValueError("block_table must have one row per query (or give seq_ids)")
     dev, K = q.device, topk_idx.shape[1]
-    out = torch.empty((T, H, v_dim), dtype=torch.bfloat16, device=dev)
+    out = q.new_empty((T, H, v_dim))
     lse = torch.empty((T, H), dtype=torch.float32, device=dev) if want_lse else None
     nws = lib.indexer_latent_attention_topk_workspace_bytes(T, H, E, v_dim, K, dt)
-    ws = workspace if workspace is not None and workspace.numel() >= nws else _workspace(nws, dev)
-    with torch.cuda.device(dev):
-        st = lib.indexer_latent_attention_topk(_ptr(q), BF16, _ptr(latent_cache), _ptr(latent_scale), dt,
-                                               _ptr(block_table), block_table.shape[1], P, _ptr(topk_idx),
-                                               _ptr(seq_ids), max(1, block_table.shape[0]), T, H, E, v_dim, page, K,
-                                               float(scale), _ptr(out), _ptr(lse), _ptr(ws), nws, _stream(dev))
-    _lib.check(st, "indexer_latent_attention_topk")
+    ws = _scratch(workspace, nws, dev)
+    st = _on_device(dev, lib.indexer_latent_attention_topk, q.data_ptr(), BF16, latent_cache.data_ptr(),
+                    _ptr(latent_scale), dt, block_table.data_ptr(), max_pages, P, topk_idx.data_ptr(), _ptr(seq_ids),
+                    B or 1, T, H, E, v_dim, page, K, scale, out.data_ptr(), _ptr(lse),
+                    ws if ws is None or type(ws) is int else ws.data_ptr(), nws)
+    if st:
+        _lib.check(st, "indexer_latent_attention_topk")
     return out, lse
 
 
@@ -571,26 +592,24 @@ def latent_attention_shared(q, latent_cache, prefix_table, prefix_len: int, bloc
     position gives zeros and -inf."""
     lib = _lib.load()
     P, page, dt = _latent_inputs(q, latent_cache, latent_scale, block_table, "latent_attention_shared",
-                                 prefix_table=prefix_table, context_lens=context_lens)
+                                 ("prefix_table", prefix_table, _INTS), ("context_lens", context_lens, _INTS))
     B, H, E = q.shape
-    if block_table.shape[0] != B or tuple(context_lens.shape) != (B,):
+    if block_table.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("block_table / context_lens shape mismatch")
     if prefix_table is not None and prefix_table.dim() != 1:
         raise ValueError("prefix_table must be one-dimensional")
-    mpp = block_table.shape[1]
-    mcl = mpp * page if max_context_len is None else int(max_context_len)
+    max_pages = block_table.shape[1]
+    mcl = max_pages * page if max_context_len is None else int(max_context_len)
     dev = q.device
-    out = torch.empty((B, H, v_dim), dtype=torch.bfloat16, device=dev)
+    out = q.new_empty((B, H, v_dim))
     lse = torch.empty((B, H), dtype=torch.float32, device=dev) if want_lse else None
-    prefix_len = int(prefix_len)
     nws = lib.indexer_latent_attention_shared_workspace_bytes(B, H, E, v_dim, prefix_len, mcl, dt)
-    ws = workspace if workspace is not None and workspace.numel() >= nws else _workspace(nws, dev)
-    with torch.cuda.device(dev):
-        st = lib.indexer_latent_attention_shared(_ptr(q), BF16, _ptr(latent_cache), _ptr(latent_scale), dt,
-                                                 _ptr(prefix_table),
-                                                 0 if prefix_table is None else prefix_table.shape[0], prefix_len,
-                                                 _ptr(block_table), mpp, P, _ptr(context_lens), mcl, B, H, E, v_dim,
-                                                 page, float(scale), _ptr(out), _ptr(lse), _ptr(ws), nws,
-                                                 _stream(dev))
-    _lib.check(st, "indexer_latent_attention_shared")
+    ws = _scratch(workspace, nws, dev)
+    st = _on_device(dev, lib.indexer_latent_attention_shared, q.data_ptr(), BF16, latent_cache.data_ptr(),
+                    _ptr(latent_scale), dt, _ptr(prefix_table), 0 if prefix_table is None else prefix_table.shape[0],
+                    prefix_len, block_table.data_ptr(), max_pages, P, context_lens.data_ptr(), mcl, B, H, E, v_dim,
+                    page, scale, out.data_ptr(), _ptr(lse),
+                    ws if ws is None or type(ws) is int else ws.data_ptr(), nws)
+    if st:
+        _lib.check(st, "indexer_latent_attention_shared")
     return out, lse

@@ -1,0 +1,292 @@
+// Attention over the paged latent cache for blocks of many query rows: 64 or
+// 128 of one query's heads, or of the batch's rows stacked against a shared
+// prefix (the formulas: latent_attention.hip).
+//
+// One workgroup of eight waves shares each staged 64-key tile; a wave owns 16
+// query rows and carries them alone through both products:
+//   S^T (64 keys x 16 rows) = K Q^T, its queries in registers;
+//   O^T (512 columns x 16 rows) += V^T P^T.
+// The first product leaves a lane with row lane % 16 and keys 4g .. 4g+3
+// (g = lane / 16) of each 16-key block, which is the second one's operand
+// when its 32 keys are counted as 4g .. 4g+3 of two blocks: P never leaves its
+// registers, and the values are read transposed in that order.  So waves meet
+// only where a tile is handed over, and the two waves of a SIMD fill each
+// other's pauses.  The exponent's reference moves when a score of the wave's
+// rows passes it by 2^kSlack.  With 64 rows the waves form two groups of four,
+// each with half of every tile's keys, joined through LDS at the end.
+#include "device_once.h"
+#include "latent_common.h"
+
+namespace dsaidx {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kAhead = 3;   // operand reads in flight
+constexpr int kLds = 2 * kTileB;
+static_assert(kLds <= 160 * 1024, "LDS budget");
+static_assert(4 * 32 * 64 * 16 + 4 * 64 * 8 <= kLds, "the join of two key groups fits the tiles' place");
+
+template <int KD, int KG, bool TOPK>
+__global__ void __launch_bounds__(kThreads, 2)
+latent_rows_kernel(LatentArgs a, LatentPlan p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int E = 32 * KD;
+    constexpr int RB = 2 * E;
+    constexpr int RG = 8 / KG;            // row groups of 16
+    constexpr int kParts = KD > 16 ? 9 : 8;  // copies of a tile that a wave makes
+    const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
+    const int n = lane & 15, g = lane >> 4;
+    const int rg = wave % RG, kg = wave / RG;
+    LatentKeys<TOPK> keys;
+    if (!keys.start(a, p)) return;
+    const int nrows = keys.nrows, t1 = keys.t1;
+    const bool active = 16 * rg < nrows;
+
+    // ---- queries: B operand of 16 rows x 32 columns ----
+    v8bf Q[KD];
+    {
+        const uint16_t* qp = a.q + (int64_t)(keys.r0 + min(16 * rg + n, nrows - 1)) * E + 8 * g;
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks) Q[ks] = *reinterpret_cast<const v8bf*>(qp + 32 * ks);
+    }
+
+    // ---- copies: rows 8w .. 8w+7 of a tile ----
+    const int kb = 8 * wave;
+    const uint32_t lds0 = lds_address(smem);
+    int rope_row = -1;   // the row whose rotary columns this lane copies a piece of
+    auto spread = [&]() {
+        if constexpr (KD > 16) rope_row = __shfl(keys.row, kb + (lane >> 3));
+    };
+    auto stage = [&](int buf, int i) {
+        const uint32_t lds = lds0 + buf * kTileB;
+        if (i < 8) {
+            copy_to_lds(row_address<RB>(a.cache, __builtin_amdgcn_readlane(keys.row, kb + i)), 16 * lane,
+                        lds + (kb + i) * kRowB);
+        } else {
+            const int piece = (lane & 7) ^ ((kb / 2 + (lane >> 4)) & 7);
+            copy_to_lds(row_address<RB>(a.cache, rope_row) + 2 * kV + 16 * piece, lds + kMainB + kb * 128);
+        }
+    };
+
+    LatentAhead ahead;
+    int t = keys.seek(keys.t0, ahead);
+    uint64_t here = keys.mask;
+    spread();
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) stage(0, i);
+    int t_next = t + 1, buf = 0;
+    // the tile behind t, from what is ahead of it
+    keys.resolve(t_next < t1 ? ahead.s2 : -1, ahead.page2);
+    if (keys.mask == 0 && t_next < t1) {
+        t_next = keys.seek(t_next + 1, ahead);
+    } else {
+        ahead.s2 = ahead.s3;
+        ahead.page2 = keys.page(ahead.s2, t_next + 1);
+        ahead.s3 = keys.entry(t_next + 2);
+    }
+    spread();
+
+    if (a.scale_log2 < 0.f)   // the products then take the scale's magnitude
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks) {
+            v4i u = __builtin_bit_cast(v4i, Q[ks]);
+            u ^= (int)0x80008000;
+            Q[ks] = __builtin_bit_cast(v8bf, u);
+        }
+    // (never 0: a score of -inf, an entry without a row, has to stay one)
+    const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
+
+    v4f O[32];
+#pragma unroll
+    for (int ct = 0; ct < 32; ++ct) O[ct] = v4f{0.f, 0.f, 0.f, 0.f};
+    float m = -__builtin_inff(), l = 0.f;
+
+    while (t < t1) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the tile
+        tile_barrier();
+        // loads for the tiles behind the next one
+        const int page3 = keys.page(ahead.s3, t_next + 2);
+        const int s4 = keys.entry(t_next + 3);
+        const int t_now = t_next;
+        const uint64_t next = keys.mask;
+        if (active) {
+            const unsigned char* tile = smem + buf * kTileB;
+            // the lane's place in the tile, made anew for every tile: kept, it would cost registers that Q and O need
+            int own = lane;
+            asm volatile("" : "+v"(own));
+            const int n = own & 15, g = own >> 4;
+            // 32 keys at a time: one of the tile's halves (KG == 2) or both
+#pragma unroll
+            for (int hh = 0; hh < 2 / KG; ++hh) {
+            const int k0 = 32 * (KG == 2 ? kg : hh);
+            // ---- scores ----
+            const unsigned char* kp = tile + (k0 + n) * kRowB + 16 * g;
+            const unsigned char* kr = tile + kMainB + (k0 + n) * 128;
+            auto read_k = [&](int f) {   // step f: columns 32 (f / 2) .., keys 16 (f % 2) ..
+                const int ks = f / 2, kt = f % 2;
+                return *reinterpret_cast<const v8bf*>(
+                    ks < 16 ? kp + 16 * kt * kRowB + 64 * ks
+                            : kr + 16 * kt * 128 + 16 * ((4 * (ks - 16) + g) ^ ((n >> 1) & 7)));
+            };
+            v4f S[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
+            v8bf K[kAhead];
+#pragma unroll
+            for (int f = 0; f < kAhead; ++f) K[f] = read_k(f);
+#pragma unroll
+            for (int ks = 0; ks < KD; ++ks) {
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt) {
+                    const int f = 2 * ks + kt;
+                    S[kt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(K[f % kAhead], Q[ks], S[kt], 0, 0, 0);
+                    if (f + kAhead < 2 * KD) K[f % kAhead] = read_k(f + kAhead);
+                }
+                if (hh == 0 && ks % 2 == 0 && ks / 2 < kParts) stage(buf ^ 1, ks / 2);   // behind the last tile: zeros
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // ---- softmax ----
+            if (here != ~0ull) {
+                const uint32_t mine = (uint32_t)(here >> (k0 + 4 * g));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    S[0][i] = mine >> i & 1 ? S[0][i] : -__builtin_inff();
+                    S[1][i] = mine >> (16 + i) & 1 ? S[1][i] : -__builtin_inff();
+                }
+            }
+            float top = fmaxf(S[0][0], S[1][0]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) top = fmaxf(top, fmaxf(S[0][i], S[1][i]));
+            top *= scale;
+            if (wave_ballot(top > m + kSlack)) {
+                // the reference moves to these keys' maximum where that is above it
+                top = fmaxf(top, __shfl_xor(top, 16, kWave));
+                top = fmaxf(top, __shfl_xor(top, 32, kWave));
+                const float to = fmaxf(m, top);
+                const float f = m == to ? 1.f : __builtin_amdgcn_exp2f(m - to);
+                m = to;
+                l *= f;
+#pragma unroll
+                for (int ct = 0; ct < 32; ++ct) O[ct] *= f;
+            }
+            const float ref = m == -__builtin_inff() ? 0.f : m;
+            v4i u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float pr[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    pr[i] = __builtin_amdgcn_exp2f(fmaf(S[h][i], scale, -ref));
+                    l += pr[i];
+                }
+                u[2 * h] = (int)pack_bf16(pr[0], pr[1]);
+                u[2 * h + 1] = (int)pack_bf16(pr[2], pr[3]);
+            }
+            const v8bf P = __builtin_bit_cast(v8bf, u);
+            // ---- values; beside them, the rows of the tile behind the next one ----
+            const unsigned char* vp = tile + (k0 + 4 * g + (n >> 2)) * kRowB + 8 * (n & 3);
+            auto read_v = [&](int ct) {
+                const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vp + 32 * ct));
+                const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vp + 32 * ct + 16 * kRowB));
+                return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            };
+            v8bf W[kAhead];
+#pragma unroll
+            for (int f = 0; f < kAhead; ++f) W[f] = read_v(f);
+#pragma unroll
+            for (int ct = 0; ct < 32; ++ct) {
+                if (ct % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+                O[ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(W[ct % kAhead], P, O[ct], 0, 0, 0);
+                if (ct + kAhead < 32) W[ct % kAhead] = read_v(ct + kAhead);
+                if (ct == 8 && hh == 2 / KG - 1) {
+                    keys.resolve(t_now + 1 < t1 ? ahead.s2 : -1, ahead.page2);
+                    spread();
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) stage(buf ^ 1, i);
+            keys.resolve(t_now + 1 < t1 ? ahead.s2 : -1, ahead.page2);
+            spread();
+        }
+        here = next;
+        buf ^= 1;
+        t = t_now;
+        t_next = t_now + 1;
+        ahead = LatentAhead{ahead.s3, page3, s4};
+        if (keys.mask == 0 && t_next < t1) {
+            t_next = keys.seek(t_next + 1, ahead);
+            spread();
+        }
+    }
+
+    // ---- join the key groups, write ----
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // no copy may still be in flight
+    l += __shfl_xor(l, 16, kWave);
+    l += __shfl_xor(l, 32, kWave);
+    if constexpr (KG == 2) {
+        v4f* there = reinterpret_cast<v4f*>(smem) + rg * 32 * 64 + lane;
+        float2* ml = reinterpret_cast<float2*>(smem + 4 * 32 * 64 * 16) + rg * 64 + lane;
+        tile_barrier();
+        if (kg == 1) {
+#pragma unroll
+            for (int ct = 0; ct < 32; ++ct) there[64 * ct] = O[ct];
+            *ml = float2{m, l};
+        }
+        tile_barrier();
+        if (kg == 1) return;
+        const float2 b = *ml;
+        const float to = fmaxf(m, b.x);
+        const float f = m == to ? 1.f : __builtin_amdgcn_exp2f(m - to);
+        const float fb = b.x == to ? 1.f : __builtin_amdgcn_exp2f(b.x - to);
+        m = to;
+        l = l * f + b.y * fb;
+#pragma unroll
+        for (int ct = 0; ct < 32; ++ct) O[ct] = O[ct] * f + there[64 * ct] * fb;
+    }
+    if (16 * rg + n >= nrows) return;
+    const int64_t r = keys.r0 + 16 * rg + n;
+    if (p.slots == 1) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* out = a.out + r * kV + 4 * g;
+#pragma unroll
+        for (int ct = 0; ct < 32; ++ct) {
+            const v4f o = O[ct] * inv;
+            *reinterpret_cast<uint2*>(out + 16 * ct) = uint2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+        }
+        if (a.lse && g == 0) a.lse[r] = l == 0.f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945f;
+    } else {
+        const int64_t at = (int64_t)keys.slot * (a.T * a.H) + r;
+        if (l != 0.f) {   // (NaN too)
+            float* out = p.part_o + at * kV + 4 * g;
+#pragma unroll
+            for (int ct = 0; ct < 32; ++ct) *reinterpret_cast<v4f*>(out + 16 * ct) = O[ct];
+        }
+        if (g == 0) p.part_ml[at] = float2{m, l};
+    }
+}
+
+template <int KD, int KG, bool TOPK>
+hipError_t run(const LatentArgs& a, const LatentPlan& p, hipStream_t stream) {
+    static PerDevice<int> once;
+    const hipError_t e = set_lds_limit(once, (const void*)latent_rows_kernel<KD, KG, TOPK>, kLds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((latent_rows_kernel<KD, KG, TOPK>), dim3((unsigned)(p.n_prefix + p.n_own)), dim3(kThreads),
+                       kLds, stream, a, p);
+    return hipGetLastError();
+}
+
+template <int KD, int KG>
+hipError_t run(const LatentArgs& a, const LatentPlan& p, hipStream_t stream) {
+    return a.idx ? run<KD, KG, true>(a, p, stream) : run<KD, KG, false>(a, p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_latent_rows(const LatentArgs& a, const LatentPlan& p, bool fp8, hipStream_t stream) {
+    if (a.E == 576) return p.rows == 64 ? run<18, 2>(a, p, stream) : run<18, 1>(a, p, stream);
+    return p.rows == 64 ? run<16, 2>(a, p, stream) : run<16, 1>(a, p, stream);
+}
+
+}  // namespace dsaidx

@@ -92,12 +92,10 @@ def test_wrappers_refuse(lib):
     table, n = torch.zeros((1, 2), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError, match="device"):
         dsa.latent_attention_topk(q, cache, table, idx, 512, 1.0)
-    with pytest.raises(ValueError, match="q must be"):
-        dsa.latent_attention_topk(q.float(), cache, table, idx, 512, 1.0)
-    with pytest.raises(ValueError, match="latent_cache"):
-        dsa.latent_attention_topk(q, cache[:, :, :512], table, idx, 512, 1.0)
-    with pytest.raises(ValueError, match="latent_scale"):
-        dsa.latent_attention_shared(q, cache.view(torch.uint8)[:, :, :576], None, 0, table, n, 512, 1.0)
+    with pytest.raises(ValueError, match="latent_cache must be"):
+        dsa.latent_attention_topk(q, cache.float(), table, idx, 512, 1.0)
+    with pytest.raises(ValueError, match="topk_idx must be"):
+        dsa.latent_attention_topk(q, cache, table, idx.long(), 512, 1.0)
     with pytest.raises(ValueError, match="device"):
         dsa.latent_attention_shared(q, cache, None, 0, table, n, 512, 1.0)
     kv = torch.zeros((3, 576), dtype=torch.bfloat16)
