@@ -50,13 +50,9 @@ template <int KD, int MT, bool FP8>
 struct Lds {
     static constexpr int kMain = FP8 ? kTile / 2 * kPairB : kMainB;                // a tile's value columns,
     static constexpr int kRope = KD > 16 ? (FP8 ? kTile * 64 : kRopeB) : 0;        // and rotary columns
-    // 64 query rows: their rotary columns stay in LDS, in place of a second set
-    // of the tile's, which is kept in registers until the scores are done
-    static constexpr bool kQInLds = MT == 4 && KD > 16;
-    static constexpr bool kOneRope = kQInLds && !FP8;
+    static constexpr bool kQInLds = MT == 4 && KD > 16;   // 64 query rows: their rotary columns stay in LDS
     static constexpr int kRopeAt = 2 * kMain;
-    static constexpr int kRopeStep = kOneRope ? 0 : kRope;
-    static constexpr int kP = kRopeAt + (kOneRope ? 1 : 2) * kRope;
+    static constexpr int kP = kRopeAt + 2 * kRope;
     static constexpr int kRed = kP + MT * 16 * kPRowB;     // [4][16 MT] floats
     static constexpr int kScale = kRed + 4 * 16 * MT * 4;  // [2][64] floats
     static constexpr int kFlag = kScale + (FP8 ? 512 : 0); // [2]
@@ -101,7 +97,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     constexpr int CT = 32 / NW;           // and 16-column blocks of the values
     constexpr int kAhead = NW == 8 ? 2 : 3;   // operand reads in flight
     constexpr int KB = kTile / NW;        // rows of a tile that a wave copies
-    constexpr int kMainParts = FP8 ? KB / 2 : KB, kParts = kMainParts + (KD == 16 || L::kOneRope ? 0 : FP8 ? 1 : KB / 8);
+    constexpr int kMainParts = FP8 ? KB / 2 : KB, kParts = kMainParts + (KD == 16 ? 0 : FP8 ? 1 : KB / 8);
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int kq = wave & 3, rh = wave >> 2;   // 16 keys, and rows 16 MQ rh .., of the scores
     const int n = lane & 15, g = lane >> 4;
@@ -148,7 +144,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     };
     auto rope_piece = [&](int r) { return 16 * ((lane & 7) ^ ((r >> 1) & 7)); };
     auto stage = [&](int buf, int i, int mine) {
-        const uint32_t lds = lds0 + buf * L::kMain, rope = lds0 + L::kRopeAt + buf * L::kRopeStep;
+        const uint32_t lds = lds0 + buf * L::kMain, rope = lds0 + L::kRopeAt + buf * L::kRope;
         if constexpr (FP8) {
             if (i < kMainParts) {
                 copy_to_lds(row_address<RB>(a.cache, mine) + 16 * ((lane & 31) ^ (lane >> 5) * 8),
@@ -164,17 +160,6 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
             const int r = kb + 8 * (i - kMainParts);
             copy_to_lds(row_address<RB>(a.cache, mine) + 2 * kV + rope_piece(r + (lane >> 3)), rope + r * 128);
         }
-    };
-    // The rotary columns that are kept in registers: 8 rows a wave.
-    v4i kept = v4i{0, 0, 0, 0};
-    auto keep = [&]() {
-        if constexpr (L::kOneRope) {
-            const int r = kb + (lane >> 3);
-            kept = *reinterpret_cast<const v4i*>(row_address<RB>(a.cache, __shfl(keys.row, r)) + 2 * kV + rope_piece(r));
-        }
-    };
-    auto put_kept = [&]() {
-        if constexpr (L::kOneRope) *reinterpret_cast<v4i*>(smem + L::kRopeAt + kb * 128 + 16 * lane) = kept;
     };
     float kscale = 0.f;   // fp8: scale of the next tile's entry `lane`
     auto load_scale = [&]() {
@@ -193,7 +178,6 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     address();
 #pragma unroll
     for (int i = 0; i < kParts; ++i) stage(0, i, part_row(i));
-    keep();
     load_scale();
     int t_next = t + 1, buf = 0;
     // the tile behind t, from what is ahead of it
@@ -207,7 +191,6 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     }
     address();
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): queries and first tile
-    put_kept();
     tile_barrier();
     // B operand of 16 rows x 32 columns: row n, columns 8g .. 8g+7 of each 32
     constexpr int KQ = L::kQInLds ? 16 : KD;
@@ -240,7 +223,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     float m[MT], l[MQ];   // references of all rows; sums of the rows and keys whose scores are this wave's
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        m[mt] = -__builtin_inff();
+        m[mt] = -3.402823466e38f;   // the lowest finite: any score but -inf moves it
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) O[ct][mt] = v4f{0.f, 0.f, 0.f, 0.f};
     }
@@ -253,7 +236,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     auto renew = [&]() { asm volatile("" : "+v"(ln)); };
     // A operand of the scores: this wave's 16 keys, 32 columns of step ks
     auto read_k = [&](int buf, int ks) {
-        const unsigned char *tile = smem + buf * L::kMain, *rope = smem + L::kRopeAt + buf * L::kRopeStep;
+        const unsigned char *tile = smem + buf * L::kMain, *rope = smem + L::kRopeAt + buf * L::kRope;
         Operand<FP8> k;
         const int n = ln & 15, g = ln >> 4;
         if constexpr (FP8) {
@@ -308,8 +291,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
 #pragma unroll
         for (int j = 0; j < MQ; ++j) {
             const int mt = MQ * rh + j;
-            const float mine = NW == 4 ? m[j] : rh ? m[MT - MQ + j] : m[j];
-            const float ref = mine == -__builtin_inff() ? 0.f : mine;
+            const float ref = NW == 4 ? m[j] : rh ? m[MT - MQ + j] : m[j];
             float pr[4];
             sum[j] = 0.f;
 #pragma unroll
@@ -340,7 +322,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
             float v = m[mt];
 #pragma unroll
             for (int w = 0; w < 4; ++w) v = fmaxf(v, red[w * 16 * MT + 16 * mt + n]);
-            const float f = m[mt] == v ? 1.f : __builtin_amdgcn_exp2f(m[mt] - v);
+            const float f = __builtin_amdgcn_exp2f(m[mt] - v);
             m[mt] = v;
             if (NW == 4 || mt / MQ == rh) l[mt % MQ] *= f;
 #pragma unroll
@@ -392,7 +374,6 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         __builtin_amdgcn_sched_barrier(0);
         // ---- softmax against the rows' references ----
         if (NW == 8) renew();
-        keep();
         if constexpr (FP8) {
             const v4f s4 = *reinterpret_cast<const v4f*>(smem + L::kScale + 256 * buf + 4 * (16 * kq + 4 * (ln >> 4)));
 #pragma unroll
@@ -441,7 +422,6 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
             }
             if (i == 2 * CT - kAhead) {
                 __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-                put_kept();
                 store_scale(buf ^ 1);
                 tile_barrier();
             }
@@ -561,7 +541,7 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 int pad8(int n) { return (n + 7) / 8 * 8; }
 
 // Query rows of a workgroup: the smallest block that holds all of them, at most 64.
-int block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int block_rows(int64_t rows, bool fp8) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || fp8 ? 64 : 128; }
 
 // Splits of the key tiles that finish first, in us (p.rows and the tile counts
 // are given).  A workgroup takes 5 and its tiles: 1 to 2.7 each by its rows,
@@ -570,7 +550,7 @@ int block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 // A run of own tiles is as long as one of the prefix.
 double split(int64_t blocks_p, int tiles_p, int64_t blocks_o, int tiles_o, int64_t rows, bool fp8, LatentPlan& p) {
     static const int kSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32};
-    const double tile = p.rows == 16 ? 1.6 : p.rows == 32 ? 1.6 : 1.8;
+    const double tile = p.rows == 16 ? 1.4 : p.rows == 32 ? 1.6 : p.rows == 64 ? 2.0 : 3.5;
     const int tiles = tiles_p > 0 ? tiles_p : tiles_o;
     double best = 1e30;
     for (int n : kSplits) {
@@ -581,8 +561,8 @@ double split(int64_t blocks_p, int tiles_p, int64_t blocks_o, int tiles_o, int64
         if (lo < ceil_div(tiles_o, 32)) lo = ceil_div(tiles_o, 32);
         const int so = tiles_o > 0 ? ceil_div(tiles_o, lo) : 0;
         const int64_t np = blocks_p * sp, no = blocks_o * so;
-        const double stream = (fp8 ? 1.8 : 3.6) * (double)(no < kCUs ? no : kCUs) / kCUs;
-        const double cp = 5 + tile * len, co = 5 + (tile > stream ? tile : stream) * lo;
+        const double full = (fp8 ? 1.8 : 3.6) - tile;   // more per tile with every CU streaming
+        const double cp = 5 + tile * len, co = 5 + (tile + (full > 0 ? full : 0) * (double)(no < kCUs ? no : kCUs) / kCUs) * lo;
         // whole rounds of prefix parts; the rest of them beside the own parts
         const int64_t rest = np % kCUs;
         int64_t k = no / kCUs;   // own parts one after another on a CU
@@ -613,14 +593,14 @@ LatentPlan make_plan(int T, int H, bool topk, int K, int prefix_len, int max_ctx
     const int64_t rows = (int64_t)T * H;
     // every query walks all its keys (none: one workgroup a row block writes that)
     LatentPlan p{};
-    p.rows = block_rows(H);
+    p.rows = block_rows(H, fp8);
     p.hb = ceil_div(H, p.rows);
     p.joint = tiles_p > 0;
     const int all = tiles_p + tiles_o;
     const double us = split(0, 0, (int64_t)T * p.hb, all > 0 ? all : 1, rows, fp8, p);
     if (tiles_p > 0) {   // or the prefix is walked once for the stacked rows
         LatentPlan s{};
-        s.rows = block_rows(rows);
+        s.rows = block_rows(rows, fp8);
         s.hb = ceil_div(H, s.rows);
         s.rb = ceil_div(rows, s.rows);
         if (split(s.rb, tiles_p, tiles_o > 0 ? (int64_t)T * s.hb : 0, tiles_o, rows, fp8, s) < us) p = s;
@@ -654,9 +634,8 @@ hipError_t run(const LatentArgs& a, const LatentPlan& p, bool fp8, hipStream_t s
 
 template <int KD>
 hipError_t run(const LatentArgs& a, const LatentPlan& p, bool fp8, hipStream_t stream) {
-    return p.rows == 16   ? run<KD, 1>(a, p, fp8, stream)
-           : p.rows == 32 ? run<KD, 2>(a, p, fp8, stream)
-                          : run<KD, 4>(a, p, fp8, stream);
+    if (p.rows == 64) return a.idx ? run<KD, 4, true, true>(a, p, stream) : run<KD, 4, false, true>(a, p, stream);
+    return p.rows == 16 ? run<KD, 1>(a, p, fp8, stream) : run<KD, 2>(a, p, fp8, stream);
 }
 
 }  // namespace
@@ -673,7 +652,7 @@ hipError_t launch_latent_attention(const LatentArgs& a, bool fp8, hipStream_t st
     LatentPlan p = make_plan(a.T, a.H, a.idx != nullptr, a.K, a.prefix_len, a.max_ctx, fp8);
     p.part_o = reinterpret_cast<float*>(a.workspace);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)p.slots * a.T * a.H * kV);
-    hipError_t e = a.E == 576 ? run<18>(a, p, fp8, stream) : run<16>(a, p, fp8, stream);
+    hipError_t e = p.rows >= 64 && !fp8 ? launch_latent_rows(a, p, stream) : a.E == 576 ? run<18>(a, p, fp8, stream) : run<16>(a, p, fp8, stream);
     if (e != hipSuccess || p.slots == 1) return e;
     hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)(a.T * a.H)), dim3(kJoinThreads), 0, stream, a, p);
     return hipGetLastError();

@@ -213,7 +213,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v2bf{(__bf16)lo, (__bf16)hi});
 }
 
-// Blocks of 64 or 128 query rows (csrc/latent_rows.hip); fewer in latent_attention.hip.
-hipError_t launch_latent_rows(const LatentArgs& a, const LatentPlan& p, bool fp8, hipStream_t stream);
+// Blocks of 64 or 128 query rows on a bf16 cache (csrc/latent_rows.hip).
+hipError_t launch_latent_rows(const LatentArgs& a, const LatentPlan& p, hipStream_t stream);
 
 }  // namespace dsaidx

@@ -76,7 +76,7 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
     for (int i = 0; i < kParts; ++i) stage(0, i);
     int t_next = t + 1, buf = 0;
     // the tile behind t, from what is ahead of it
-    keys.resolve(t_next < t1 ? ahead.s2 : -1, ahead.page2);
+    keys.resolve(t_next < t1 ? keys.entry_of(t_next, ahead.s2) : -1, ahead.page2);
     if (keys.mask == 0 && t_next < t1) {
         t_next = keys.seek(t_next + 1, ahead);
     } else {
@@ -96,10 +96,15 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
     // (never 0: a score of -inf, an entry without a row, has to stay one)
     const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
 
+    // The lane, made anew for every phase: what follows from it, kept longer,
+    // would cost registers that the queries and sums need.
+    int ln = lane;
+    auto renew = [&]() { asm volatile("" : "+v"(ln)); };
     v4f O[32];
 #pragma unroll
     for (int ct = 0; ct < 32; ++ct) O[ct] = v4f{0.f, 0.f, 0.f, 0.f};
-    float m = -__builtin_inff(), l = 0.f;
+    // the reference starts below every score that is not -inf, so that a row's first one moves it
+    float m = -3.402823466e38f, l = 0.f;
 
     while (t < t1) {
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the tile
@@ -111,22 +116,19 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
         const uint64_t next = keys.mask;
         if (active) {
             const unsigned char* tile = smem + buf * kTileB;
-            // the lane's place in the tile, made anew for every tile: kept, it would cost registers that Q and O need
-            int own = lane;
-            asm volatile("" : "+v"(own));
-            const int n = own & 15, g = own >> 4;
             // 32 keys at a time: one of the tile's halves (KG == 2) or both
 #pragma unroll
             for (int hh = 0; hh < 2 / KG; ++hh) {
             const int k0 = 32 * (KG == 2 ? kg : hh);
             // ---- scores ----
-            const unsigned char* kp = tile + (k0 + n) * kRowB + 16 * g;
-            const unsigned char* kr = tile + kMainB + (k0 + n) * 128;
+            renew();
+            const unsigned char* kp = tile + (k0 + (ln & 15)) * kRowB + 16 * (ln >> 4);
+            const unsigned char* kr = tile + kMainB + (k0 + (ln & 15)) * 128;
             auto read_k = [&](int f) {   // step f: columns 32 (f / 2) .., keys 16 (f % 2) ..
                 const int ks = f / 2, kt = f % 2;
                 return *reinterpret_cast<const v8bf*>(
                     ks < 16 ? kp + 16 * kt * kRowB + 64 * ks
-                            : kr + 16 * kt * 128 + 16 * ((4 * (ks - 16) + g) ^ ((n >> 1) & 7)));
+                            : kr + 16 * kt * 128 + 16 * ((4 * (ks - 16) + (ln >> 4)) ^ ((ln >> 1) & 7)));
             };
             v4f S[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
             v8bf K[kAhead];
@@ -145,8 +147,9 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
             }
             __builtin_amdgcn_sched_barrier(0);
             // ---- softmax ----
+            renew();
             if (here != ~0ull) {
-                const uint32_t mine = (uint32_t)(here >> (k0 + 4 * g));
+                const uint32_t mine = (uint32_t)(here >> k0) >> (4 * (ln >> 4));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     S[0][i] = mine >> i & 1 ? S[0][i] : -__builtin_inff();
@@ -162,20 +165,19 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
                 top = fmaxf(top, __shfl_xor(top, 16, kWave));
                 top = fmaxf(top, __shfl_xor(top, 32, kWave));
                 const float to = fmaxf(m, top);
-                const float f = m == to ? 1.f : __builtin_amdgcn_exp2f(m - to);
+                const float f = __builtin_amdgcn_exp2f(m - to);
                 m = to;
                 l *= f;
 #pragma unroll
                 for (int ct = 0; ct < 32; ++ct) O[ct] *= f;
             }
-            const float ref = m == -__builtin_inff() ? 0.f : m;
             v4i u;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float pr[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    pr[i] = __builtin_amdgcn_exp2f(fmaf(S[h][i], scale, -ref));
+                    pr[i] = __builtin_amdgcn_exp2f(fmaf(S[h][i], scale, -m));
                     l += pr[i];
                 }
                 u[2 * h] = (int)pack_bf16(pr[0], pr[1]);
@@ -183,7 +185,7 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
             }
             const v8bf P = __builtin_bit_cast(v8bf, u);
             // ---- values; beside them, the rows of the tile behind the next one ----
-            const unsigned char* vp = tile + (k0 + 4 * g + (n >> 2)) * kRowB + 8 * (n & 3);
+            const unsigned char* vp = tile + (k0 + 4 * (ln >> 4) + (ln >> 2 & 3)) * kRowB + 8 * (ln & 3);
             auto read_v = [&](int ct) {
                 const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vp + 32 * ct));
                 const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vp + 32 * ct + 16 * kRowB));
@@ -198,7 +200,7 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
                 O[ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(W[ct % kAhead], P, O[ct], 0, 0, 0);
                 if (ct + kAhead < 32) W[ct % kAhead] = read_v(ct + kAhead);
                 if (ct == 8 && hh == 2 / KG - 1) {
-                    keys.resolve(t_now + 1 < t1 ? ahead.s2 : -1, ahead.page2);
+                    keys.resolve(t_now + 1 < t1 ? keys.entry_of(t_now + 1, ahead.s2) : -1, ahead.page2);
                     spread();
                 }
             }
@@ -207,7 +209,7 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
         } else {
 #pragma unroll
             for (int i = 0; i < kParts; ++i) stage(buf ^ 1, i);
-            keys.resolve(t_now + 1 < t1 ? ahead.s2 : -1, ahead.page2);
+            keys.resolve(t_now + 1 < t1 ? keys.entry_of(t_now + 1, ahead.s2) : -1, ahead.page2);
             spread();
         }
         here = next;
@@ -238,8 +240,7 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
         if (kg == 1) return;
         const float2 b = *ml;
         const float to = fmaxf(m, b.x);
-        const float f = m == to ? 1.f : __builtin_amdgcn_exp2f(m - to);
-        const float fb = b.x == to ? 1.f : __builtin_amdgcn_exp2f(b.x - to);
+        const float f = __builtin_amdgcn_exp2f(m - to), fb = __builtin_amdgcn_exp2f(b.x - to);
         m = to;
         l = l * f + b.y * fb;
 #pragma unroll
@@ -284,7 +285,7 @@ hipError_t run(const LatentArgs& a, const LatentPlan& p, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_latent_rows(const LatentArgs& a, const LatentPlan& p, bool fp8, hipStream_t stream) {
+hipError_t launch_latent_rows(const LatentArgs& a, const LatentPlan& p, hipStream_t stream) {
     if (a.E == 576) return p.rows == 64 ? run<18, 2>(a, p, stream) : run<18, 1>(a, p, stream);
     return p.rows == 64 ? run<16, 2>(a, p, stream) : run<16, 1>(a, p, stream);
 }
