@@ -541,7 +541,7 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 int pad8(int n) { return (n + 7) / 8 * 8; }
 
 // Query rows of a workgroup: the smallest block that holds all of them, at most 64.
-int block_rows(int64_t rows, bool fp8) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || fp8 ? 64 : 128; }
+int block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
 // Splits of the key tiles that finish first, in us (p.rows and the tile counts
 // are given).  A workgroup takes 5 and its tiles: 1 to 2.7 each by its rows,
@@ -593,14 +593,14 @@ LatentPlan make_plan(int T, int H, bool topk, int K, int prefix_len, int max_ctx
     const int64_t rows = (int64_t)T * H;
     // every query walks all its keys (none: one workgroup a row block writes that)
     LatentPlan p{};
-    p.rows = block_rows(H, fp8);
+    p.rows = block_rows(H);
     p.hb = ceil_div(H, p.rows);
     p.joint = tiles_p > 0;
     const int all = tiles_p + tiles_o;
     const double us = split(0, 0, (int64_t)T * p.hb, all > 0 ? all : 1, rows, fp8, p);
     if (tiles_p > 0) {   // or the prefix is walked once for the stacked rows
         LatentPlan s{};
-        s.rows = block_rows(rows, fp8);
+        s.rows = block_rows(rows);
         s.hb = ceil_div(H, s.rows);
         s.rb = ceil_div(rows, s.rows);
         if (split(s.rb, tiles_p, tiles_o > 0 ? (int64_t)T * s.hb : 0, tiles_o, rows, fp8, s) < us) p = s;
@@ -652,7 +652,7 @@ hipError_t launch_latent_attention(const LatentArgs& a, bool fp8, hipStream_t st
     LatentPlan p = make_plan(a.T, a.H, a.idx != nullptr, a.K, a.prefix_len, a.max_ctx, fp8);
     p.part_o = reinterpret_cast<float*>(a.workspace);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)p.slots * a.T * a.H * kV);
-    hipError_t e = p.rows >= 64 && !fp8 ? launch_latent_rows(a, p, stream) : a.E == 576 ? run<18>(a, p, fp8, stream) : run<16>(a, p, fp8, stream);
+    hipError_t e = p.rows == 128 || (p.rows == 64 && !fp8) ? launch_latent_rows(a, p, fp8, stream) : a.E == 576 ? run<18>(a, p, fp8, stream) : run<16>(a, p, fp8, stream);
     if (e != hipSuccess || p.slots == 1) return e;
     hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)(a.T * a.H)), dim3(kJoinThreads), 0, stream, a, p);
     return hipGetLastError();

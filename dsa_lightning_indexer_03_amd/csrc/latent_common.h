@@ -68,6 +68,10 @@ __device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, uint
 __device__ __forceinline__ void copy_to_lds(const void* p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
 }
+// The same, 4 bytes per lane.
+__device__ __forceinline__ void copy4_to_lds(const void* p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory");
+}
 
 // Eight E4M3 codes -> eight bf16 (exact).
 __device__ __forceinline__ v4i widen8(uint2 c) {
@@ -213,7 +217,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v2bf{(__bf16)lo, (__bf16)hi});
 }
 
-// Blocks of 64 or 128 query rows on a bf16 cache (csrc/latent_rows.hip).
-hipError_t launch_latent_rows(const LatentArgs& a, const LatentPlan& p, hipStream_t stream);
+// Blocks of 128 query rows, or of 64 on a bf16 cache (csrc/latent_rows.hip).
+hipError_t launch_latent_rows(const LatentArgs& a, const LatentPlan& p, bool fp8, hipStream_t stream);
 
 }  // namespace dsaidx
