@@ -543,26 +543,29 @@ int pad8(int n) { return (n + 7) / 8 * 8; }
 // Query rows of a workgroup: the smallest block that holds all of them, at most 64.
 int block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
+double tile_us(int rows) { return rows == 16 ? 1.4 : rows == 32 ? 1.9 : rows == 64 ? 2.6 : 4.2; }
+
 // Splits of the key tiles that finish first, in us (p.rows and the tile counts
 // are given).  A workgroup takes 5 and its tiles: 1 to 2.7 each by its rows,
 // or what streaming 74 KB to every busy CU takes; the GPU runs one per CU,
 // prefix parts first; joining takes 4 and reads and writes every slot's sums.
 // A run of own tiles is as long as one of the prefix.
-double split(int64_t blocks_p, int tiles_p, int64_t blocks_o, int tiles_o, int64_t rows, bool fp8, LatentPlan& p) {
+double split(int64_t blocks_p, int tiles_p, int64_t blocks_o, int tiles_o, int64_t rows, int H, bool fp8, LatentPlan& p) {
     static const int kSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32};
-    const double tile = p.rows == 16 ? 1.4 : p.rows == 32 ? 1.6 : p.rows == 64 ? 2.0 : 3.5;
+    const double tile = tile_us(p.rows), tile_o = tile_us(block_rows(H < p.rows ? H : p.rows));
     const int tiles = tiles_p > 0 ? tiles_p : tiles_o;
     double best = 1e30;
     for (int n : kSplits) {
         if (n > 1 && n > tiles) break;
         const int len = ceil_div(tiles, n);
         const int sp = tiles_p > 0 ? ceil_div(tiles_p, len) : 0;
-        int lo = len < tiles_o ? len : tiles_o;
+        int lo = tiles_p > 0 ? (int)(len * tile / tile_o) : len;
+        if (lo > tiles_o) lo = tiles_o;
         if (lo < ceil_div(tiles_o, 32)) lo = ceil_div(tiles_o, 32);
         const int so = tiles_o > 0 ? ceil_div(tiles_o, lo) : 0;
         const int64_t np = blocks_p * sp, no = blocks_o * so;
-        const double full = (fp8 ? 1.8 : 3.6) - tile;   // more per tile with every CU streaming
-        const double cp = 5 + tile * len, co = 5 + (tile + (full > 0 ? full : 0) * (double)(no < kCUs ? no : kCUs) / kCUs) * lo;
+        const double full = (fp8 ? 1.8 : 3.6) - tile_o;   // more per tile with every CU streaming
+        const double cp = 5 + tile * len, co = 5 + (tile_o + (full > 0 ? full : 0) * (double)(no < kCUs ? no : kCUs) / kCUs) * lo;
         // whole rounds of prefix parts; the rest of them beside the own parts
         const int64_t rest = np % kCUs;
         int64_t k = no / kCUs;   // own parts one after another on a CU
@@ -597,13 +600,13 @@ LatentPlan make_plan(int T, int H, bool topk, int K, int prefix_len, int max_ctx
     p.hb = ceil_div(H, p.rows);
     p.joint = tiles_p > 0;
     const int all = tiles_p + tiles_o;
-    const double us = split(0, 0, (int64_t)T * p.hb, all > 0 ? all : 1, rows, fp8, p);
+    const double us = split(0, 0, (int64_t)T * p.hb, all > 0 ? all : 1, rows, H, fp8, p);
     if (tiles_p > 0) {   // or the prefix is walked once for the stacked rows
         LatentPlan s{};
         s.rows = block_rows(rows);
         s.hb = ceil_div(H, s.rows);
         s.rb = ceil_div(rows, s.rows);
-        if (split(s.rb, tiles_p, tiles_o > 0 ? (int64_t)T * s.hb : 0, tiles_o, rows, fp8, s) < us) p = s;
+        if (split(s.rb, tiles_p, tiles_o > 0 ? (int64_t)T * s.hb : 0, tiles_o, rows, H, fp8, s) < us) p = s;
     }
     p.n_prefix = pad8(p.rb * p.sp);
     p.n_own = pad8(T * p.hb * p.so);

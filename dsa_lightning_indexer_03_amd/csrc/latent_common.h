@@ -145,7 +145,8 @@ struct LatentKeys {
             const bool ok = b >= 0 && b < a.B;
             table = a.block_table + (int64_t)(ok ? b : 0) * a.max_pages;
             idx = a.idx + (int64_t)q * a.K;
-            len = ok ? a.K : 0;
+            len = a.K;   // (known before b is, so that the first entries' loads do not wait for it)
+            if (!ok) max_pages = 0;
         } else {
             table = a.block_table + (int64_t)q * a.max_pages;
             len = min(max(a.context_lens[q], 0), a.max_ctx);
@@ -185,16 +186,22 @@ struct LatentKeys {
     }
     // First tile at or behind t with a row, resolved, and what is ahead of it; t1: none.
     __device__ __forceinline__ int seek(int t, LatentAhead& ahead) {
-        resolve(-1, -1);
-        for (; t < t1; ++t) {
-            const int s = entry(t);
-            resolve(s, page(s, t));
-            if (mask) break;
-        }
+        int s = entry(t);
         LatentAhead h;
         h.s2 = entry(t + 1);
         h.s3 = entry(t + 2);
-        h.page2 = page(h.s2, t + 1);
+        resolve(-1, -1);
+        for (;;) {
+            const int id = page(s, t);
+            h.page2 = page(h.s2, t + 1);
+            if (t >= t1) break;
+            resolve(s, id);
+            if (mask) break;
+            ++t;
+            s = h.s2;
+            h.s2 = h.s3;
+            h.s3 = entry(t + 2);
+        }
         ahead = h;
         return t;
     }
