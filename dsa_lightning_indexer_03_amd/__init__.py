@@ -70,6 +70,7 @@ def _stream(device) -> int:
 
 # the same handle without the Python stream object (1.8 us a call) where torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor | None:
@@ -412,25 +413,32 @@ def prefill_chunk_paged(q, q_scale, w, k_cache, k_scale, block_table, q0: int, t
     return idx.view(B, Lq, topk), None if val is None else val.view(B, Lq, topk)
 
 
-def _all(dev, *checks) -> None:
+def _all(index: int, checks) -> None:
     """(name, tensor or None, element types): each tensor of one of its types,
-    contiguous, on `dev`, a GPU."""
+    contiguous, on GPU `index`."""
+    for _, t, dtypes in checks:
+        if t is not None and (t.dtype not in dtypes or t.get_device() != index or not t.is_contiguous()):
+            break
+    else:
+        if index >= 0:
+            return
     for name, t, dtypes in checks:
-        if t is not None and t.dtype not in dtypes:
-            _need(t, name, *dtypes)
+        _need(t, name, *dtypes)
     for name, t, _ in checks:
-        if t is not None and (t.device != dev or not t.is_contiguous() or dev.type != "cuda"):
+        if t is not None:
             _dev(t, name)
-            raise ValueError(f"{name} must be on {dev}, the device of the other tensors")
+            if t.get_device() != index:
+                raise ValueError(f"{name} must be on device {index}, the device of the other tensors")
 
 
 def _rows(t, name: str) -> int:
     """Row stride (elements) of a 2-D device tensor whose rows are contiguous."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+    s = t.stride()
+    if len(s) != 2 or (s[1] != 1 and t.shape[1] != 1):
         raise ValueError(f"{name} must be 2-D with contiguous rows")
-    return t.stride(0)
+    return s[0]
 
 
 def _inference_only(where: str, *tensors) -> None:
@@ -439,10 +447,9 @@ def _inference_only(where: str, *tensors) -> None:
             raise ValueError(f"{where} has no backward: call it under torch.no_grad() or detach its inputs")
 
 
-def _on_device(dev, fn, *args):
-    """fn(*args, stream) with `dev` current, on its current stream."""
-    index = dev.index
-    if torch.cuda.current_device() == index:
+def _on_device(index: int, fn, *args):
+    """fn(*args, stream) with GPU `index` current, on its current stream."""
+    if _current_device() == index:
         return fn(*args, _raw_stream(index))
     with torch.cuda.device(index):
         return fn(*args, _raw_stream(index))
@@ -471,17 +478,19 @@ def cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin
     all three None: latent rows only.  kv_interleaved, index_interleaved: pair
     i is columns (2i, 2i+1), else (i, i + R/2).  Returns nothing."""
     lib = _lib.load()
-    dev = kv.device
-    if kv.dtype not in _NEW:
+    index = kv.get_device()
+    dtype = kv.dtype
+    if dtype not in _NEW:
         _need(kv, "kv", *_NEW)
     kv_stride = _rows(kv, "kv")
     T, E = kv.shape
-    _all(dev, ("latent_cache", latent_cache, _LATENT), ("latent_scale", latent_scale, _FLOATS),
-         ("cos_sin", cos_sin, _FLOATS), ("seq_ids", seq_ids, _INTS), ("positions", positions, _INTS),
-         ("block_table", block_table, _INTS), ("k_cache", k_cache, _CODES), ("k_scale", k_scale, _FLOATS))
-    if latent_cache.dim() != 3 or latent_cache.shape[2] != E:
+    _all(index, (("latent_cache", latent_cache, _LATENT), ("latent_scale", latent_scale, _FLOATS),
+                 ("cos_sin", cos_sin, _FLOATS), ("seq_ids", seq_ids, _INTS), ("positions", positions, _INTS),
+                 ("block_table", block_table, _INTS), ("k_cache", k_cache, _CODES), ("k_scale", k_scale, _FLOATS)))
+    shape = latent_cache.shape
+    if len(shape) != 3 or shape[2] != E:
         raise ValueError("latent_cache must be [P, page, E] with the E of kv")
-    P, page, _ = latent_cache.shape
+    P, page, _ = shape
     fp8 = latent_cache.dtype != torch.bfloat16
     if fp8 != (latent_scale is not None) or (fp8 and latent_scale.shape != (P, page)):
         raise ValueError("latent_scale [P, page] goes with fp8 latent rows, None with bf16 rows")
@@ -494,17 +503,17 @@ def cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin
         raise ValueError("index_k, k_cache and k_scale go together")
     if index_k is not None:
         index_stride = _rows(index_k, "index_k")
-        D = index_k.shape[1]
-        if index_k.dtype != kv.dtype or index_k.shape[0] != T or index_k.device != dev:
+        n, D = index_k.shape
+        if index_k.dtype != dtype or n != T or index_k.get_device() != index:
             raise ValueError("index_k must be [T, D] of kv's type, on its device")
         if k_cache.shape != (P, page, D) or k_scale.shape != (P, page):
             raise ValueError("k_cache [P, page, D] / k_scale [P, page] shape mismatch")
     _inference_only("cache_append_rope", kv, index_k)
     B, max_pages = block_table.shape
     rope_len, R = cos_sin.shape
-    st = _on_device(dev, lib.indexer_cache_append_rope, kv.data_ptr(), kv_stride, 1 if kv_interleaved else 0,
+    st = _on_device(index, lib.indexer_cache_append_rope, kv.data_ptr(), kv_stride, 1 if kv_interleaved else 0,
                     _ptr(index_k), index_stride, 1 if index_interleaved else 0,
-                    BF16 if kv.dtype == torch.bfloat16 else F32, cos_sin.data_ptr(), rope_len, R,
+                    BF16 if dtype == torch.bfloat16 else F32, cos_sin.data_ptr(), rope_len, R,
                     seq_ids.data_ptr(), positions.data_ptr(), block_table.data_ptr(), B, max_pages,
                     latent_cache.data_ptr(), _ptr(latent_scale), FP8_E4M3 if fp8 else BF16, _ptr(k_cache),
                     _ptr(k_scale), P, T, E, D, page)
@@ -514,11 +523,12 @@ def cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin
 
 def _latent_inputs(q, latent_cache, latent_scale, block_table, where: str, *others):
     """Checks that the latent-attention calls share; returns (P, page, dtype code of the rows)."""
-    _all(q.device, ("q", q, _BF16), ("latent_cache", latent_cache, _LATENT), ("latent_scale", latent_scale, _FLOATS),
-         ("block_table", block_table, _INTS), *others)
-    if q.dim() != 3 or latent_cache.dim() != 3 or latent_cache.shape[2] != q.shape[2]:
+    _all(q.get_device(), (("q", q, _BF16), ("latent_cache", latent_cache, _LATENT),
+                          ("latent_scale", latent_scale, _FLOATS), ("block_table", block_table, _INTS), *others))
+    shape = latent_cache.shape
+    if q.dim() != 3 or len(shape) != 3 or shape[2] != q.shape[2]:
         raise ValueError("q must be [rows, H, E] and latent_cache [P, page, E]")
-    P, page, _ = latent_cache.shape
+    P, page, _ = shape
     fp8 = latent_cache.dtype != torch.bfloat16
     if fp8 != (latent_scale is not None) or (fp8 and latent_scale.shape != (P, page)):
         raise ValueError("latent_scale [P, page] goes with fp8 latent rows, None with bf16 rows")
@@ -528,16 +538,16 @@ def _latent_inputs(q, latent_cache, latent_scale, block_table, where: str, *othe
     return P, page, FP8_E4M3 if fp8 else BF16
 
 
-def _scratch(workspace, nbytes: int, dev):
-    """The caller's workspace where it is one (enough bytes, on `dev`), else a new one; None where none is needed."""
+def _scratch(workspace, nbytes: int, q):
+    """The caller's workspace where it is one (enough bytes, on q's device), else a new one; None where none is needed."""
     if nbytes == 0:
         return None
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        if workspace.get_device() != q.get_device() or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {q.device}")
         if workspace.numel() * workspace.element_size() >= nbytes:
-            return workspace.data_ptr()
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            return workspace
+    return q.new_empty(nbytes, dtype=torch.uint8)
 
 
 def latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim: int, scale: float, latent_scale=None,
@@ -563,15 +573,15 @@ def latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim: int, sc
     B, max_pages = block_table.shape
     if seq_ids is None and B != T:
         raise ValueError("block_table must have one row per query (or give seq_ids)")
-    dev, K = q.device, topk_idx.shape[1]
+    K = topk_idx.shape[1]
     out = q.new_empty((T, H, v_dim))
-    lse = torch.empty((T, H), dtype=torch.float32, device=dev) if want_lse else None
+    lse = q.new_empty((T, H), dtype=torch.float32) if want_lse else None
     nws = lib.indexer_latent_attention_topk_workspace_bytes(T, H, E, v_dim, K, dt)
-    ws = _scratch(workspace, nws, dev)
-    st = _on_device(dev, lib.indexer_latent_attention_topk, q.data_ptr(), BF16, latent_cache.data_ptr(),
+    ws = _scratch(workspace, nws, q)
+    st = _on_device(q.get_device(), lib.indexer_latent_attention_topk, q.data_ptr(), BF16, latent_cache.data_ptr(),
                     _ptr(latent_scale), dt, block_table.data_ptr(), max_pages, P, topk_idx.data_ptr(), _ptr(seq_ids),
                     B or 1, T, H, E, v_dim, page, K, scale, out.data_ptr(), _ptr(lse),
-                    ws if ws is None or type(ws) is int else ws.data_ptr(), nws)
+                    _ptr(ws), nws)
     if st:
         _lib.check(st, "indexer_latent_attention_topk")
     return out, lse
@@ -600,16 +610,15 @@ def latent_attention_shared(q, latent_cache, prefix_table, prefix_len: int, bloc
         raise ValueError("prefix_table must be one-dimensional")
     max_pages = block_table.shape[1]
     mcl = max_pages * page if max_context_len is None else int(max_context_len)
-    dev = q.device
     out = q.new_empty((B, H, v_dim))
-    lse = torch.empty((B, H), dtype=torch.float32, device=dev) if want_lse else None
+    lse = q.new_empty((B, H), dtype=torch.float32) if want_lse else None
     nws = lib.indexer_latent_attention_shared_workspace_bytes(B, H, E, v_dim, prefix_len, mcl, dt)
-    ws = _scratch(workspace, nws, dev)
-    st = _on_device(dev, lib.indexer_latent_attention_shared, q.data_ptr(), BF16, latent_cache.data_ptr(),
+    ws = _scratch(workspace, nws, q)
+    st = _on_device(q.get_device(), lib.indexer_latent_attention_shared, q.data_ptr(), BF16, latent_cache.data_ptr(),
                     _ptr(latent_scale), dt, _ptr(prefix_table), 0 if prefix_table is None else prefix_table.shape[0],
                     prefix_len, block_table.data_ptr(), max_pages, P, context_lens.data_ptr(), mcl, B, H, E, v_dim,
                     page, scale, out.data_ptr(), _ptr(lse),
-                    ws if ws is None or type(ws) is int else ws.data_ptr(), nws)
+                    _ptr(ws), nws)
     if st:
         _lib.check(st, "indexer_latent_attention_shared")
     return out, lse
