@@ -50,20 +50,18 @@ template <int KD, int MT, bool FP8>
 struct Lds {
     static constexpr int kMain = FP8 ? kTile / 2 * kPairB : kMainB;                // a tile's value columns,
     static constexpr int kRope = KD > 16 ? (FP8 ? kTile * 64 : kRopeB) : 0;        // and rotary columns
-    static constexpr bool kQInLds = MT == 4 && KD > 16;   // 64 query rows: their rotary columns stay in LDS
     static constexpr int kRopeAt = 2 * kMain;
     static constexpr int kP = kRopeAt + 2 * kRope;
     static constexpr int kRed = kP + MT * 16 * kPRowB;     // [4][16 MT] floats
     static constexpr int kScale = kRed + 4 * 16 * MT * 4;  // [2][64] floats
     static constexpr int kFlag = kScale + (FP8 ? 512 : 0); // [2]
     static constexpr int kUsed = kFlag + 16;
-    // queries: 16 MT padded rows, in the second tile's place or, too large for it, behind both
+    // queries: 16 MT padded rows, in the second tile's place or, too large for
+    // it, behind both; their rotary columns behind them
     static constexpr int kQ = FP8 ? kP : kMain;
-    static constexpr int kQEnd = kQ + MT * 16 * kRowB;
-    // their rotary columns: behind them, or where they stay
-    static constexpr int kQRope = kUsed > kQEnd ? kUsed : kQEnd;
-    static constexpr int kBytes0 = kQRope + (KD > 16 ? MT * 16 * 128 : 0);
-    static constexpr int kBytes = kUsed > kBytes0 ? kUsed : kBytes0;
+    static constexpr int kQRope = kQ + MT * 16 * kRowB;
+    static constexpr int kQEnd = kQRope + (KD > 16 ? MT * 16 * 128 : 0);
+    static constexpr int kBytes = kUsed > kQEnd ? kUsed : kQEnd;
     static_assert(kBytes <= 160 * 1024, "LDS budget");
 };
 
@@ -81,25 +79,20 @@ struct Operand<true> {
     }
 };
 
-// Four waves, a wave per SIMD with all its registers; eight for 64 rows, where
-// one wave could not issue all that stands beside its matrix instructions.
-constexpr int waves_of(int mt) { return mt == 4 ? 8 : 4; }
+constexpr int kThreads = 256;   // four waves, a wave per SIMD with all its registers
 
 template <int KD, int MT, bool TOPK, bool FP8>
-__global__ void __launch_bounds__(64 * waves_of(MT), waves_of(MT) / 4)
+__global__ void __launch_bounds__(kThreads, 1)
 latent_attention_kernel(LatentArgs a, LatentPlan p) {
     extern __shared__ __align__(16) unsigned char smem[];
     using L = Lds<KD, MT, FP8>;
     constexpr int E = 32 * KD;
     constexpr int RB = FP8 ? E : 2 * E;   // bytes of a cached row
-    constexpr int NW = waves_of(MT);
-    constexpr int MQ = MT * 4 / NW;       // 16-row blocks whose scores a wave computes,
-    constexpr int CT = 32 / NW;           // and 16-column blocks of the values
-    constexpr int kAhead = NW == 8 ? 2 : 3;   // operand reads in flight
-    constexpr int KB = kTile / NW;        // rows of a tile that a wave copies
+    constexpr int CT = 8;                 // 16-column blocks of the values that a wave computes
+    constexpr int kAhead = 3;             // operand reads in flight
+    constexpr int KB = kTile / 4;         // rows of a tile that a wave copies
     constexpr int kMainParts = FP8 ? KB / 2 : KB, kParts = kMainParts + (KD == 16 ? 0 : FP8 ? 1 : KB / 8);
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
-    const int kq = wave & 3, rh = wave >> 2;   // 16 keys, and rows 16 MQ rh .., of the scores
     const int n = lane & 15, g = lane >> 4;
     const int total = a.T * a.H;
     LatentKeys<TOPK> keys;
@@ -112,19 +105,15 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     {
         const uint16_t* q = a.q + (int64_t)keys.r0 * E;
 #pragma unroll
-        for (int i = 0; i < 16 * MT / NW; ++i) {
-            const int r = 16 * MT / NW * wave + i;
+        for (int i = 0; i < 4 * MT; ++i) {
+            const int r = 4 * MT * wave + i;
             copy_to_lds(q + (int64_t)min(r, nrows - 1) * E, 16 * lane, lds0 + L::kQ + r * kRowB);
         }
         if constexpr (KD > 16)
-#pragma unroll
-            for (int j = 0; j < (2 * MT + NW - 1) / NW; ++j) {
-                const int r8 = 8 * (wave + NW * j);
-                if (r8 < 16 * MT) {
-                    const int r = r8 + (lane >> 3);
-                    copy_to_lds(q + (int64_t)min(r, nrows - 1) * E + kV + 8 * ((lane & 7) ^ ((r >> 1) & 7)),
-                                lds0 + L::kQRope + r8 * 128);
-                }
+            if (wave < 2 * MT) {
+                const int r = 8 * wave + (lane >> 3);
+                copy_to_lds(q + (int64_t)min(r, nrows - 1) * E + kV + 8 * ((lane & 7) ^ ((r >> 1) & 7)),
+                            lds0 + L::kQRope + 8 * wave * 128);
             }
     }
 
@@ -135,7 +124,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     // ahead.
     auto part_row = [&](int i) -> int {
         if constexpr (FP8)
-            return __shfl(keys.row, i < kMainParts ? kb + 2 * i + (lane >> 5) : 16 * kq + (lane >> 2));
+            return __shfl(keys.row, i < kMainParts ? kb + 2 * i + (lane >> 5) : 16 * wave + (lane >> 2));
         return i < kMainParts ? -1 : __shfl(keys.row, kb + 8 * (i - kMainParts) + (lane >> 3));
     };
     uint64_t src = 0;   // bf16: addresses of the next tile's rows
@@ -149,10 +138,10 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
             if (i < kMainParts) {
                 copy_to_lds(row_address<RB>(a.cache, mine) + 16 * ((lane & 31) ^ (lane >> 5) * 8),
                             lds + (kb / 2 + i) * kPairB);
-            } else if (NW == 4 || wave < 4) {
-                const int r = 16 * kq + (lane >> 2);
+            } else {
+                const int r = 16 * wave + (lane >> 2);
                 copy_to_lds(row_address<RB>(a.cache, mine) + kV + 16 * ((lane & 3) ^ ((r >> 2) & 3)),
-                            rope + 16 * kq * 64);
+                            rope + 16 * wave * 64);
             }
         } else if (i < kMainParts) {
             copy_to_lds(lane_pointer(src, kb + i), 16 * lane, lds + (kb + i) * kRowB);
@@ -193,10 +182,9 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): queries and first tile
     tile_barrier();
     // B operand of 16 rows x 32 columns: row n, columns 8g .. 8g+7 of each 32
-    constexpr int KQ = L::kQInLds ? 16 : KD;
-    v8bf Q[MQ][KQ];
-    auto read_q = [&](int mt, int ks, int ln) {
-        const int n = ln & 15, g = ln >> 4, r = 16 * mt + n;
+    v8bf Q[MT][KD];
+    auto read_q = [&](int mt, int ks) {
+        const int r = 16 * mt + n;
         v8bf q = *reinterpret_cast<const v8bf*>(
             smem + (ks < 16 ? L::kQ + r * kRowB + 16 * g + 64 * ks
                             : L::kQRope + r * 128 + 16 * ((4 * (ks - 16) + g) ^ ((n >> 1) & 7))));
@@ -208,9 +196,9 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         return q;
     };
 #pragma unroll
-    for (int j = 0; j < MQ; ++j)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int ks = 0; ks < KQ; ++ks) Q[j][ks] = read_q(MQ * rh + j, ks, lane);
+        for (int ks = 0; ks < KD; ++ks) Q[mt][ks] = read_q(mt, ks);
     // (never 0: a score of -inf, an entry without a row, has to stay one)
     const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
     tile_barrier();
@@ -220,15 +208,14 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     store_scale(0);
 
     v4f O[CT][MT];
-    float m[MT], l[MQ];   // references of all rows; sums of the rows and keys whose scores are this wave's
+    float m[MT], l[MT];   // the rows' references; their sums over this wave's keys
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         m[mt] = -3.402823466e38f;   // the lowest finite: any score but -inf moves it
+        l[mt] = 0.f;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) O[ct][mt] = v4f{0.f, 0.f, 0.f, 0.f};
     }
-#pragma unroll
-    for (int j = 0; j < MQ; ++j) l[j] = 0.f;
 
     // The lane, made anew for every tile and phase: what follows from it, kept
     // longer, would cost registers that the queries and sums need.
@@ -240,15 +227,15 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         Operand<FP8> k;
         const int n = ln & 15, g = ln >> 4;
         if constexpr (FP8) {
-            const int odd = kq & 1, q = 16 * (kq >> 1) + n;   // row 2q + odd
+            const int odd = wave & 1, q = 16 * (wave >> 1) + n;   // row 2q + odd
             k.x = *reinterpret_cast<const v2i*>(
                 ks < 16 ? tile + q * kPairB + kV * odd + 8 * g + (ks & 4 ? -128 : 128) * odd + 32 * ks
                         : rope + (2 * q + odd) * 64 + 16 * ((2 * (ks - 16) + (g >> 1)) ^ ((n >> 1) & 3)) +
                               8 * (g & 1));
         } else {
             k.x = *reinterpret_cast<const v8bf*>(
-                ks < 16 ? tile + (16 * kq + n) * kRowB + 16 * g + 64 * ks
-                        : rope + (16 * kq + n) * 128 + 16 * ((4 * (ks - 16) + g) ^ ((n >> 1) & 7)));
+                ks < 16 ? tile + (16 * wave + n) * kRowB + 16 * g + 64 * ks
+                        : rope + (16 * wave + n) * 128 + 16 * ((4 * (ks - 16) + g) ^ ((n >> 1) & 7)));
         }
         return k;
     };
@@ -272,14 +259,10 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         }
         return w;
     };
-    // Steps of the scores: the rotary columns, whose queries may have to be read, are the 5th and 7th.
-    auto column = [](int at) constexpr {
-        return KD == 16 || at < 4 ? at : at == 4 ? 16 : at == 5 ? 4 : at == 6 ? 17 : at - 2;
-    };
     Operand<FP8> K[kAhead], W[kAhead];
     v8bf P[MT];
-    v4f S[MQ];
-    float sum[MQ], ks4[4] = {1.f, 1.f, 1.f, 1.f};
+    v4f S[MT];
+    float sum[MT], ks4[4] = {1.f, 1.f, 1.f, 1.f};
     auto read_p = [&](int kk) {
         const int n = ln & 15, g = ln >> 4;
 #pragma unroll
@@ -289,20 +272,18 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     auto write_p = [&]() {
         const int n = ln & 15, g = ln >> 4;
 #pragma unroll
-        for (int j = 0; j < MQ; ++j) {
-            const int mt = MQ * rh + j;
-            const float ref = NW == 4 ? m[j] : rh ? m[MT - MQ + j] : m[j];
+        for (int j = 0; j < MT; ++j) {
             float pr[4];
             sum[j] = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                pr[e] = __builtin_amdgcn_exp2f(fmaf(S[j][e], scale, -ref));
+                pr[e] = __builtin_amdgcn_exp2f(fmaf(S[j][e], scale, -m[j]));
                 sum[j] += pr[e];
                 if constexpr (FP8) pr[e] *= ks4[e];
             }
-            // P[row][key]: 16-byte piece 4(kq/2) + g holds the keys 4g .. 4g+3 of the key blocks
-            // 2(kq/2) and 2(kq/2) + 1
-            *reinterpret_cast<uint2*>(smem + L::kP + (16 * mt + n) * kPRowB + 16 * (4 * (kq >> 1) + g) + 8 * (kq & 1)) =
+            // P[row][key]: 16-byte piece 4(wave/2) + g holds the keys 4g .. 4g+3 of the key blocks
+            // 2(wave/2) and 2(wave/2) + 1
+            *reinterpret_cast<uint2*>(smem + L::kP + (16 * j + n) * kPRowB + 16 * (4 * (wave >> 1) + g) + 8 * (wave & 1)) =
                 uint2{pack_bf16(pr[0], pr[1]), pack_bf16(pr[2], pr[3])};
         }
     };
@@ -310,11 +291,11 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     // The rows' references move to the tile's maxima where those are above them.
     auto rebase = [&]() {
 #pragma unroll
-        for (int j = 0; j < MQ; ++j) {
+        for (int j = 0; j < MT; ++j) {
             float v = highest(j);
             v = fmaxf(v, __shfl_xor(v, 16, kWave));
             v = fmaxf(v, __shfl_xor(v, 32, kWave));
-            if (g == 0) red[kq * 16 * MT + 16 * (MQ * rh + j) + n] = v;
+            if (g == 0) red[wave * 16 * MT + 16 * j + n] = v;
         }
         tile_barrier();
 #pragma unroll
@@ -324,7 +305,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
             for (int w = 0; w < 4; ++w) v = fmaxf(v, red[w * 16 * MT + 16 * mt + n]);
             const float f = __builtin_amdgcn_exp2f(m[mt] - v);
             m[mt] = v;
-            if (NW == 4 || mt / MQ == rh) l[mt % MQ] *= f;
+            l[mt] *= f;
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) O[ct][mt] *= f;
         }
@@ -335,7 +316,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
 
     tile_barrier();
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) K[i] = read_k(0, column(i));
+    for (int i = 0; i < kAhead; ++i) K[i] = read_k(0, i);
     while (t < t1) {
         renew();
         // loads for the tiles behind the next one
@@ -346,52 +327,43 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         const uint64_t next = keys.mask;
         int mine = part_row(0);
 #pragma unroll
-        for (int j = 0; j < MQ; ++j) S[j] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < MT; ++j) S[j] = v4f{0.f, 0.f, 0.f, 0.f};
 
         // ---- scores: S^T, keys 4g .. 4g+3 of this wave's 16, row n of each block; beside
         //      them the next tile's copies (behind the last tile: zeros that nobody reads) ----
-        v8bf qr[MQ];   // rotary columns of the queries that stay in LDS, read two steps ahead
 #pragma unroll
-        for (int st = 0; st < KD; ++st) {
-            const int ks = column(st);
+        for (int ks = 0; ks < KD; ++ks) {
             __builtin_amdgcn_sched_barrier(0);
-            const v8bf k = K[st % kAhead].get();
+            const v8bf k = K[ks % kAhead].get();
 #pragma unroll
-            for (int j = 0; j < MQ; ++j) {
-                const v8bf q = L::kQInLds && ks >= 16 ? qr[j] : Q[j][ks < KQ ? ks : 0];
-                S[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q, S[j], 0, 0, 0);
-            }
-            if (st + kAhead < KD) K[st % kAhead] = read_k(buf, column(st + kAhead));
-            if (L::kQInLds && (st == 2 || st == 4))
-#pragma unroll
-                for (int j = 0; j < MQ; ++j) qr[j] = read_q(MQ * rh + j, 15 + st / 2, ln);
-            if ((st + 1) * kParts / KD > st * kParts / KD) {
-                const int i = st * kParts / KD, row = mine;
+            for (int j = 0; j < MT; ++j) S[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, Q[j][ks], S[j], 0, 0, 0);
+            if (ks + kAhead < KD) K[ks % kAhead] = read_k(buf, ks + kAhead);
+            if ((ks + 1) * kParts / KD > ks * kParts / KD) {
+                const int i = ks * kParts / KD, row = mine;
                 if (i + 1 < kParts) mine = part_row(i + 1);
                 stage(buf ^ 1, i, row);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
         // ---- softmax against the rows' references ----
-        if (NW == 8) renew();
         if constexpr (FP8) {
-            const v4f s4 = *reinterpret_cast<const v4f*>(smem + L::kScale + 256 * buf + 4 * (16 * kq + 4 * (ln >> 4)));
+            const v4f s4 = *reinterpret_cast<const v4f*>(smem + L::kScale + 256 * buf + 4 * (16 * wave + 4 * (ln >> 4)));
 #pragma unroll
             for (int e = 0; e < 4; ++e) ks4[e] = s4[e];
 #pragma unroll
-            for (int j = 0; j < MQ; ++j) S[j] *= s4;
+            for (int j = 0; j < MT; ++j) S[j] *= s4;
         }
         if (here != ~0ull) {
-            const uint32_t mine = FP8 ? (uint32_t)(here >> (32 * (kq >> 1) + (kq & 1))) >> (8 * (ln >> 4))
-                                      : (uint32_t)(here >> (16 * kq)) >> (4 * (ln >> 4));
+            const uint32_t mine = FP8 ? (uint32_t)(here >> (32 * (wave >> 1) + (wave & 1))) >> (8 * (ln >> 4))
+                                      : (uint32_t)(here >> (16 * wave)) >> (4 * (ln >> 4));
 #pragma unroll
-            for (int j = 0; j < MQ; ++j)
+            for (int j = 0; j < MT; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) S[j][e] = mine >> (FP8 ? 2 * e : e) & 1 ? S[j][e] : -__builtin_inff();
         }
         bool rise = false;
 #pragma unroll
-        for (int j = 0; j < MQ; ++j) rise |= highest(j) > (NW == 4 ? m[j] : rh ? m[MT - MQ + j] : m[j]) + kSlack;
+        for (int j = 0; j < MT; ++j) rise |= highest(j) > m[j] + kSlack;
         write_p();
         if (wave_ballot(rise) && lane == 0) flag[buf] = 1;
         if (threadIdx.x == 0) flag[buf ^ 1] = 0;
@@ -402,11 +374,10 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         read_p(0);
         if (uniform(risen)) rebase();
 #pragma unroll
-        for (int j = 0; j < MQ; ++j) l[j] += sum[j];
+        for (int j = 0; j < MT; ++j) l[j] += sum[j];
 
         // ---- O^T += V^T P^T; beside it the rows of the tile behind the next one, and the
         //      hand-over: every wave has read its last operands, and the next tile is there ----
-        if (NW == 8) renew();
 #pragma unroll
         for (int i = 0; i < 2 * CT; ++i) {
             __builtin_amdgcn_sched_barrier(0);
@@ -425,7 +396,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
                 store_scale(buf ^ 1);
                 tile_barrier();
             }
-            if (i >= 2 * CT - kAhead) K[i - (2 * CT - kAhead)] = read_k(buf ^ 1, column(i - (2 * CT - kAhead)));
+            if (i >= 2 * CT - kAhead) K[i - (2 * CT - kAhead)] = read_k(buf ^ 1, i - (2 * CT - kAhead));
         }
         __builtin_amdgcn_sched_barrier(0);
         here = next;
@@ -443,11 +414,11 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     __builtin_amdgcn_s_waitcnt(0x0F70);  // no copy may still be in flight
     tile_barrier();
 #pragma unroll
-    for (int j = 0; j < MQ; ++j) {
+    for (int j = 0; j < MT; ++j) {
         float x = l[j];
         x += __shfl_xor(x, 16, kWave);
         x += __shfl_xor(x, 32, kWave);
-        if (g == 0) red[kq * 16 * MT + 16 * (MQ * rh + j) + n] = x;
+        if (g == 0) red[wave * 16 * MT + 16 * j + n] = x;
     }
     tile_barrier();
 #pragma unroll
@@ -625,7 +596,7 @@ hipError_t run(const LatentArgs& a, const LatentPlan& p, hipStream_t stream) {
     const hipError_t e = set_lds_limit(once, (const void*)latent_attention_kernel<KD, MT, TOPK, FP8>, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((latent_attention_kernel<KD, MT, TOPK, FP8>), dim3((unsigned)(p.n_prefix + p.n_own)),
-                       dim3(64 * waves_of(MT)), lds, stream, a, p);
+                       dim3(kThreads), lds, stream, a, p);
     return hipGetLastError();
 }
 
@@ -637,7 +608,6 @@ hipError_t run(const LatentArgs& a, const LatentPlan& p, bool fp8, hipStream_t s
 
 template <int KD>
 hipError_t run(const LatentArgs& a, const LatentPlan& p, bool fp8, hipStream_t stream) {
-    if (p.rows == 64) return a.idx ? run<KD, 4, true, true>(a, p, stream) : run<KD, 4, false, true>(a, p, stream);
     return p.rows == 16 ? run<KD, 1>(a, p, fp8, stream) : run<KD, 2>(a, p, fp8, stream);
 }
 
@@ -655,7 +625,7 @@ hipError_t launch_latent_attention(const LatentArgs& a, bool fp8, hipStream_t st
     LatentPlan p = make_plan(a.T, a.H, a.idx != nullptr, a.K, a.prefix_len, a.max_ctx, fp8);
     p.part_o = reinterpret_cast<float*>(a.workspace);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)p.slots * a.T * a.H * kV);
-    hipError_t e = p.rows == 128 || (p.rows == 64 && !fp8) ? launch_latent_rows(a, p, fp8, stream) : a.E == 576 ? run<18>(a, p, fp8, stream) : run<16>(a, p, fp8, stream);
+    hipError_t e = p.rows >= 64 ? launch_latent_rows(a, p, fp8, stream) : a.E == 576 ? run<18>(a, p, fp8, stream) : run<16>(a, p, fp8, stream);
     if (e != hipSuccess || p.slots == 1) return e;
     hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)(a.T * a.H)), dim3(kJoinThreads), 0, stream, a, p);
     return hipGetLastError();

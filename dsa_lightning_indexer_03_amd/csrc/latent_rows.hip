@@ -15,10 +15,11 @@
 // rows passes it by 2^kSlack.  With 64 rows the waves form two groups of four,
 // each with half of every tile's keys, joined through LDS at the end.
 //
-// fp8 rows (blocks of 128) are staged as codes two tiles ahead.  Beside the
-// products of one half tile, 32 keys, the waves widen the next half to bf16
-// in the other of two buffers, once for all rows: in registers every wave
-// would widen every operand.  The rows' scales multiply the scores and P.
+// fp8 rows are staged as codes two tiles ahead.  Beside the products of one half
+// tile, 32 keys, the next half is widened to bf16 in the other of two buffers,
+// once for all rows: in registers every wave would widen every operand.  The
+// rows' scales multiply the scores and P.  With 64 rows four waves compute and
+// the other four copy and widen.
 #include "device_once.h"
 #include "latent_common.h"
 
@@ -44,16 +45,17 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int E = 32 * KD;
     constexpr int RB = FP8 ? E : 2 * E;
-    static_assert(!FP8 || KG == 1, "half tiles are not divided further");
     constexpr int RG = 8 / KG;            // row groups of 16
-    constexpr int kMainParts = FP8 ? 4 : 8, kParts = kMainParts + (KD > 16);  // copies of a tile that a wave makes
+    constexpr bool kMovers = FP8 && KG == 2;    // the second four waves move data for the first
+    constexpr int kMainParts = FP8 && KG == 1 ? 4 : 8, kParts = kMainParts + (KD > 16);  // copies of a tile that a wave makes
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int n = lane & 15, g = lane >> 4;
     const int rg = wave % RG, kg = wave / RG;
     LatentKeys<TOPK> keys;
     if (!keys.start(a, p)) return;
     const int nrows = keys.nrows, t1 = keys.t1;
-    const bool active = 16 * rg < nrows;
+    const bool active = 16 * rg < nrows && !(kMovers && kg == 1);
+    const bool mover = !kMovers || kg == 1;
 
     // ---- queries: B operand of 16 rows x 32 columns ----
     v8bf Q[KD];
@@ -63,9 +65,9 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
         for (int ks = 0; ks < KD; ++ks) Q[ks] = *reinterpret_cast<const v8bf*>(qp + 32 * ks);
     }
 
-    // ---- copies: rows 8w .. 8w+7 of a tile; fp8: their codes two rows at a time, the
-    //      rotary columns of 16 rows by each of four waves, the scales by another ----
-    const int kb = 8 * wave;
+    // ---- copies: rows kb .. of a tile; fp8: their codes two rows at a time, the rotary
+    //      columns of 16 rows by each of four waves, the scales by one ----
+    const int kb = kMovers ? 16 * (wave & 3) : 8 * wave;
     const uint32_t lds0 = lds_address(smem);
     int rope_row = -1;   // bf16: the row whose rotary columns this lane copies a piece of
     auto spread = [&]() {
@@ -74,12 +76,12 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
     auto stage = [&](int buf, int i) {
         if constexpr (FP8) {
             const uint32_t lds = lds0 + kCodesAt + buf * kCodesB;
-            if (i < 4) {
+            if (i < kMainParts) {
                 const int mine = __shfl(keys.row, kb + 2 * i + (lane >> 5));
                 copy_to_lds(row_address<RB>(a.cache, mine) + 16 * (lane & 31), lds + (kb + 2 * i) * kV);
-            } else if (wave < 4) {
-                const int mine = __shfl(keys.row, 16 * wave + (lane >> 2));
-                copy_to_lds(row_address<RB>(a.cache, mine) + kV + 16 * (lane & 3), lds + kTile * kV + 16 * wave * 64);
+            } else if (kMovers || wave < 4) {
+                const int r = 16 * (wave & 3), mine = __shfl(keys.row, r + (lane >> 2));
+                copy_to_lds(row_address<RB>(a.cache, mine) + kV + 16 * (lane & 3), lds + kTile * kV + r * 64);
             }
         } else {
             const uint32_t lds = lds0 + buf * kTileB;
@@ -116,9 +118,11 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
     };
     uint64_t here = keys.mask;
     spread();
+    if (mover) {
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) stage(0, i);
-    stage_scales(0);
+        for (int i = 0; i < kParts; ++i) stage(0, i);
+        stage_scales(0);
+    }
     int buf = 0;
     advance();
 
@@ -238,19 +242,19 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    // fp8: rows 4w .. 4w+3 of half hb of the codes in buffer `from`, to bf16 in half buffer hb.
+    // fp8: rows r4 .. r4+3 of half hb of the codes in buffer `from`, to bf16 in half buffer hb.
     // Steps 0 .. 17, a row at a time: read, and written three steps later.
     uint2 codes{0, 0}, rope_codes{0, 0};
-    auto widen = [&](int from, int hb, int step) {
-        const int r = 32 * hb + 4 * wave;
+    auto widen = [&](int from, int hb, int r4, int step) {
+        const int r = 32 * hb + r4;
         const unsigned char* in = smem + kCodesAt + from * kCodesB;
         unsigned char* out = smem + hb * kHalfB;
         if (step < 16 && step % 4 == 0)
             codes = *reinterpret_cast<const uint2*>(in + (r + step / 4) * kV + 8 * ln);
         if (step < 16 && step % 4 == 3)
-            *reinterpret_cast<v4i*>(out + (4 * wave + step / 4) * kRowB + 16 * ln) = widen8(codes);
+            *reinterpret_cast<v4i*>(out + (r4 + step / 4) * kRowB + 16 * ln) = widen8(codes);
         if constexpr (KD > 16) {   // (both halves of the wave the same)
-            const int row = 4 * wave + (ln >> 3 & 3);
+            const int row = r4 + (ln >> 3 & 3);
             if (step == 14)
                 rope_codes = *reinterpret_cast<const uint2*>(in + kTile * kV + (32 * hb + row) * 64 + 8 * (ln & 7));
             if (step == 17)
@@ -258,16 +262,23 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
                     widen8(rope_codes);
         }
     };
+    auto widen_all = [&](int from, int hb) {   // this wave's rows, at once
+#pragma unroll
+        for (int j = 0; j < (kMovers ? 2 : 1); ++j)
+#pragma unroll
+            for (int step = 0; step < 18; ++step) widen(from, hb, kMovers ? 8 * (wave & 3) + 4 * j : 4 * wave, step);
+    };
 
     int at = 0;   // fp8: the place of this tile's scales
     if constexpr (FP8) {
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the first tile
         tile_barrier();
+        if (mover) {
+            widen_all(0, 0);
 #pragma unroll
-        for (int i = 0; i < 18; ++i) widen(0, 0, i);
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) stage(1, i);
-        stage_scales(1);
+            for (int i = 0; i < kParts; ++i) stage(1, i);
+            stage_scales(1);
+        }
     }
 
     while (t < t1) {
@@ -293,27 +304,32 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
         };
         if constexpr (FP8) {
             const unsigned char* by = smem + kScaleAt + at * kTile * 4;
-            auto first = [&](int ks) { widen(buf, 1, ks); };
+            auto first = [&](int ks) {
+                if constexpr (!kMovers) widen(buf, 1, 4 * wave, ks);
+            };
             if (active) {
                 half(smem, smem + 32 * kRowB, (uint32_t)here, by, first, resolve);
             } else {
-#pragma unroll
-                for (int ks = 0; ks < 18; ++ks) first(ks);
+                if (mover) widen_all(buf, 1);
                 resolve();
             }
             step();
             __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the next tile
             tile_barrier();
             auto second = [&](int ks) {   // behind the last tile: zeros
-                widen(buf ^ 1, 0, ks);
-                if (ks % 4 == 1 && ks / 4 < kParts) stage(buf, ks / 4);
-                if (ks == 2) stage_scales((at + 2) & 3);
+                if constexpr (!kMovers) {
+                    widen(buf ^ 1, 0, 4 * wave, ks);
+                    if (ks % 4 == 1 && ks / 4 < kParts) stage(buf, ks / 4);
+                    if (ks == 2) stage_scales((at + 2) & 3);
+                }
             };
             if (active) {
                 half(smem + kHalfB, smem + kHalfB + 32 * kRowB, (uint32_t)(here >> 32), by + 128, second, [] {});
-            } else {
+            } else if (mover) {
 #pragma unroll
-                for (int ks = 0; ks < 18; ++ks) second(ks);
+                for (int i = 0; i < kParts; ++i) stage(buf, i);
+                stage_scales((at + 2) & 3);
+                widen_all(buf ^ 1, 0);
             }
             at = (at + 1) & 3;
         } else {
@@ -346,7 +362,9 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
     __builtin_amdgcn_s_waitcnt(0x0F70);  // no copy may still be in flight
     l += __shfl_xor(l, 16, kWave);
     l += __shfl_xor(l, 32, kWave);
-    if constexpr (KG == 2) {
+    if constexpr (kMovers) {
+        if (kg == 1) return;
+    } else if constexpr (KG == 2) {
         v4f* there = reinterpret_cast<v4f*>(smem) + rg * 32 * 64 + lane;
         float2* ml = reinterpret_cast<float2*>(smem + 4 * 32 * 64 * 16) + rg * 64 + lane;
         tile_barrier();
@@ -398,15 +416,15 @@ hipError_t run(const LatentArgs& a, const LatentPlan& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int KD, int KG, bool FP8>
-hipError_t run(const LatentArgs& a, const LatentPlan& p, hipStream_t stream) {
-    return a.idx ? run<KD, KG, true, FP8>(a, p, stream) : run<KD, KG, false, FP8>(a, p, stream);
+template <int KD, int KG>
+hipError_t run(const LatentArgs& a, const LatentPlan& p, bool fp8, hipStream_t stream) {
+    if (a.idx) return fp8 ? run<KD, KG, true, true>(a, p, stream) : run<KD, KG, true, false>(a, p, stream);
+    return fp8 ? run<KD, KG, false, true>(a, p, stream) : run<KD, KG, false, false>(a, p, stream);
 }
 
 template <int KD>
 hipError_t run(const LatentArgs& a, const LatentPlan& p, bool fp8, hipStream_t stream) {
-    if (fp8) return run<KD, 1, true>(a, p, stream);
-    return p.rows == 64 ? run<KD, 2, false>(a, p, stream) : run<KD, 1, false>(a, p, stream);
+    return p.rows == 64 ? run<KD, 2>(a, p, fp8, stream) : run<KD, 1>(a, p, fp8, stream);
 }
 
 }  // namespace
