@@ -34,6 +34,7 @@ namespace dsaidx {
 namespace {
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 2048;
 
 // LDS: two tiles, P (its rows padded like a bf16 tile's), the exchange of
 // maxima and sums, the rows' fp8 scales, flags.  The queries pass through the
@@ -449,16 +450,20 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     }
 }
 
-// Joins the slots' partial results of a row: one workgroup per row, a wave
-// takes every fourth slot (8 columns a lane), the waves' sums meet in LDS.
-// Slots are at most 64, one per lane for the weights.  Bound by reading the
-// partial sums; with few rows by latency, so a wave has four slots in flight.
+// Joins the slots' partial results, W waves to a row: each takes every W-th
+// slot, 8 columns a lane, and the waves' sums meet in LDS.  Slots are at most
+// 64, one per lane for the weights.  Bound by reading the partial sums; with
+// few rows by latency, so a wave has four slots in flight.  8192 rows of 4
+// slots (67 MB): 13.0 us with one wave a row, 19.7 with four; 16 rows of 32
+// slots: 6.6 and 3.9; 1320 rows of 13 slots (36 MB): 7.5 and 6.9.
+template <int W>
 __global__ void __launch_bounds__(kJoinThreads)
 latent_join_kernel(LatentArgs a, LatentPlan p) {
-    __shared__ float sums[4][kV];
+    __shared__ float sums[W == 1 ? 1 : 4][kV];
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int total = a.T * a.H;
-    const int64_t r = blockIdx.x;
+    const int64_t r = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+    if (W == 1 && r >= total) return;
     const float2 ml = lane < p.slots ? p.part_ml[(int64_t)lane * total + r] : float2{0.f, 0.f};
     const bool some = ml.y != 0.f;
     float top = some ? ml.x : -__builtin_inff();
@@ -474,13 +479,13 @@ latent_join_kernel(LatentArgs a, LatentPlan p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = 0.f;
     if (filled)
-        for (int s0 = wave; s0 < p.slots; s0 += 16) {
+        for (int s0 = W == 1 ? 0 : wave; s0 < p.slots; s0 += 4 * W) {
             v4f x[4], y[4];
             float f[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {   // a slot that holds nothing was not written: another's place, weight 0
-                const int s = s0 + 4 * u < p.slots ? s0 + 4 * u : any;
-                const bool ok = s0 + 4 * u < p.slots && filled >> s & 1;
+                const int s = s0 + W * u < p.slots ? s0 + W * u : any;
+                const bool ok = s0 + W * u < p.slots && filled >> s & 1;
                 f[u] = ok ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), s)) : 0.f;
                 const float* at = p.part_o + ((int64_t)(ok ? s : any) * total + r) * kV + 8 * lane;
                 x[u] = *reinterpret_cast<const v4f*>(at);
@@ -494,17 +499,25 @@ latent_join_kernel(LatentArgs a, LatentPlan p) {
                     o[4 + j] += f[u] * y[u][j];
                 }
         }
-    *reinterpret_cast<v4f*>(&sums[wave][8 * lane]) = v4f{o[0], o[1], o[2], o[3]};
-    *reinterpret_cast<v4f*>(&sums[wave][8 * lane + 4]) = v4f{o[4], o[5], o[6], o[7]};
-    __syncthreads();
     const float inv = l != 0.f ? 1.f / l : 0.f;
-    const int c = 2 * threadIdx.x;
-    v2bf out;
+    if constexpr (W == 1) {
+        v4i out;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        out[j] = (__bf16)(((sums[0][c + j] + sums[1][c + j]) + (sums[2][c + j] + sums[3][c + j])) * inv);
-    *reinterpret_cast<v2bf*>(a.out + r * kV + c) = out;
-    if (a.lse && threadIdx.x == 0) a.lse[r] = l != 0.f ? (top + log2f(l)) * 0.693147180559945f : -__builtin_inff();
+        for (int j = 0; j < 4; ++j) out[j] = (int)pack_bf16(o[2 * j] * inv, o[2 * j + 1] * inv);
+        *reinterpret_cast<v4i*>(a.out + r * kV + 8 * lane) = out;
+        if (a.lse && lane == 0) a.lse[r] = l != 0.f ? (top + log2f(l)) * 0.693147180559945f : -__builtin_inff();
+    } else {
+        *reinterpret_cast<v4f*>(&sums[wave][8 * lane]) = v4f{o[0], o[1], o[2], o[3]};
+        *reinterpret_cast<v4f*>(&sums[wave][8 * lane + 4]) = v4f{o[4], o[5], o[6], o[7]};
+        __syncthreads();
+        const int c = 2 * threadIdx.x;
+        v2bf out;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            out[j] = (__bf16)(((sums[0][c + j] + sums[1][c + j]) + (sums[2][c + j] + sums[3][c + j])) * inv);
+        *reinterpret_cast<v2bf*>(a.out + r * kV + c) = out;
+        if (a.lse && threadIdx.x == 0) a.lse[r] = l != 0.f ? (top + log2f(l)) * 0.693147180559945f : -__builtin_inff();
+    }
 }
 
 constexpr int kCUs = 256;
@@ -627,7 +640,11 @@ hipError_t launch_latent_attention(const LatentArgs& a, bool fp8, hipStream_t st
     p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)p.slots * a.T * a.H * kV);
     hipError_t e = p.rows >= 64 ? launch_latent_rows(a, p, fp8, stream) : a.E == 576 ? run<18>(a, p, fp8, stream) : run<16>(a, p, fp8, stream);
     if (e != hipSuccess || p.slots == 1) return e;
-    hipLaunchKernelGGL(latent_join_kernel, dim3((unsigned)(a.T * a.H)), dim3(kJoinThreads), 0, stream, a, p);
+    const int rows = a.T * a.H;
+    if (rows >= kJoinRows)
+        hipLaunchKernelGGL(latent_join_kernel<1>, dim3((unsigned)ceil_div(rows, 4)), dim3(kJoinThreads), 0, stream, a, p);
+    else
+        hipLaunchKernelGGL(latent_join_kernel<4>, dim3((unsigned)rows), dim3(kJoinThreads), 0, stream, a, p);
     return hipGetLastError();
 }
 

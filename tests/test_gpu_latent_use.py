@@ -8,7 +8,7 @@ import torch
 import dsa_lightning_indexer_03_amd as dsa
 from dsa_lightning_indexer_03_amd import _lib
 from gpu_util import say
-from latent_util import V, bf16, check_attention
+from latent_util import V, bf16, check_attention, expect_topk, make_pool
 from oracle.latent import attend, slots
 
 pytestmark = pytest.mark.gpu
@@ -131,6 +131,24 @@ def test_the_same_call_twice(heads):
                  dsa.latent_attention_shared(**shared_args(x, n), v_dim=V, scale=SCALE, want_lse=True)]
         for a, b in zip(first, again):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("T,heads,K", [(23, 97, 400), (11, 100, 129), (40, 55, 300)])
+def test_many_rows_in_several_parts(T, heads, K, kind):
+    """Enough rows that a wave joins each, in parts that some rows do not reach."""
+    rng = np.random.default_rng(T)
+    mpp, pages = 4, 4 * T
+    table = rng.permutation(pages).reshape(T, mpp)
+    idx = rng.integers(-1, mpp * 64, (T, K))
+    idx[1], idx[2, 64:], idx[3, : K - 2] = -1, -1, -1
+    cache, scale, rows = make_pool(rng, pages, E, kind)
+    q, qv = bf16(1.5 * rng.normal(size=(T, heads, E)))
+    say(f"{T} queries of {heads} heads, {K} selected, {kind}")
+    out, lse = dsa.latent_attention_topk(q.cuda(), cache, ints(table), ints(idx), V, SCALE, latent_scale=scale,
+                                         want_lse=True)
+    torch.cuda.synchronize()
+    check_attention(out, lse, expect_topk(qv, rows, table, idx, np.arange(T), SCALE, pages), "many rows")
 
 
 def test_two_streams():
