@@ -18,6 +18,11 @@
 // stand before the checks, so that they do not wait for the chain position ->
 // page -> place; a token without a place takes position 0's angles, if it has
 // none of its own, and stores nothing.
+//
+// Bound by HBM with many tokens: 32768 tokens of 576 + 128 columns, bf16 rows
+// (92 MB with the angles): 21 us, 4.3 TB/s (a 1 GiB copy: 5.2); two tokens a
+// wave in full rounds of lanes took 24.  fp8 rows (68 MB): 24 us, bound by the
+// exact quotients.  One token: 3 us, the launch.
 #include "common.h"
 #include "fp8_row.h"
 #include "kernels.h"

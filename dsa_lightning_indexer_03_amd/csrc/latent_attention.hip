@@ -9,10 +9,11 @@
 // (shared).  "Study MLA Indexer", the data-flow diagram's last step; "Lightning
 // Indexer explained", section 1.
 //
-// One workgroup of four waves takes a block of up to 16*MT query rows (a
-// query's heads, or the stacked heads of several queries for the shared
-// prefix) and a run of 64-key tiles.  A tile is staged once in LDS and serves
-// both products:
+// Here: blocks of 16 or 32 query rows (larger ones: latent_rows.hip), the
+// choice of block and split, and the join.  One workgroup of four waves takes
+// a block (a query's heads, or the stacked heads of several queries for the
+// shared prefix) and a run of 64-key tiles.  A tile is staged once in LDS and
+// serves both products:
 //   S^T (16 keys x rows) = K Q^T: wave w has keys 16w .. 16w+15, the queries
 //     sit in its registers;
 //   O^T (128 columns x rows) += V^T P^T: wave w has columns 128w .. 128w+127,
@@ -20,13 +21,20 @@
 //     are read transposed from the same tile.
 // Both leave a lane with one query row (lane % 16 of each 16-row block), so
 // the softmax's factors are per lane.  The exponent's reference m is common to
-// the four waves and only moves when a score exceeds it by more than
-// 2^kSlack (base 2): a flag in LDS, read behind the barrier that the exchange of P needs
+// the four waves and only moves when a score exceeds it by more than kSlack
+// (base 2): a flag in LDS, read behind the barrier that the exchange of P needs
 // anyway, sends all waves through a second pass that takes the tile's maximum,
-// rescales and rewrites P.  Sums are fp32; P is rounded to bf16 (the second
-// product's operand; its sum is taken before the rounding).
+// rescales and rewrites P.  Sums are fp32; P is rounded to bf16, the second
+// product's operand (its sum is taken before the rounding; the output is bf16
+// too).
 // When the rows alone do not fill the GPU the key tiles are split over
 // workgroups, whose fp32 partial sums a second kernel joins by their maxima.
+//
+// With few rows a tile is bound by its bytes: 64 queries of 16 heads, 2048 rows
+// of 1152 bytes each, take 33 us and the join 3, 4.5 TB/s of distinct rows
+// (a 1 GiB copy reaches 5.2 read and written); from MALL the same tiles take
+// 1.7 us instead of 3.6.  With one query it is latency: 32 workgroups of one
+// tile take 8 us, four dependent loads and the launch, and joining them 4.
 #include "device_once.h"
 #include "latent_common.h"
 
@@ -34,7 +42,7 @@ namespace dsaidx {
 namespace {
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 2048;
+constexpr int kJoinRows = 2048;   // from here on a wave joins a row
 
 // LDS: two tiles, P (its rows padded like a bf16 tile's), the exchange of
 // maxima and sums, the rows' fp8 scales, flags.  The queries pass through the
@@ -524,17 +532,25 @@ constexpr int kCUs = 256;
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 int pad8(int n) { return (n + 7) / 8 * 8; }
 
-// Query rows of a workgroup: the smallest block that holds all of them, at most 64.
+// Query rows of a workgroup: the smallest block that holds all of them, at
+// most 128.  1000 queries, 2048 selected rows of 576 (bf16 / fp8), in us:
+//   32 heads: blocks of 16: 422 / 427, of 32: 241 / 260, of 64: 272 / 344
+//   64 heads: of 32: 493 / 516, of 64: 319 / 397, of 128: 377 / 457
+//   128 heads: of 64: 622 / 787, of 128: 542 / 589
 int block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
+// Time of a 64-key tile in a block of that many rows, on a busy GPU and not
+// bound by memory.
 double tile_us(int rows) { return rows == 16 ? 1.4 : rows == 32 ? 1.9 : rows == 64 ? 2.6 : 4.2; }
 
 // Splits of the key tiles that finish first, in us (p.rows and the tile counts
-// are given).  A workgroup takes 5 and its tiles: 1 to 2.7 each by its rows,
-// or what streaming 74 KB to every busy CU takes; the GPU runs one per CU,
-// prefix parts first; joining takes 4 and reads and writes every slot's sums.
-// A run of own tiles is as long as one of the prefix.
-double split(int64_t blocks_p, int tiles_p, int64_t blocks_o, int tiles_o, int64_t rows, int H, bool fp8, LatentPlan& p) {
+// are given).  A workgroup takes 5 and its tiles, own ones longer the more CUs
+// stream 74 KB (fp8: 37) a tile of their own; the GPU runs one workgroup per
+// CU, prefix parts first; joining takes 4 and reads and writes every slot's
+// sums.  A run of own tiles takes as long as one of the prefix.  64 queries of
+// 16 heads, 2048 selected: 2 splits 45.6 us, 4 (chosen) 36.
+double split(int64_t blocks_p, int tiles_p, int64_t blocks_o, int tiles_o, int64_t rows, int H, bool fp8,
+             LatentPlan& p) {
     static const int kSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32};
     const double tile = tile_us(p.rows), tile_o = tile_us(block_rows(H < p.rows ? H : p.rows));
     const int tiles = tiles_p > 0 ? tiles_p : tiles_o;
