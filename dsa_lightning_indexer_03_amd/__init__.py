@@ -27,7 +27,8 @@ F32, BF16, FP8_E4M3 = 0, 1, 2
 __all__ = ["indexer_prefill", "indexer_prefill_noalloc", "indexer_decode_paged", "topk_select", "kcache_append", "topk_gather",
            "topk_gather_layers",
            "prefill_chunk_paged", "prefill_chunk_varlen",
-           "cache_append_rope", "latent_attention_topk", "latent_attention_shared", "dtype_code", "F32", "BF16", "FP8_E4M3"]
+           "cache_append_rope", "latent_attention_topk", "latent_attention_shared", "latent_topk_workspace_bytes",
+           "latent_shared_workspace_bytes", "dtype_code", "F32", "BF16", "FP8_E4M3"]
 
 
 def dtype_code(t: torch.Tensor) -> int:
@@ -550,6 +551,16 @@ def _scratch(workspace, nbytes: int, q):
     return q.new_empty(nbytes, dtype=torch.uint8)
 
 
+def latent_topk_workspace_bytes(T: int, H: int, E: int, v_dim: int, topk: int, fp8: bool = False) -> int:
+    return _lib.load().indexer_latent_attention_topk_workspace_bytes(T, H, E, v_dim, topk, FP8_E4M3 if fp8 else BF16)
+
+
+def latent_shared_workspace_bytes(B: int, H: int, E: int, v_dim: int, prefix_len: int, max_context_len: int,
+                                  fp8: bool = False) -> int:
+    return _lib.load().indexer_latent_attention_shared_workspace_bytes(B, H, E, v_dim, prefix_len, max_context_len,
+                                                                       FP8_E4M3 if fp8 else BF16)
+
+
 def latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim: int, scale: float, latent_scale=None,
                           seq_ids=None, want_lse: bool = False, workspace: torch.Tensor | None = None):
     """Attention of every head over the latent rows at each query's selected
@@ -560,6 +571,8 @@ def latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim: int, sc
     its value.  block_table [B,max_pages] int32; topk_idx [T,K] int32 positions
     (-1, or outside the table: no row); seq_ids [T] int32 gives each query's
     row of the table (outside [0, B): no rows), None: query t uses row t.
+    ``workspace``: the caller's scratch of latent_topk_workspace_bytes, not
+    shared by calls in flight (default: a new one each call).
     Returns (out bf16 [T,H,v_dim], lse fp32 [T,H] or None); a query without a
     row gives zeros and -inf."""
     lib = _lib.load()
@@ -598,6 +611,8 @@ def latent_attention_shared(q, latent_cache, prefix_table, prefix_len: int, bloc
     positions (None when that is 0); block_table [B,max_pages] int32 and
     context_lens [B] int32: the sequences' own pages and lengths.
     ``max_context_len`` bounds context_lens (default: max_pages * page).
+    ``workspace``: the caller's scratch of latent_shared_workspace_bytes, not
+    shared by calls in flight (default: a new one each call).
     Returns (out bf16 [B,H,v_dim], lse fp32 [B,H] or None); a query without a
     position gives zeros and -inf."""
     lib = _lib.load()
@@ -610,6 +625,8 @@ def latent_attention_shared(q, latent_cache, prefix_table, prefix_len: int, bloc
         raise ValueError("prefix_table must be one-dimensional")
     max_pages = block_table.shape[1]
     mcl = max_pages * page if max_context_len is None else int(max_context_len)
+    if prefix_len >> 31 or mcl >> 31:
+        raise ValueError("prefix_len and max_context_len must be in [0, 2^31)")
     out = q.new_empty((B, H, v_dim))
     lse = q.new_empty((B, H), dtype=torch.float32) if want_lse else None
     nws = lib.indexer_latent_attention_shared_workspace_bytes(B, H, E, v_dim, prefix_len, mcl, dt)

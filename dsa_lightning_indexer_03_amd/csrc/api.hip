@@ -242,6 +242,7 @@ namespace {
 
 constexpr int kMaxLatentTokens = 1 << 27;  // longest list of keys of one query
 constexpr int kMaxLatentHeads = 128;
+constexpr float kLog2E = 1.44269504088896341f;
 
 // The checks that both latent-attention entry points share; 0 when all pass.
 dsaidx_status latent_check(const void* q, int q_dtype, const void* latent_cache, const float* latent_scale,
@@ -265,8 +266,10 @@ dsaidx_status latent_check(const void* q, int q_dtype, const void* latent_cache,
     if ((int64_t)max_pages_per_seq * page_size > kMaxLatentTokens || num_pages > kMaxLatentTokens / 64)
         return fail(DSAIDX_ERR_UNSUPPORTED, "max_pages_per_seq=%d num_pages=%d (tables and pools of at most %d tokens)",
                     max_pages_per_seq, num_pages, kMaxLatentTokens);
-    if ((int64_t)T * H > (1 << 24)) return fail(DSAIDX_ERR_UNSUPPORTED, "rows * H = %lld > 2^24", (long long)T * H);
-    if (!(scale - scale == 0.f)) return fail(DSAIDX_ERR_SHAPE, "scale must be finite");
+    // (a launch holds less than 2^32 threads, and a query takes a workgroup)
+    if ((int64_t)T * H > (1 << 23)) return fail(DSAIDX_ERR_UNSUPPORTED, "rows * H = %lld > 2^23", (long long)T * H);
+    const float in_base_2 = scale * kLog2E;
+    if (!(in_base_2 - in_base_2 == 0.f)) return fail(DSAIDX_ERR_SHAPE, "scale * log2(e) must be finite");
     if (T == 0) return DSAIDX_OK;
     if (!q) return fail(DSAIDX_ERR_NULL, "q is NULL");
     if (!latent_cache) return fail(DSAIDX_ERR_NULL, "latent_cache is NULL");
@@ -283,7 +286,7 @@ dsaidx_status latent_run(dsaidx::LatentArgs& a, int latent_dtype, float scale, v
         return fail(DSAIDX_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
     if (need > 0 && !aligned16(workspace)) return fail(DSAIDX_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
     a.workspace = workspace;
-    a.scale_log2 = scale * 1.44269504088896341f;
+    a.scale_log2 = scale * kLog2E;
     const hipError_t e = dsaidx::launch_latent_attention(a, latent_dtype == DSAIDX_FP8_E4M3, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, name);
     return DSAIDX_OK;

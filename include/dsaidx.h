@@ -425,7 +425,7 @@ dsaidx_status indexer_cache_append_rope(const void* kv, int64_t kv_stride, int k
  * T = 0 is a no-op.
  *
  * Supported: (E, V) = (576, 512) or (512, 512), 1 <= H <= 128, page_size = 64,
- * 1 <= topk <= 131072, T * H <= 2^24, tables and pools of at most 2^27 tokens.
+ * 1 <= topk <= 131072, T * H <= 2^23, tables and pools of at most 2^27 tokens.
  */
 dsaidx_status indexer_latent_attention_topk(const void* q, int q_dtype, const void* latent_cache,
                                             const float* latent_scale, int latent_dtype, const int32_t* block_table,

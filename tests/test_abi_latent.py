@@ -61,13 +61,13 @@ COMMON = [
     (dict(ldt=-1), DTYPE), (dict(qd=0), UNSUP), (dict(qd=2), UNSUP), (dict(ldt=0), UNSUP), (dict(ldt=2), SHAPE),
     (dict(ls=P), SHAPE), (dict(H=0), SHAPE), (dict(H=129), UNSUP), (dict(E=640), UNSUP), (dict(V=256), UNSUP),
     (dict(ps=32, mpp=8), UNSUP), (dict(npg=0), SHAPE), (dict(mpp=0), SHAPE), (dict(scale=float("inf")), SHAPE),
-    (dict(scale=float("nan")), SHAPE), (dict(q=P + 8), UNSUP), (dict(lc=P + 8), UNSUP), (dict(out=P + 8), UNSUP),
+    (dict(scale=float("nan")), SHAPE), (dict(scale=3e38), SHAPE), (dict(q=P + 8), UNSUP), (dict(lc=P + 8), UNSUP), (dict(out=P + 8), UNSUP),
     (dict(mpp=1 << 22), UNSUP), (dict(npg=1 << 22), UNSUP)]
 
 
 @pytest.mark.parametrize("kw,status", COMMON + [
     (dict(idx=None), NULL), (dict(K=0), SHAPE), (dict(K=131073), UNSUP), (dict(T=3), SHAPE), (dict(T=-1), SHAPE),
-    (dict(T=1 << 21, seq=P), UNSUP), (dict(K=2048, ws=None), WS), (dict(K=2048, nws=8), WS),
+    (dict(T=1 << 21, seq=P), UNSUP), (dict(T=(1 << 23) + 1, H=1, seq=P), UNSUP), (dict(K=2048, ws=None), WS), (dict(K=2048, nws=8), WS),
     (dict(K=2048, ws=P + 8), UNSUP), (dict(T=0), OK), (dict(T=0, idx=None, q=None), OK), (dict(B=0), SHAPE)])
 def test_topk_rejects_before_launch(lib, kw, status):
     assert topk(lib, **kw) == status
@@ -101,3 +101,15 @@ def test_wrappers_refuse(lib):
     kv = torch.zeros((3, 576), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device"):
         dsa.cache_append_rope(kv, n, n, table, cache, torch.zeros((4, 64)))
+
+
+def test_workspace_sizes(lib):
+    """The wrappers' sizes are the library's: none without splits, whole rows of sums and pairs with them."""
+    import dsa_lightning_indexer_03_amd as dsa
+
+    assert dsa.latent_topk_workspace_bytes(1000, 128, 576, 512, 64) == 0
+    n = dsa.latent_topk_workspace_bytes(1, 16, 576, 512, 2048)
+    assert n > 0 and n % (16 * 514 * 4) == 0
+    assert n == lib.indexer_latent_attention_topk_workspace_bytes(1, 16, 576, 512, 2048, 1)
+    n = dsa.latent_shared_workspace_bytes(3, 128, 512, 512, 30000, 100, fp8=True)
+    assert n > 0 and n == lib.indexer_latent_attention_shared_workspace_bytes(3, 128, 512, 512, 30000, 100, 2)

@@ -6,7 +6,6 @@ import pytest
 import torch
 
 import dsa_lightning_indexer_03_amd as dsa
-from dsa_lightning_indexer_03_amd import _lib
 from gpu_util import say
 from latent_util import V, bf16, check_attention, expect_topk, make_pool
 from oracle.latent import attend, slots
@@ -187,10 +186,9 @@ def test_graphs():
         for b in range(B):
             s.append(np.full(300, b), s.prefix + np.arange(300))
 
-        lib = _lib.load()
-        h["ws1"] = torch.empty(lib.indexer_latent_attention_topk_workspace_bytes(B, H, E, V, K, 2) + 16,
-                               dtype=torch.uint8, device="cuda")
-        h["ws2"] = torch.empty(lib.indexer_latent_attention_shared_workspace_bytes(B, H, E, V, s.prefix, 512, 2) + 16,
+        h["ws1"] = torch.empty(dsa.latent_topk_workspace_bytes(B, H, E, V, K, True) + 16, dtype=torch.uint8,
+                               device="cuda")
+        h["ws2"] = torch.empty(dsa.latent_shared_workspace_bytes(B, H, E, V, s.prefix, 512, True) + 16,
                                dtype=torch.uint8, device="cuda")
 
         def step(h, s, own_space):
@@ -233,7 +231,7 @@ def test_graphs():
 def test_the_callers_workspace():
     x = inputs(6, 4, 600)
     want, _ = dsa.latent_attention_topk(**x, v_dim=V, scale=SCALE)
-    n = _lib.load().indexer_latent_attention_topk_workspace_bytes(4, H, E, V, 600, 1)
+    n = dsa.latent_topk_workspace_bytes(4, H, E, V, 600)
     assert n > 0
     ws = torch.full((n + 64,), 0xAB, dtype=torch.uint8, device="cuda")
     got, _ = dsa.latent_attention_topk(**x, v_dim=V, scale=SCALE, workspace=ws)
@@ -264,6 +262,9 @@ def test_refusals_on_the_device():
         call(latent_scale=torch.ones((24, 64), device="cuda"))
     with pytest.raises(ValueError, match="device"):
         call(topk_idx=x["topk_idx"].cpu())
+    with pytest.raises(ValueError, match="must be in"):
+        dsa.latent_attention_shared(x["q"], x["latent_cache"], x["block_table"][0].contiguous(), 2 ** 32 + 5,
+                                    x["block_table"], ints([1, 1]), V, SCALE)
     torch.cuda.synchronize()
 
 
