@@ -442,18 +442,9 @@ def _rows(t, name: str) -> int:
     return s[0]
 
 
-def _inference_only(where: str, *tensors) -> None:
-    for t in tensors:
-        if t is not None and t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{where} has no backward: call it under torch.no_grad() or detach its inputs")
-
-
-def _on_device(index: int, fn, *args):
-    """fn(*args, stream) with GPU `index` current, on its current stream."""
-    if _current_device() == index:
-        return fn(*args, _raw_stream(index))
-    with torch.cuda.device(index):
-        return fn(*args, _raw_stream(index))
+def _inference_only(where: str) -> None:
+    if torch.is_grad_enabled():
+        raise ValueError(f"{where} has no backward: call it under torch.no_grad() or detach its inputs")
 
 
 _BF16 = (torch.bfloat16,)
@@ -509,15 +500,22 @@ def cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin
             raise ValueError("index_k must be [T, D] of kv's type, on its device")
         if k_cache.shape != (P, page, D) or k_scale.shape != (P, page):
             raise ValueError("k_cache [P, page, D] / k_scale [P, page] shape mismatch")
-    _inference_only("cache_append_rope", kv, index_k)
+        if index_k.requires_grad:
+            _inference_only("cache_append_rope")
+    if kv.requires_grad:
+        _inference_only("cache_append_rope")
     B, max_pages = block_table.shape
     rope_len, R = cos_sin.shape
-    st = _on_device(index, lib.indexer_cache_append_rope, kv.data_ptr(), kv_stride, 1 if kv_interleaved else 0,
-                    _ptr(index_k), index_stride, 1 if index_interleaved else 0,
-                    BF16 if dtype == torch.bfloat16 else F32, cos_sin.data_ptr(), rope_len, R,
-                    seq_ids.data_ptr(), positions.data_ptr(), block_table.data_ptr(), B, max_pages,
-                    latent_cache.data_ptr(), _ptr(latent_scale), FP8_E4M3 if fp8 else BF16, _ptr(k_cache),
-                    _ptr(k_scale), P, T, E, D, page)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin, latent_scale,
+                                     kv_interleaved, index_k, k_cache, k_scale, index_interleaved)
+    st = lib.indexer_cache_append_rope(kv.data_ptr(), kv_stride, 1 if kv_interleaved else 0, _ptr(index_k),
+                                       index_stride, 1 if index_interleaved else 0,
+                                       BF16 if dtype == torch.bfloat16 else F32, cos_sin.data_ptr(), rope_len, R,
+                                       seq_ids.data_ptr(), positions.data_ptr(), block_table.data_ptr(), B, max_pages,
+                                       latent_cache.data_ptr(), _ptr(latent_scale), FP8_E4M3 if fp8 else BF16,
+                                       _ptr(k_cache), _ptr(k_scale), P, T, E, D, page, _raw_stream(index))
     if st:
         _lib.check(st, "indexer_cache_append_rope")
 
@@ -535,7 +533,8 @@ def _latent_inputs(q, latent_cache, latent_scale, block_table, where: str, *othe
         raise ValueError("latent_scale [P, page] goes with fp8 latent rows, None with bf16 rows")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
-    _inference_only(where, q, latent_cache)
+    if q.requires_grad or latent_cache.requires_grad:
+        _inference_only(where)
     return P, page, FP8_E4M3 if fp8 else BF16
 
 
@@ -586,15 +585,19 @@ def latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim: int, sc
     B, max_pages = block_table.shape
     if seq_ids is None and B != T:
         raise ValueError("block_table must have one row per query (or give seq_ids)")
-    K = topk_idx.shape[1]
+    K, index = topk_idx.shape[1], q.get_device()
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim, scale, latent_scale, seq_ids,
+                                         want_lse, workspace)
     out = q.new_empty((T, H, v_dim))
     lse = q.new_empty((T, H), dtype=torch.float32) if want_lse else None
     nws = lib.indexer_latent_attention_topk_workspace_bytes(T, H, E, v_dim, K, dt)
     ws = _scratch(workspace, nws, q)
-    st = _on_device(q.get_device(), lib.indexer_latent_attention_topk, q.data_ptr(), BF16, latent_cache.data_ptr(),
-                    _ptr(latent_scale), dt, block_table.data_ptr(), max_pages, P, topk_idx.data_ptr(), _ptr(seq_ids),
-                    B or 1, T, H, E, v_dim, page, K, scale, out.data_ptr(), _ptr(lse),
-                    _ptr(ws), nws)
+    st = lib.indexer_latent_attention_topk(q.data_ptr(), BF16, latent_cache.data_ptr(), _ptr(latent_scale), dt,
+                                           block_table.data_ptr(), max_pages, P, topk_idx.data_ptr(), _ptr(seq_ids),
+                                           B or 1, T, H, E, v_dim, page, K, scale, out.data_ptr(), _ptr(lse),
+                                           _ptr(ws), nws, _raw_stream(index))
     if st:
         _lib.check(st, "indexer_latent_attention_topk")
     return out, lse
@@ -627,15 +630,20 @@ def latent_attention_shared(q, latent_cache, prefix_table, prefix_len: int, bloc
     mcl = max_pages * page if max_context_len is None else int(max_context_len)
     if prefix_len >> 31 or mcl >> 31:
         raise ValueError("prefix_len and max_context_len must be in [0, 2^31)")
+    index = q.get_device()
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return latent_attention_shared(q, latent_cache, prefix_table, prefix_len, block_table, context_lens,
+                                           v_dim, scale, max_context_len, latent_scale, want_lse, workspace)
     out = q.new_empty((B, H, v_dim))
     lse = q.new_empty((B, H), dtype=torch.float32) if want_lse else None
     nws = lib.indexer_latent_attention_shared_workspace_bytes(B, H, E, v_dim, prefix_len, mcl, dt)
     ws = _scratch(workspace, nws, q)
-    st = _on_device(q.get_device(), lib.indexer_latent_attention_shared, q.data_ptr(), BF16, latent_cache.data_ptr(),
-                    _ptr(latent_scale), dt, _ptr(prefix_table), 0 if prefix_table is None else prefix_table.shape[0],
-                    prefix_len, block_table.data_ptr(), max_pages, P, context_lens.data_ptr(), mcl, B, H, E, v_dim,
-                    page, scale, out.data_ptr(), _ptr(lse),
-                    _ptr(ws), nws)
+    st = lib.indexer_latent_attention_shared(q.data_ptr(), BF16, latent_cache.data_ptr(), _ptr(latent_scale), dt,
+                                             _ptr(prefix_table), 0 if prefix_table is None else prefix_table.shape[0],
+                                             prefix_len, block_table.data_ptr(), max_pages, P,
+                                             context_lens.data_ptr(), mcl, B, H, E, v_dim, page, scale, out.data_ptr(),
+                                             _ptr(lse), _ptr(ws), nws, _raw_stream(index))
     if st:
         _lib.check(st, "indexer_latent_attention_shared")
     return out, lse
