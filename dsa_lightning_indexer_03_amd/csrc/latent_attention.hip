@@ -88,21 +88,25 @@ struct Operand<true> {
     }
 };
 
-constexpr int kThreads = 256;   // four waves, a wave per SIMD with all its registers
+// Four waves for 16 rows; eight for 32, which then share the keys' 16-row
+// blocks by halves of the rows, and have 64 columns of the values each.
+constexpr int waves_of(int mt) { return 4 * mt; }
 
 template <int KD, int MT, bool TOPK, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(64 * waves_of(MT), MT)
 latent_attention_kernel(LatentArgs a, LatentPlan p) {
     extern __shared__ __align__(16) unsigned char smem[];
     using L = Lds<KD, MT, FP8>;
     constexpr int E = 32 * KD;
     constexpr int RB = FP8 ? E : 2 * E;   // bytes of a cached row
-    constexpr int CT = 8;                 // 16-column blocks of the values that a wave computes
+    constexpr int NW = waves_of(MT);
+    constexpr int CT = 32 / NW;           // 16-column blocks of the values that a wave computes
     constexpr int kAhead = 3;             // operand reads in flight
-    constexpr int KB = kTile / 4;         // rows of a tile that a wave copies
+    constexpr int KB = kTile / NW;        // rows of a tile that a wave copies
     constexpr int kMainParts = FP8 ? KB / 2 : KB, kParts = kMainParts + (KD == 16 ? 0 : FP8 ? 1 : KB / 8);
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int n = lane & 15, g = lane >> 4;
+    const int kq = wave & 3, mq = wave >> 2;   // whose 16 keys' and 16 rows' scores this wave computes
     const int total = a.T * a.H;
     LatentKeys<TOPK> keys;
     if (!keys.start(a, p)) return;
@@ -114,8 +118,8 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     {
         const uint16_t* q = a.q + (int64_t)keys.r0 * E;
 #pragma unroll
-        for (int i = 0; i < 4 * MT; ++i) {
-            const int r = 4 * MT * wave + i;
+        for (int i = 0; i < 16 * MT / NW; ++i) {
+                const int r = 16 * MT / NW * wave + i;
             copy_to_lds(q + (int64_t)min(r, nrows - 1) * E, 16 * lane, lds0 + L::kQ + r * kRowB);
         }
         if constexpr (KD > 16)
@@ -133,7 +137,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     // ahead.
     auto part_row = [&](int i) -> int {
         if constexpr (FP8)
-            return __shfl(keys.row, i < kMainParts ? kb + 2 * i + (lane >> 5) : 16 * wave + (lane >> 2));
+            return __shfl(keys.row, i < kMainParts ? kb + 2 * i + (lane >> 5) : 16 * kq + (lane >> 2));
         return i < kMainParts ? -1 : __shfl(keys.row, kb + 8 * (i - kMainParts) + (lane >> 3));
     };
     uint64_t src = 0;   // bf16: addresses of the next tile's rows
@@ -147,10 +151,10 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
             if (i < kMainParts) {
                 copy_to_lds(row_address<RB>(a.cache, mine) + 16 * ((lane & 31) ^ (lane >> 5) * 8),
                             lds + (kb / 2 + i) * kPairB);
-            } else {
-                const int r = 16 * wave + (lane >> 2);
+            } else if (NW == 4 || wave < 4) {
+                const int r = 16 * kq + (lane >> 2);
                 copy_to_lds(row_address<RB>(a.cache, mine) + kV + 16 * ((lane & 3) ^ ((r >> 2) & 3)),
-                            rope + 16 * wave * 64);
+                            rope + 16 * kq * 64);
             }
         } else if (i < kMainParts) {
             copy_to_lds(lane_pointer(src, kb + i), 16 * lane, lds + (kb + i) * kRowB);
@@ -191,7 +195,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): queries and first tile
     tile_barrier();
     // B operand of 16 rows x 32 columns: row n, columns 8g .. 8g+7 of each 32
-    v8bf Q[MT][KD];
+    v8bf Q[KD];
     auto read_q = [&](int mt, int ks) {
         const int r = 16 * mt + n;
         v8bf q = *reinterpret_cast<const v8bf*>(
@@ -205,9 +209,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         return q;
     };
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int ks = 0; ks < KD; ++ks) Q[mt][ks] = read_q(mt, ks);
+    for (int ks = 0; ks < KD; ++ks) Q[ks] = read_q(mq, ks);
     // (never 0: a score of -inf, an entry without a row, has to stay one)
     const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
     tile_barrier();
@@ -217,11 +219,10 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     store_scale(0);
 
     v4f O[CT][MT];
-    float m[MT], l[MT];   // the rows' references; their sums over this wave's keys
+    float m[MT], l = 0.f;   // all rows' references; the sums of the rows and keys whose scores are this wave's
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         m[mt] = -3.402823466e38f;   // the lowest finite: any score but -inf moves it
-        l[mt] = 0.f;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) O[ct][mt] = v4f{0.f, 0.f, 0.f, 0.f};
     }
@@ -236,15 +237,15 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         Operand<FP8> k;
         const int n = ln & 15, g = ln >> 4;
         if constexpr (FP8) {
-            const int odd = wave & 1, q = 16 * (wave >> 1) + n;   // row 2q + odd
+            const int odd = kq & 1, q = 16 * (kq >> 1) + n;   // row 2q + odd
             k.x = *reinterpret_cast<const v2i*>(
                 ks < 16 ? tile + q * kPairB + kV * odd + 8 * g + (ks & 4 ? -128 : 128) * odd + 32 * ks
                         : rope + (2 * q + odd) * 64 + 16 * ((2 * (ks - 16) + (g >> 1)) ^ ((n >> 1) & 3)) +
                               8 * (g & 1));
         } else {
             k.x = *reinterpret_cast<const v8bf*>(
-                ks < 16 ? tile + (16 * wave + n) * kRowB + 16 * g + 64 * ks
-                        : rope + (16 * wave + n) * 128 + 16 * ((4 * (ks - 16) + g) ^ ((n >> 1) & 7)));
+                ks < 16 ? tile + (16 * kq + n) * kRowB + 16 * g + 64 * ks
+                        : rope + (16 * kq + n) * 128 + 16 * ((4 * (ks - 16) + g) ^ ((n >> 1) & 7)));
         }
         return k;
     };
@@ -270,42 +271,38 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     };
     Operand<FP8> K[kAhead], W[kAhead];
     v8bf P[MT];
-    v4f S[MT];
-    float sum[MT], ks4[4] = {1.f, 1.f, 1.f, 1.f};
+    v4f S;
+    float sum = 0.f, ks4[4] = {1.f, 1.f, 1.f, 1.f};
     auto read_p = [&](int kk) {
         const int n = ln & 15, g = ln >> 4;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
             P[mt] = *reinterpret_cast<const v8bf*>(smem + L::kP + (16 * mt + n) * kPRowB + 16 * (4 * kk + g));
     };
+    auto own_m = [&]() { return MT == 1 || mq == 0 ? m[0] : m[MT - 1]; };
     auto write_p = [&]() {
         const int n = ln & 15, g = ln >> 4;
+        const float ref = own_m();
+        float pr[4];
+        sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            float pr[4];
-            sum[j] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                pr[e] = __builtin_amdgcn_exp2f(fmaf(S[j][e], scale, -m[j]));
-                sum[j] += pr[e];
-                if constexpr (FP8) pr[e] *= ks4[e];
-            }
-            // P[row][key]: 16-byte piece 4(wave/2) + g holds the keys 4g .. 4g+3 of the key blocks
-            // 2(wave/2) and 2(wave/2) + 1
-            *reinterpret_cast<uint2*>(smem + L::kP + (16 * j + n) * kPRowB + 16 * (4 * (wave >> 1) + g) + 8 * (wave & 1)) =
-                uint2{pack_bf16(pr[0], pr[1]), pack_bf16(pr[2], pr[3])};
+        for (int e = 0; e < 4; ++e) {
+            pr[e] = __builtin_amdgcn_exp2f(fmaf(S[e], scale, -ref));
+            sum += pr[e];
+            if constexpr (FP8) pr[e] *= ks4[e];
         }
+        // P[row][key]: 16-byte piece 4(kq/2) + g holds the keys 4g .. 4g+3 of the key blocks
+        // 2(kq/2) and 2(kq/2) + 1
+        *reinterpret_cast<uint2*>(smem + L::kP + (16 * mq + n) * kPRowB + 16 * (4 * (kq >> 1) + g) + 8 * (kq & 1)) =
+            uint2{pack_bf16(pr[0], pr[1]), pack_bf16(pr[2], pr[3])};
     };
-    auto highest = [&](int j) { return scale * fmaxf(fmaxf(S[j][0], S[j][1]), fmaxf(S[j][2], S[j][3])); };
+    auto highest = [&]() { return scale * fmaxf(fmaxf(S[0], S[1]), fmaxf(S[2], S[3])); };
     // The rows' references move to the tile's maxima where those are above them.
     auto rebase = [&]() {
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            float v = highest(j);
-            v = fmaxf(v, __shfl_xor(v, 16, kWave));
-            v = fmaxf(v, __shfl_xor(v, 32, kWave));
-            if (g == 0) red[wave * 16 * MT + 16 * j + n] = v;
-        }
+        float top = highest();
+        top = fmaxf(top, __shfl_xor(top, 16, kWave));
+        top = fmaxf(top, __shfl_xor(top, 32, kWave));
+        if (g == 0) red[kq * 16 * MT + 16 * mq + n] = top;
         tile_barrier();
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -314,7 +311,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
             for (int w = 0; w < 4; ++w) v = fmaxf(v, red[w * 16 * MT + 16 * mt + n]);
             const float f = __builtin_amdgcn_exp2f(m[mt] - v);
             m[mt] = v;
-            l[mt] *= f;
+            if (mt == mq) l *= f;
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) O[ct][mt] *= f;
         }
@@ -335,8 +332,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         const int t_now = t_next;
         const uint64_t next = keys.mask;
         int mine = part_row(0);
-#pragma unroll
-        for (int j = 0; j < MT; ++j) S[j] = v4f{0.f, 0.f, 0.f, 0.f};
+        S = v4f{0.f, 0.f, 0.f, 0.f};
 
         // ---- scores: S^T, keys 4g .. 4g+3 of this wave's 16, row n of each block; beside
         //      them the next tile's copies (behind the last tile: zeros that nobody reads) ----
@@ -344,8 +340,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         for (int ks = 0; ks < KD; ++ks) {
             __builtin_amdgcn_sched_barrier(0);
             const v8bf k = K[ks % kAhead].get();
-#pragma unroll
-            for (int j = 0; j < MT; ++j) S[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, Q[j][ks], S[j], 0, 0, 0);
+            S = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, Q[ks], S, 0, 0, 0);
             if (ks + kAhead < KD) K[ks % kAhead] = read_k(buf, ks + kAhead);
             if ((ks + 1) * kParts / KD > ks * kParts / KD) {
                 const int i = ks * kParts / KD, row = mine;
@@ -356,23 +351,18 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         __builtin_amdgcn_sched_barrier(0);
         // ---- softmax against the rows' references ----
         if constexpr (FP8) {
-            const v4f s4 = *reinterpret_cast<const v4f*>(smem + L::kScale + 256 * buf + 4 * (16 * wave + 4 * (ln >> 4)));
+            const v4f s4 = *reinterpret_cast<const v4f*>(smem + L::kScale + 256 * buf + 4 * (16 * kq + 4 * (ln >> 4)));
 #pragma unroll
             for (int e = 0; e < 4; ++e) ks4[e] = s4[e];
-#pragma unroll
-            for (int j = 0; j < MT; ++j) S[j] *= s4;
+            S *= s4;
         }
         if (here != ~0ull) {
-            const uint32_t mine = FP8 ? (uint32_t)(here >> (32 * (wave >> 1) + (wave & 1))) >> (8 * (ln >> 4))
-                                      : (uint32_t)(here >> (16 * wave)) >> (4 * (ln >> 4));
+            const uint32_t mine = FP8 ? (uint32_t)(here >> (32 * (kq >> 1) + (kq & 1))) >> (8 * (ln >> 4))
+                                      : (uint32_t)(here >> (16 * kq)) >> (4 * (ln >> 4));
 #pragma unroll
-            for (int j = 0; j < MT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[j][e] = mine >> (FP8 ? 2 * e : e) & 1 ? S[j][e] : -__builtin_inff();
+            for (int e = 0; e < 4; ++e) S[e] = mine >> (FP8 ? 2 * e : e) & 1 ? S[e] : -__builtin_inff();
         }
-        bool rise = false;
-#pragma unroll
-        for (int j = 0; j < MT; ++j) rise |= highest(j) > m[j] + kSlack;
+        const bool rise = highest() > own_m() + kSlack;
         write_p();
         if (wave_ballot(rise) && lane == 0) flag[buf] = 1;
         if (threadIdx.x == 0) flag[buf ^ 1] = 0;
@@ -382,8 +372,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         const int risen = flag[buf];
         read_p(0);
         if (uniform(risen)) rebase();
-#pragma unroll
-        for (int j = 0; j < MT; ++j) l[j] += sum[j];
+        l += sum;
 
         // ---- O^T += V^T P^T; beside it the rows of the tile behind the next one, and the
         //      hand-over: every wave has read its last operands, and the next tile is there ----
@@ -422,13 +411,9 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     // ---- join the waves' sums, write ----
     __builtin_amdgcn_s_waitcnt(0x0F70);  // no copy may still be in flight
     tile_barrier();
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        float x = l[j];
-        x += __shfl_xor(x, 16, kWave);
-        x += __shfl_xor(x, 32, kWave);
-        if (g == 0) red[wave * 16 * MT + 16 * j + n] = x;
-    }
+    l += __shfl_xor(l, 16, kWave);
+    l += __shfl_xor(l, 32, kWave);
+    if (g == 0) red[kq * 16 * MT + 16 * mq + n] = l;
     tile_barrier();
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -625,7 +610,7 @@ hipError_t run(const LatentArgs& a, const LatentPlan& p, hipStream_t stream) {
     const hipError_t e = set_lds_limit(once, (const void*)latent_attention_kernel<KD, MT, TOPK, FP8>, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((latent_attention_kernel<KD, MT, TOPK, FP8>), dim3((unsigned)(p.n_prefix + p.n_own)),
-                       dim3(kThreads), lds, stream, a, p);
+                       dim3(64 * waves_of(MT)), lds, stream, a, p);
     return hipGetLastError();
 }
 
