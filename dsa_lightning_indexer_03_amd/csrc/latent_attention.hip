@@ -10,18 +10,20 @@
 // Indexer explained", section 1.
 //
 // Here: blocks of 16 or 32 query rows (larger ones: latent_rows.hip), the
-// choice of block and split, and the join.  One workgroup of four waves takes
-// a block (a query's heads, or the stacked heads of several queries for the
-// shared prefix) and a run of 64-key tiles.  A tile is staged once in LDS and
-// serves both products:
+// choice of block and split, and the join.  One workgroup takes a block (a
+// query's heads, or the stacked heads of several queries for the shared prefix)
+// and a run of 64-key tiles.  A tile is staged once in LDS and serves both
+// products; with four waves, for 16 rows:
 //   S^T (16 keys x rows) = K Q^T: wave w has keys 16w .. 16w+15, the queries
 //     sit in its registers;
 //   O^T (128 columns x rows) += V^T P^T: wave w has columns 128w .. 128w+127,
 //     the probabilities of all 64 keys come through LDS as bf16, the values
 //     are read transposed from the same tile.
-// Both leave a lane with one query row (lane % 16 of each 16-row block), so
+// Eight waves, for 32 rows, take 16 keys and 16 rows each, and 64 columns: 229
+// us for 1000 queries of 32 heads, 2048 selected, where four took 239.  Both
+// products leave a lane with one query row (lane % 16 of each 16-row block), so
 // the softmax's factors are per lane.  The exponent's reference m is common to
-// the four waves and only moves when a score exceeds it by more than kSlack
+// the waves and only moves when a score exceeds it by more than kSlack
 // (base 2): a flag in LDS, read behind the barrier that the exchange of P needs
 // anyway, sends all waves through a second pass that takes the tile's maximum,
 // rescales and rewrites P.  Sums are fp32; P is rounded to bf16, the second
@@ -31,10 +33,11 @@
 // workgroups, whose fp32 partial sums a second kernel joins by their maxima.
 //
 // With few rows a tile is bound by its bytes: 64 queries of 16 heads, 2048 rows
-// of 1152 bytes each, take 33 us and the join 3, 4.5 TB/s of distinct rows
-// (a 1 GiB copy reaches 5.2 read and written); from MALL the same tiles take
-// 1.7 us instead of 3.6.  With one query it is latency: 32 workgroups of one
-// tile take 8 us, four dependent loads and the launch, and joining them 4.
+// of 1152 bytes each, take 31 us and the join 5, 4.9 TB/s of distinct rows (a
+// 1 GiB copy reaches 5.2 read and written).  1000 queries of 16 heads on 4
+// sequences take 214 us, 11 TB/s of rows from the caches; most of a tile's 1.7
+// us is the wait for its copies.  With one query it is latency: 32 workgroups
+// of one tile take 8 us, four dependent loads and the launch, and the join 4.
 #include "device_once.h"
 #include "latent_common.h"
 
@@ -88,8 +91,7 @@ struct Operand<true> {
     }
 };
 
-// Four waves for 16 rows; eight for 32, which then share the keys' 16-row
-// blocks by halves of the rows, and have 64 columns of the values each.
+// Four waves for 16 rows, eight for 32.
 constexpr int waves_of(int mt) { return 4 * mt; }
 
 template <int KD, int MT, bool TOPK, bool FP8>
@@ -519,7 +521,7 @@ int pad8(int n) { return (n + 7) / 8 * 8; }
 
 // Query rows of a workgroup: the smallest block that holds all of them, at
 // most 128.  1000 queries, 2048 selected rows of 576 (bf16 / fp8), in us:
-//   32 heads: blocks of 16: 422 / 427, of 32: 241 / 260, of 64: 272 / 344
+//   32 heads: blocks of 16: 422 / 427, of 32: 229 / 242, of 64: 272 / 344
 //   64 heads: of 32: 493 / 516, of 64: 319 / 397, of 128: 377 / 457
 //   128 heads: of 64: 622 / 787, of 128: 542 / 589
 int block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
