@@ -179,6 +179,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
     LatentAhead ahead;
     int t = keys.seek(keys.t0, ahead);
     uint64_t here = keys.mask;   // the entries of the tile that is computed
+    const float shift = FP8 ? scale_shift(keys, a.cache_scale) : 0.f;
     address();
 #pragma unroll
     for (int i = 0; i < kParts; ++i) stage(0, i, part_row(i));
@@ -304,7 +305,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         float top = highest();
         top = fmaxf(top, __shfl_xor(top, 16, kWave));
         top = fmaxf(top, __shfl_xor(top, 32, kWave));
-        if (g == 0) red[kq * 16 * MT + 16 * mq + n] = top;
+        if (g == 0) red[kq * 16 * MT + 16 * mq + n] = top + shift;
         tile_barrier();
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -364,7 +365,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) S[e] = mine >> (FP8 ? 2 * e : e) & 1 ? S[e] : -__builtin_inff();
         }
-        const bool rise = highest() > own_m() + kSlack;
+        const bool rise = highest() > own_m() + (kSlack - shift);
         write_p();
         if (wave_ballot(rise) && lane == 0) flag[buf] = 1;
         if (threadIdx.x == 0) flag[buf ^ 1] = 0;

@@ -220,6 +220,18 @@ __device__ __forceinline__ const unsigned char* lane_pointer(uint64_t p, int lan
     const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(p >> 32), lane);
     return reinterpret_cast<const unsigned char*>((uint64_t)hi << 32 | lo);
 }
+// fp8 rows: the exponents' references are raised by log2 of the scale of the
+// run's first row, so that probabilities are rounded to bf16, after the product
+// with their rows' scales, in units of it.  A run of one row, or of rows of one
+// scale, then rounds only probabilities: the scale's own rounding, which all the
+// heads would share, stays out.  The sums have the same reference.
+template <bool TOPK>
+__device__ __forceinline__ float scale_shift(const LatentKeys<TOPK>& keys, const float* scales) {
+    if (keys.mask == 0) return 0.f;
+    const float s = fabsf(scales[__builtin_amdgcn_readlane(keys.row, __builtin_ctzll(keys.mask))]);
+    const float shift = s >= 0x1p-40f && s <= 0x1p40f ? __builtin_amdgcn_logf(s) : 0.f;
+    return __int_as_float(uniform(__float_as_int(shift)));
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v2bf{(__bf16)lo, (__bf16)hi});
 }

@@ -126,6 +126,7 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
         spread();
     };
     uint64_t here = keys.mask;
+    const float shift = FP8 ? scale_shift(keys, a.cache_scale) : 0.f;
     spread();
     if (mover) {
 #pragma unroll
@@ -207,11 +208,11 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
 #pragma unroll
         for (int i = 1; i < 4; ++i) top = fmaxf(top, fmaxf(S[0][i], S[1][i]));
         top *= scale;
-        if (wave_ballot(top > m + kSlack)) {
+        if (wave_ballot(top > m + (kSlack - shift))) {
             // the reference moves to these keys' maximum where that is above it
             top = fmaxf(top, __shfl_xor(top, 16, kWave));
             top = fmaxf(top, __shfl_xor(top, 32, kWave));
-            const float to = fmaxf(m, top);
+            const float to = fmaxf(m, top + shift);
             const float f = __builtin_amdgcn_exp2f(m - to);
             m = to;
             l *= f;

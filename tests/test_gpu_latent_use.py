@@ -295,3 +295,28 @@ def test_pool_beyond_32_bit_offsets(heads, kind):
             dsa.latent_attention_shared(q, small, pre_l, 100, low, n, V, SCALE, latent_scale=s4)[0]]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) and bool(a.any()) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("heads", [1, 24, 64, 128])
+@pytest.mark.parametrize("K", [1, 3])
+def test_one_fp8_row_rounds_once(heads, K):
+    """A query whose only row (K times) is an fp8 row gets that row, rounded
+    once.  The product of its probability and scale is 1 up to the rounding of
+    the exponent: scores in base 2 stay below 64 here, so the exponent is off by
+    2^-18 at most, the product by 2^-18, and bf16 rounds it to 1; the sum, which
+    is not rounded, keeps that error.  What is left is the output's half step,
+    2^-8, those 2^-18, and a few roundings of fp32, 2^-20 together."""
+    rng = np.random.default_rng(heads + K)
+    T = 40
+    cache, scale, rows = make_pool(rng, 2 * T, E, "fp8")
+    scale *= torch.exp(torch.randn(scale.shape, device="cuda"))
+    rows = values(cache, scale)
+    table = ints(np.arange(2 * T).reshape(T, 2))
+    at = rng.integers(0, 128, T)
+    q = bf16(rng.normal(size=(T, heads, E)))[0].cuda()
+    assert np.abs(np.einsum("the,te->th", q.double().cpu().numpy(), rows[np.arange(T) * 128 + at])).max() * SCALE < 44
+    say(f"one fp8 row {K} times, {heads} heads")
+    out, _ = dsa.latent_attention_topk(q, cache, table, ints(np.tile(at[:, None], (1, K))), V, SCALE, latent_scale=scale)
+    torch.cuda.synchronize()
+    want = rows[np.arange(T) * 128 + at][:, None, :V]
+    assert (np.abs(out.double().cpu().numpy() - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -18 + 2.0 ** -20)).all()
