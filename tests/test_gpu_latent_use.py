@@ -320,3 +320,29 @@ def test_one_fp8_row_rounds_once(heads, K):
     torch.cuda.synchronize()
     want = rows[np.arange(T) * 128 + at][:, None, :V]
     assert (np.abs(out.double().cpu().numpy() - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -18 + 2.0 ** -20)).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("heads", [7, 20, 100])
+def test_long_lists_of_keys(heads, kind):
+    """Selections and prefixes of many thousand rows, in 32 parts each, the last
+    ones short; every part holds keys of its own."""
+    rng = np.random.default_rng(heads)
+    mpp, T, K = 330, 2, 20001
+    pages = mpp + 1
+    cache, scale, rows = make_pool(rng, pages, E, kind)
+    table = rng.permutation(pages)[:mpp]
+    idx = np.stack([rng.permutation(mpp * 64)[:K] for _ in range(T)])
+    q, qv = bf16(1.5 * rng.normal(size=(T, heads, E)))
+    say(f"{K} selected rows and a prefix of {mpp * 64 - 3}, {heads} heads, {kind}")
+    out, lse = dsa.latent_attention_topk(q.cuda(), cache, ints(np.tile(table, (T, 1))), ints(idx), V, SCALE,
+                                         latent_scale=scale, want_lse=True)
+    n = mpp * 64 - 3
+    own = np.full((T, 1), mpp)                         # the page that no table held: not an id of the pool for query 1
+    own[1] = pages
+    out_s, lse_s = dsa.latent_attention_shared(q.cuda(), cache, ints(table), n, ints(own), ints([0, 9]), V, SCALE,
+                                               latent_scale=scale, want_lse=True)
+    torch.cuda.synchronize()
+    check_attention(out, lse, expect_topk(qv, rows, np.tile(table, (T, 1)), idx, np.arange(T), SCALE, pages), "selected")
+    s = slots(np.zeros(n, int), np.arange(n), table[None], pages)
+    check_attention(out_s, lse_s, [attend(qv[b], rows[s], SCALE, V) for b in range(T)], "prefix")
