@@ -10,7 +10,9 @@
 //     a' = a cos - b sin,   b' = b cos + a sin
 // where pair i is columns (2i, 2i + 1) or (i, i + R/2) of the rotated part.
 // bf16 rows are the fp32 results rounded once; fp8 rows (fp8_row.h) take
-// their scale from the rotated row.
+// their scale from the rotated row.  A NaN stays one in a latent row of either
+// type, so that attention over the row shows it; index keys are stored as
+// kcache_append stores them, without NaN codes, which no score may meet.
 //
 // Layout: one wave per token.  Its 8-column pieces, latent row first, index key
 // behind it, go to lanes 0, 1, ... and round again; a piece whose partner
@@ -148,10 +150,10 @@ cache_append_rope_kernel(AppendRopeArgs a) {
         const int j = lane + 64 * s;
         if (j >= n) continue;
         if (index[s]) {
-            *reinterpret_cast<uint2*>(a.k_cache + row * kD + 8 * (j - n_kv)) = quant8(y[s], s_ix);
+            *reinterpret_cast<uint2*>(a.k_cache + row * kD + 8 * (j - n_kv)) = quant8<false>(y[s], s_ix);
         } else if constexpr (FP8) {
             *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(a.latent) + row * a.E + 8 * j) =
-                quant8(y[s], s_kv);
+                quant8<true>(y[s], s_kv);
         } else {
             v8bf b;
 #pragma unroll

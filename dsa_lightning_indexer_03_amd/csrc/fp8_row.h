@@ -1,6 +1,11 @@
 // One row of values to the library's FP8 storage: E4M3FN codes and one fp32
 // scale, scale = max|x| / 448 (1 for an all-zero row), code = the E4M3FN value
 // nearest to the correctly rounded quotient x / scale, ties to even.
+//
+// An infinite element makes the scale infinite and is stored as +-448, its own
+// sign: it reads as itself (and the row's finite elements, codes 0, as NaN).  A
+// zero whose row's scale underflows to 0 stays a zero.  A NaN does not enter
+// the scale; KEEP_NAN stores it as a NaN code, else it takes a finite one.
 #pragma once
 
 #include "common.h"
@@ -12,6 +17,7 @@ constexpr float kE4m3Max = 448.f;
 __device__ __forceinline__ float row_scale(float absmax) { return absmax > 0.f ? absmax / kE4m3Max : 1.f; }
 
 // Codes of eight consecutive elements of a row with this scale.
+template <bool KEEP_NAN>
 __device__ __forceinline__ uint2 quant8(const float (&x)[8], float scale) {
     float q[8];
     if (scale >= 0x1p-80f && scale <= 0x1p+80f) {
@@ -37,8 +43,15 @@ __device__ __forceinline__ uint2 quant8(const float (&x)[8], float scale) {
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = fminf(fmaxf(x[j] / scale, -kE4m3Max), kE4m3Max);
+        for (int j = 0; j < 8; ++j) {
+            const float r = x[j] / scale;   // NaN: inf / inf, 0 / 0 or x itself
+            q[j] = r == r ? fminf(fmaxf(r, -kE4m3Max), kE4m3Max)
+                          : __builtin_copysignf(x[j] == 0.f ? 0.f : kE4m3Max, x[j]);
+        }
     }
+    if constexpr (KEEP_NAN)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = x[j] == x[j] ? q[j] : x[j];
     int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
     w0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w0, true);
     int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);

@@ -100,7 +100,7 @@ kcache_append_kernel(KcacheArgs a) {
 #pragma unroll
             for (int d = 8; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 16));
             const float scale = m > 0.f ? m / 448.f : 1.f;
-            const uint2 w = quant8(x[u], scale);
+            const uint2 w = quant8<false>(x[u], scale);
             if (ok[u]) {
                 *reinterpret_cast<uint2*>(a.k_cache + row[u] * kD + 8 * l16) = w;
                 if (l16 == 0) a.k_scale[row[u]] = scale;

@@ -266,7 +266,9 @@ size_t indexer_prefill_chunk_paged_workspace_bytes(int B, int T, int max_kv_len,
  *   scale  = max_d |k_d| / 448 (binary32 division; 1 for an all-zero key)
  *   code_d = the E4M3FN value nearest to k_d / scale (binary32 quotient),
  *            ties to the even code, magnitudes above 448 saturated, sign kept
- * so decode(code_d) * scale is within half a code step of k_d.
+ * so decode(code_d) * scale is within half a code step of k_d.  An infinite
+ * element makes the scale infinite and is stored as +-448, so that it reads as
+ * itself; the finite elements beside it are stored as zeros.
  *
  *   k            [T][D] new keys in k_dtype (DSAIDX_BF16 or DSAIDX_F32),
  *                16-byte aligned
@@ -358,7 +360,10 @@ dsaidx_status indexer_topk_gather_layers(const void* const* latent_caches, void*
  * Pair i is the rotated part's columns (2i, 2i + 1) when the row's
  * `interleaved` argument is nonzero, (i, i + rope_dim/2) when it is zero.
  * bf16 rows are rounded once to nearest even; fp8 rows are quantised as
- * indexer_kcache_append does, from the rotated row.
+ * indexer_kcache_append does, from the rotated row.  A NaN in a latent row (the
+ * rotation makes one of an infinity times 0, too) stays a NaN, as the code 0x7F
+ * or 0xFF in an fp8 row, and does not enter the row's scale; index keys hold no
+ * NaN codes.
  *
  *   kv           [T] rows of E elements in in_dtype (BF16 or F32), kv_stride
  *                elements apart
