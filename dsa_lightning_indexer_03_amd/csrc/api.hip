@@ -266,7 +266,9 @@ dsaidx_status latent_check(const void* q, int q_dtype, const void* latent_cache,
     if ((int64_t)max_pages_per_seq * page_size > kMaxLatentTokens || num_pages > kMaxLatentTokens / 64)
         return fail(DSAIDX_ERR_UNSUPPORTED, "max_pages_per_seq=%d num_pages=%d (tables and pools of at most %d tokens)",
                     max_pages_per_seq, num_pages, kMaxLatentTokens);
-    // (a launch holds less than 2^32 threads, and a query takes a workgroup)
+    // (a launch holds less than 2^32 threads; a query whose keys are not cut takes a
+    // workgroup of 256 up to 16 heads, of 512 above, and plans with more parts are
+    // taken only where they fit)
     if ((int64_t)T * H > (1 << 23)) return fail(DSAIDX_ERR_UNSUPPORTED, "rows * H = %lld > 2^23", (long long)T * H);
     const float in_base_2 = scale * kLog2E;
     if (!(in_base_2 - in_base_2 == 0.f)) return fail(DSAIDX_ERR_SHAPE, "scale * log2(e) must be finite");

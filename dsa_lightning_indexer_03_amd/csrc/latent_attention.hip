@@ -531,8 +531,12 @@ int block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <
 // bound by memory.
 double tile_us(int rows) { return rows == 16 ? 1.4 : rows == 32 ? 1.9 : rows == 64 ? 2.6 : 4.2; }
 
+// Threads of a workgroup (launch_latent_attention), and of the largest launch.
+int plan_threads(int rows) { return rows == 16 ? 64 * waves_of(1) : 512; }
+constexpr int64_t kMaxThreads = (1ll << 32) - 1;
+
 // Splits of the key tiles that finish first, in us (p.rows and the tile counts
-// are given).  A workgroup takes 5 and its tiles, own ones longer the more CUs
+// are given); 1e30 where every one passes a launch's threads.  A workgroup takes 5 and its tiles, own ones longer the more CUs
 // stream 74 KB (fp8: 37) a tile of their own; the GPU runs one workgroup per
 // CU, prefix parts first; joining takes 4 and reads and writes every slot's
 // sums.  A run of own tiles takes as long as one of the prefix.  64 queries of
@@ -552,6 +556,7 @@ double split(int64_t blocks_p, int tiles_p, int64_t blocks_o, int tiles_o, int64
         if (lo < ceil_div(tiles_o, 32)) lo = ceil_div(tiles_o, 32);
         const int so = tiles_o > 0 ? ceil_div(tiles_o, lo) : 0;
         const int64_t np = blocks_p * sp, no = blocks_o * so;
+        if ((np + no + 14) * plan_threads(p.rows) > kMaxThreads) continue;   // (14: both rounded up to 8s)
         const double full = (fp8 ? 1.8 : 3.6) - tile_o;   // more per tile with every CU streaming
         const double cp = 5 + tile * len, co = 5 + (tile_o + (full > 0 ? full : 0) * (double)(no < kCUs ? no : kCUs) / kCUs) * lo;
         // whole rounds of prefix parts; the rest of them beside the own parts
@@ -588,6 +593,7 @@ LatentPlan make_plan(int T, int H, bool topk, int K, int prefix_len, int max_ctx
     p.hb = ceil_div(H, p.rows);
     p.joint = tiles_p > 0;
     const int all = tiles_p + tiles_o;
+    // (in one part it is T workgroups, which fit a launch for all T * H <= 2^23)
     const double us = split(0, 0, (int64_t)T * p.hb, all > 0 ? all : 1, rows, H, fp8, p);
     if (tiles_p > 0) {   // or the prefix is walked once for the stacked rows
         LatentPlan s{};

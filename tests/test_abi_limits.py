@@ -1,0 +1,36 @@
+"""Host-only checks of the largest calls that the entry points take: a launch
+holds less than 2^32 threads, whatever the sizes."""
+import os
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "dsa_lightning_indexer_03_amd", "libdsaidx.so")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(LIB):
+        pytest.skip("libdsaidx.so not built")
+    from dsa_lightning_indexer_03_amd import _lib
+    return _lib.load(LIB)
+
+
+@pytest.mark.parametrize("dt", [1, 2])
+@pytest.mark.parametrize("B,H,prefix,ctx", [
+    (1 << 23, 1, 1, 1), (1 << 22, 1, 1000, 4096), (1 << 22, 2, 1000, 4096), (1 << 22, 1, 40000, 131072),
+    (1 << 21, 2, 40000, 131072), (1 << 21, 1, 1 << 20, 1 << 27), (1 << 19, 16, 1 << 20, 1 << 27)])
+def test_plans_fit_a_launch(lib, B, H, prefix, ctx, dt):
+    """At these sizes only one workgroup a query fits: beside a stacked prefix
+    each query's own keys would be two workgroups or more of 512 threads (one,
+    for the first), cut in pieces of the prefix's length.  Parts would show in
+    the workspace, as 514 floats for each row and part."""
+    assert lib.indexer_latent_attention_shared_workspace_bytes(B, H, 576, 512, prefix, ctx, dt) == 0
+    assert B * 256 < 1 << 32 and H <= 16   # the launch without parts: blocks of 16 rows, 256 threads
+
+
+def test_smaller_batches_keep_their_parts(lib):
+    """The limit leaves plans alone that fit: 64 queries of 16 heads on 32768
+    shared positions are cut in parts, and 2^20 queries of one head, too."""
+    for B, H, prefix, ctx in ((64, 16, 32768, 512), (1 << 20, 1, 40000, 131072)):
+        assert lib.indexer_latent_attention_shared_workspace_bytes(B, H, 576, 512, prefix, ctx, 1) > 0
