@@ -442,9 +442,10 @@ def _rows(t, name: str) -> int:
     return s[0]
 
 
-def _inference_only(where: str) -> None:
-    if torch.is_grad_enabled():
-        raise ValueError(f"{where} has no backward: call it under torch.no_grad() or detach its inputs")
+def _inference_only(where: str, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{where} has no backward: call it under torch.no_grad() or detach its inputs")
 
 
 _BF16 = (torch.bfloat16,)
@@ -500,10 +501,7 @@ def cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin
             raise ValueError("index_k must be [T, D] of kv's type, on its device")
         if k_cache.shape != (P, page, D) or k_scale.shape != (P, page):
             raise ValueError("k_cache [P, page, D] / k_scale [P, page] shape mismatch")
-        if index_k.requires_grad:
-            _inference_only("cache_append_rope")
-    if kv.requires_grad:
-        _inference_only("cache_append_rope")
+    _inference_only("cache_append_rope", kv, index_k, cos_sin, latent_cache, latent_scale, k_scale)
     B, max_pages = block_table.shape
     rope_len, R = cos_sin.shape
     if _current_device() != index:
@@ -533,8 +531,7 @@ def _latent_inputs(q, latent_cache, latent_scale, block_table, where: str, *othe
         raise ValueError("latent_scale [P, page] goes with fp8 latent rows, None with bf16 rows")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
-    if q.requires_grad or latent_cache.requires_grad:
-        _inference_only(where)
+    _inference_only(where, q, latent_cache, latent_scale)
     return P, page, FP8_E4M3 if fp8 else BF16
 
 

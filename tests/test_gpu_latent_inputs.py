@@ -1,0 +1,73 @@
+"""What the calls on the latent cache accept and refuse on the device: inputs
+that want a gradient, and bf16 given as bit patterns."""
+import pytest
+import torch
+
+import dsa_lightning_indexer_03_amd as dsa
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+E, V = 576, 512
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def append_args(g, fp8=False):
+    T = 5
+    kv = torch.randn((T, E + 128), generator=g, device="cuda").bfloat16()
+    ang = torch.rand((64, 32), generator=g, device="cuda")
+    latent = torch.zeros((2, 64, E), dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+    return dict(kv=kv[:, :E], seq_ids=torch.zeros(T, dtype=torch.int32, device="cuda"),
+                positions=torch.arange(T, dtype=torch.int32, device="cuda"),
+                block_table=torch.tensor([[1, 0]], dtype=torch.int32, device="cuda"), latent_cache=latent,
+                cos_sin=torch.cat([ang.cos(), ang.sin()], 1), latent_scale=torch.zeros((2, 64), device="cuda") if fp8 else None,
+                index_k=kv[:, E:], k_cache=torch.zeros((2, 64, 128), dtype=torch.uint8, device="cuda"),
+                k_scale=torch.zeros((2, 64), device="cuda"))
+
+
+def attend_args(g, fp8=False):
+    cache = torch.randn((3, 64, E), generator=g, device="cuda").bfloat16()
+    if fp8:
+        cache = (cache.float() * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    return dict(q=torch.randn((2, 16, E), generator=g, device="cuda").bfloat16(), latent_cache=cache,
+                block_table=torch.tensor([[0, 2], [1, 2]], dtype=torch.int32, device="cuda"), v_dim=V, scale=0.04,
+                latent_scale=0.01 + 0.01 * torch.rand((3, 64), generator=g, device="cuda") if fp8 else None)
+
+
+def topk(**kw):
+    idx = torch.arange(0, 128, 2, dtype=torch.int32, device="cuda").repeat(2, 1)
+    return dsa.latent_attention_topk(topk_idx=idx, want_lse=True, **kw)
+
+
+def shared(**kw):
+    return dsa.latent_attention_shared(prefix_table=kw["block_table"][0].contiguous(), prefix_len=70,
+                                       context_lens=torch.tensor([3, 128], dtype=torch.int32, device="cuda"),
+                                       want_lse=True, **kw)
+
+
+@pytest.mark.parametrize("call,make,names", [
+    (dsa.cache_append_rope, append_args, ("kv", "index_k", "cos_sin", "latent_scale", "k_scale")),
+    (topk, attend_args, ("q", "latent_scale")), (shared, attend_args, ("q", "latent_scale"))])
+def test_inputs_that_want_a_gradient(call, make, names):
+    """None of these calls has a backward, so each refuses every input that wants one, except under no_grad."""
+    args = make(torch.Generator(device="cuda").manual_seed(1), fp8=True)
+    for name in names:
+        wants = {**args, name: args[name].detach().clone().requires_grad_()}
+        say(f"{name} wants a gradient")
+        with pytest.raises(ValueError, match="backward"):
+            call(**wants)
+        with torch.no_grad():
+            call(**wants)
+    torch.cuda.synchronize()
+
+
+def test_a_bf16_cache_that_wants_a_gradient():
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for call, make in ((dsa.cache_append_rope, append_args), (topk, attend_args), (shared, attend_args)):
+        args = make(g)
+        with pytest.raises(ValueError, match="backward"):
+            call(**{**args, "latent_cache": args["latent_cache"].requires_grad_()})
