@@ -448,9 +448,9 @@ def _inference_only(where: str, *tensors) -> None:
             raise ValueError(f"{where} has no backward: call it under torch.no_grad() or detach its inputs")
 
 
-_BF16 = (torch.bfloat16,)
-_NEW = (torch.bfloat16, torch.float32)
-_LATENT = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_NEW = _BF16 + (torch.float32,)
+_LATENT = _BF16 + _CODES
 _FLOATS = (torch.float32,)
 _INTS = (torch.int32,)
 
@@ -484,7 +484,7 @@ def cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin
     if len(shape) != 3 or shape[2] != E:
         raise ValueError("latent_cache must be [P, page, E] with the E of kv")
     P, page, _ = shape
-    fp8 = latent_cache.dtype != torch.bfloat16
+    fp8 = latent_cache.dtype in _CODES
     if fp8 != (latent_scale is not None) or (fp8 and latent_scale.shape != (P, page)):
         raise ValueError("latent_scale [P, page] goes with fp8 latent rows, None with bf16 rows")
     if cos_sin.dim() != 2 or block_table.dim() != 2:
@@ -510,7 +510,7 @@ def cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin
                                      kv_interleaved, index_k, k_cache, k_scale, index_interleaved)
     st = lib.indexer_cache_append_rope(kv.data_ptr(), kv_stride, 1 if kv_interleaved else 0, _ptr(index_k),
                                        index_stride, 1 if index_interleaved else 0,
-                                       BF16 if dtype == torch.bfloat16 else F32, cos_sin.data_ptr(), rope_len, R,
+                                       F32 if dtype == torch.float32 else BF16, cos_sin.data_ptr(), rope_len, R,
                                        seq_ids.data_ptr(), positions.data_ptr(), block_table.data_ptr(), B, max_pages,
                                        latent_cache.data_ptr(), _ptr(latent_scale), FP8_E4M3 if fp8 else BF16,
                                        _ptr(k_cache), _ptr(k_scale), P, T, E, D, page, _raw_stream(index))
@@ -526,7 +526,7 @@ def _latent_inputs(q, latent_cache, latent_scale, block_table, where: str, *othe
     if q.dim() != 3 or len(shape) != 3 or shape[2] != q.shape[2]:
         raise ValueError("q must be [rows, H, E] and latent_cache [P, page, E]")
     P, page, _ = shape
-    fp8 = latent_cache.dtype != torch.bfloat16
+    fp8 = latent_cache.dtype in _CODES
     if fp8 != (latent_scale is not None) or (fp8 and latent_scale.shape != (P, page)):
         raise ValueError("latent_scale [P, page] goes with fp8 latent rows, None with bf16 rows")
     if block_table.dim() != 2:
@@ -587,7 +587,7 @@ def latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim: int, sc
         with torch.cuda.device(index):
             return latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim, scale, latent_scale, seq_ids,
                                          want_lse, workspace)
-    out = q.new_empty((T, H, v_dim))
+    out = q.new_empty((T, H, v_dim), dtype=torch.bfloat16)
     lse = q.new_empty((T, H), dtype=torch.float32) if want_lse else None
     nws = lib.indexer_latent_attention_topk_workspace_bytes(T, H, E, v_dim, K, dt)
     ws = _scratch(workspace, nws, q)
@@ -632,7 +632,7 @@ def latent_attention_shared(q, latent_cache, prefix_table, prefix_len: int, bloc
         with torch.cuda.device(index):
             return latent_attention_shared(q, latent_cache, prefix_table, prefix_len, block_table, context_lens,
                                            v_dim, scale, max_context_len, latent_scale, want_lse, workspace)
-    out = q.new_empty((B, H, v_dim))
+    out = q.new_empty((B, H, v_dim), dtype=torch.bfloat16)
     lse = q.new_empty((B, H), dtype=torch.float32) if want_lse else None
     nws = lib.indexer_latent_attention_shared_workspace_bytes(B, H, E, v_dim, prefix_len, mcl, dt)
     ws = _scratch(workspace, nws, q)

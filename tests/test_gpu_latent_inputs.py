@@ -71,3 +71,23 @@ def test_a_bf16_cache_that_wants_a_gradient():
         args = make(g)
         with pytest.raises(ValueError, match="backward"):
             call(**{**args, "latent_cache": args["latent_cache"].requires_grad_()})
+
+
+@pytest.mark.parametrize("bits", [torch.int16, torch.uint16])
+def test_bf16_as_bit_patterns(bits):
+    """bf16 inputs may come as int16 or uint16 patterns, as in the package's other calls; the output is bfloat16."""
+    say(f"bf16 inputs as {bits}")
+    want, got = (append_args(torch.Generator(device="cuda").manual_seed(3)) for _ in range(2))
+    dsa.cache_append_rope(**want)
+    as_bits = {k: got[k].view(bits) for k in ("kv", "index_k", "latent_cache")}
+    dsa.cache_append_rope(**{**got, **as_bits})
+    torch.cuda.synchronize()
+    assert bool(want["latent_cache"].any()) and bool(want["k_cache"].any())
+    for k in ("latent_cache", "k_cache", "k_scale"):
+        assert torch.equal(want[k].view(torch.uint8), got[k].view(torch.uint8))
+    for fp8 in (False, True):
+        args = attend_args(torch.Generator(device="cuda").manual_seed(4), fp8)
+        as_bits = {k: args[k].view(bits) for k in (("q",) if fp8 else ("q", "latent_cache"))}
+        for call in (topk, shared):
+            for a, b in zip(call(**args), call(**{**args, **as_bits})):
+                assert a.dtype == b.dtype and torch.equal(a, b) and bool(a.any())
