@@ -74,6 +74,15 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
         for (int ks = 0; ks < KD; ++ks) Q[ks] = *reinterpret_cast<const v8bf*>(qp + 32 * ks);
     }
 
+    // The lane, made anew for every phase: what follows from it, kept longer,
+    // would cost registers that the queries and sums need (or spill, and a reload
+    // waits for every copy in flight).
+    int ln = lane;
+    auto renew = [&]() { asm volatile("" : "+v"(ln)); };
+    // x of another lane
+    auto from_lane = [](int x, int i) { return __builtin_amdgcn_ds_bpermute(4 * i, x); };
+    auto across = [&](float x, int d) { return __int_as_float(from_lane(__float_as_int(x), ln ^ d)); };
+
     // ---- copies: rows kb .. of a tile; fp8: their codes two rows at a time, the rotary
     //      columns of 16 rows by each of four waves, the scales by one ----
     const int kb = kMovers ? 16 * (wave & 3) : 8 * wave;
@@ -86,11 +95,11 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
         if constexpr (FP8) {
             const uint32_t lds = lds0 + kCodesAt + buf * kCodesB;
             if (i < kMainParts) {
-                const int mine = __shfl(keys.row, kb + 2 * i + (lane >> 5));
-                copy_to_lds(row_address<RB>(a.cache, mine) + 16 * (lane & 31), lds + (kb + 2 * i) * kV);
+                const int mine = from_lane(keys.row, kb + 2 * i + (ln >> 5));
+                copy_to_lds(row_address<RB>(a.cache, mine) + 16 * (ln & 31), lds + (kb + 2 * i) * kV);
             } else if (kMovers || wave < 4) {
-                const int r = 16 * (wave & 3), mine = __shfl(keys.row, r + (lane >> 2));
-                copy_to_lds(row_address<RB>(a.cache, mine) + kV + 16 * (lane & 3), lds + kTile * kV + r * 64);
+                const int r = 16 * (wave & 3), mine = from_lane(keys.row, r + (ln >> 2));
+                copy_to_lds(row_address<RB>(a.cache, mine) + kV + 16 * (ln & 3), lds + kTile * kV + r * 64);
             }
         } else {
             const uint32_t lds = lds0 + buf * kTileB;
@@ -146,10 +155,6 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
     // (never 0: a score of -inf, an entry without a row, has to stay one)
     const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
 
-    // The lane, made anew for every phase: what follows from it, kept longer,
-    // would cost registers that the queries and sums need.
-    int ln = lane;
-    auto renew = [&]() { asm volatile("" : "+v"(ln)); };
     v4f O[32];
 #pragma unroll
     for (int ct = 0; ct < 32; ++ct) O[ct] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -210,8 +215,8 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
         top *= scale;
         if (wave_ballot(top > m + (kSlack - shift))) {
             // the reference moves to these keys' maximum where that is above it
-            top = fmaxf(top, __shfl_xor(top, 16, kWave));
-            top = fmaxf(top, __shfl_xor(top, 32, kWave));
+            top = fmaxf(top, across(top, 16));
+            top = fmaxf(top, across(top, 32));
             const float to = fmaxf(m, top + shift);
             const float f = __builtin_amdgcn_exp2f(m - to);
             m = to;
