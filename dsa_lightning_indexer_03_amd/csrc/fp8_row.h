@@ -39,7 +39,10 @@ __device__ __forceinline__ uint2 quant8(const float (&x)[8], float scale) {
             const float q0 = x[j] * y;
             const float q1 = fmaf(fmaf(-scale, q0, x[j]), y, q0);
             const float q2 = fmaf(fmaf(-scale, q1, x[j]), y, q1);
-            q[j] = fminf(fmaxf(__builtin_copysignf(q2, x[j]), -kE4m3Max), kE4m3Max);
+            q[j] = __builtin_copysignf(q2, x[j]);
+            // |x| <= 448 scale (1 + 2^-24): the quotient is below the midpoint above
+            // 448 in any case, and the clamp only there for NaN
+            if constexpr (!KEEP_NAN) q[j] = fminf(fmaxf(q[j], -kE4m3Max), kE4m3Max);
         }
     } else {
 #pragma unroll
@@ -47,11 +50,9 @@ __device__ __forceinline__ uint2 quant8(const float (&x)[8], float scale) {
             const float r = x[j] / scale;   // NaN: inf / inf, 0 / 0 or x itself
             q[j] = r == r ? fminf(fmaxf(r, -kE4m3Max), kE4m3Max)
                           : __builtin_copysignf(x[j] == 0.f ? 0.f : kE4m3Max, x[j]);
+            if constexpr (KEEP_NAN) q[j] = x[j] == x[j] ? q[j] : x[j];
         }
     }
-    if constexpr (KEEP_NAN)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = x[j] == x[j] ? q[j] : x[j];
     int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
     w0 = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w0, true);
     int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
