@@ -194,7 +194,7 @@ dsaidx_status indexer_cache_append_rope(const void* kv, int64_t kv_stride, int k
     if ((index_k != nullptr) != (k_cache != nullptr) || (index_k != nullptr) != (k_scale != nullptr))
         return fail(DSAIDX_ERR_SHAPE, "index_k, k_cache and k_scale are given together or not at all");
     // (a wave a token, and a launch holds less than 2^32 threads)
-    if (T >= 1 << 26) return fail(DSAIDX_ERR_UNSUPPORTED, "T=%d >= 2^26", T);
+    if (T > 1 << 25) return fail(DSAIDX_ERR_UNSUPPORTED, "T=%d > 2^25", T);
     if (T == 0) return DSAIDX_OK;
     if (!kv) return fail(DSAIDX_ERR_NULL, "kv is NULL");
     if (!cos_sin) return fail(DSAIDX_ERR_NULL, "cos_sin is NULL");

@@ -382,7 +382,7 @@ dsaidx_status indexer_topk_gather_layers(const void* const* latent_caches, void*
  * same (sequence, position) leave that slot's contents undefined.  T = 0 is
  * a no-op.  No workspace.
  *
- * Supported: D = 128, page_size = 64, T < 2^26, E a multiple of 8 up to 1024,
+ * Supported: D = 128, page_size = 64, T <= 2^25, E a multiple of 8 up to 1024,
  * rope_dim a multiple of 16 up to 128 (and E); rows, cos_sin and latent_cache
  * 16-byte aligned, k_cache 8-byte.
  */

@@ -36,10 +36,10 @@ def test_smaller_batches_keep_their_parts(lib):
         assert lib.indexer_latent_attention_shared_workspace_bytes(B, H, 576, 512, prefix, ctx, 1) > 0
 
 
-@pytest.mark.parametrize("T", [1 << 26, (1 << 31) - 1])
+@pytest.mark.parametrize("T", [(1 << 25) + 1, (1 << 26) - 1, 1 << 26, (1 << 31) - 1])
 def test_appends_fit_a_launch(lib, T):
-    """A wave a token: 2^26 tokens would be 2^32 threads.  Refused before any launch."""
+    """A wave a token, four to a workgroup: 2^26 - 3 tokens would be 2^32 threads.  Refused before any launch."""
     P = 4096   # a fake, aligned device address (never dereferenced)
     st = lib.indexer_cache_append_rope(P, 576, 1, P, 128, 0, 1, P, 100, 64, P, P, P, 1, 2, P, None, 1, P, P, 2, T, 576,
                                        128, 64, None)
-    assert st == 4 and b"2^26" in lib.dsaidx_last_error()
+    assert st == 4 and b"2^25" in lib.dsaidx_last_error()
