@@ -290,7 +290,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            pr[e] = __builtin_amdgcn_exp2f(fmaf(S[e], scale, -ref));
+            pr[e] = __builtin_amdgcn_exp2f(S[e] - ref);
             sum += pr[e];
             if constexpr (FP8) pr[e] *= ks4[e];
         }
@@ -299,7 +299,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         *reinterpret_cast<uint2*>(smem + L::kP + (16 * mq + n) * kPRowB + 16 * (4 * (kq >> 1) + g) + 8 * (kq & 1)) =
             uint2{pack_bf16(pr[0], pr[1]), pack_bf16(pr[2], pr[3])};
     };
-    auto highest = [&]() { return scale * fmaxf(fmaxf(S[0], S[1]), fmaxf(S[2], S[3])); };
+    auto highest = [&]() { return fmaxf(fmaxf(S[0], S[1]), fmaxf(S[2], S[3])); };
     // The rows' references move to the tile's maxima where those are above them.
     auto rebase = [&]() {
         float top = highest();
@@ -359,6 +359,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
             for (int e = 0; e < 4; ++e) ks4[e] = s4[e];
             S *= s4;
         }
+        S = scaled_scores(S, scale);
         if (here != ~0ull) {
             const uint32_t mine = FP8 ? (uint32_t)(here >> (32 * (kq >> 1) + (kq & 1))) >> (8 * (ln >> 4))
                                       : (uint32_t)(here >> (16 * kq)) >> (4 * (ln >> 4));

@@ -232,6 +232,13 @@ __device__ __forceinline__ float scale_shift(const LatentKeys<TOPK>& keys, const
     const float shift = s >= 0x1p-40f && s <= 0x1p40f ? __builtin_amdgcn_logf(s) : 0.f;
     return __int_as_float(uniform(__float_as_int(shift)));
 }
+// Scores times the softmax's scale, rounded before their maximum is taken off
+// them: of a product left whole (in an fma), scores past 2^31 would keep more
+// than 2^7 that their maximum, rounded, has not, and 2 to that is infinite.
+__device__ __forceinline__ v4f scaled_scores(v4f s, float scale) {
+#pragma clang fp contract(off)
+    return s * scale;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v2bf{(__bf16)lo, (__bf16)hi});
 }

@@ -195,12 +195,14 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
         // ---- softmax ----
         renew();
         v4f by4[2];
-        if constexpr (FP8)
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
+        for (int kt = 0; kt < 2; ++kt) {
+            if constexpr (FP8) {
                 by4[kt] = *reinterpret_cast<const v4f*>(by + 64 * kt + 16 * (ln >> 4));
                 S[kt] *= by4[kt];
             }
+            S[kt] = scaled_scores(S[kt], scale);
+        }
         if (live != ~0u) {
             const uint32_t mine = live >> (4 * (ln >> 4));
 #pragma unroll
@@ -212,7 +214,6 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
         float top = fmaxf(S[0][0], S[1][0]);
 #pragma unroll
         for (int i = 1; i < 4; ++i) top = fmaxf(top, fmaxf(S[0][i], S[1][i]));
-        top *= scale;
         if (wave_ballot(top > m + (kSlack - shift))) {
             // the reference moves to these keys' maximum where that is above it
             top = fmaxf(top, across(top, 16));
@@ -230,7 +231,7 @@ latent_rows_kernel(LatentArgs a, LatentPlan p) {
             float pr[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                pr[i] = __builtin_amdgcn_exp2f(fmaf(S[kt][i], scale, -m));
+                pr[i] = __builtin_amdgcn_exp2f(S[kt][i] - m);
                 l += pr[i];
                 if constexpr (FP8) pr[i] *= by4[kt][i];
             }
