@@ -60,3 +60,29 @@ def test_far_scores(H, power, scale, kind):
         # one rounding of P and one of the output
         assert bool(((o - row).abs() <= 2 * 2.0 ** -8 * row.abs()).all()), "out is not the row of the highest score"
         assert bool(((l - top).abs() <= 2.0 ** -21 * top.abs()).all()), "lse"
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("T,H,n", [(2, 16, 500), (260, 16, 500), (2, 31, 300), (260, 64, 300), (3, 64, 500), (2, 128, 500)])
+def test_a_bad_head_stays_alone(T, H, n, kind):
+    """A head whose query holds NaN or infinities gives NaN, in one run and in
+    several; the heads beside it, in its block and its wave, what they give without."""
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    x = torch.randn((8, 64, E), generator=g, device="cuda")
+    cache, cs = (x.bfloat16(), None) if kind == "bf16" else ((x * 100).clamp(-448, 448).to(torch.float8_e4m3fn),
+                                                            0.005 + 0.01 * torch.rand((8, 64), generator=g, device="cuda"))
+    q = torch.randn((T, H, E), generator=g, device="cuda").bfloat16()
+    idx = torch.randint(0, 512, (T, n), generator=g, device="cuda", dtype=torch.int32)
+    say(f"bad heads, T={T} H={H} {kind}")
+
+    def call(q):
+        return dsa.latent_attention_topk(q, cache, ints(np.arange(8)[None]), idx, V, 0.04, latent_scale=cs,
+                                         seq_ids=ints(np.zeros(T)), want_lse=True)
+    want, wl = call(q)
+    bad = torch.zeros((T, H), dtype=torch.bool, device="cuda")
+    bad[0, 1], bad[T - 1, 0], bad[1, H - 1] = True, True, True
+    q[0, 1, 100], q[T - 1, 0, 550], q[1, H - 1, 7] = float("nan"), float("nan"), float("inf")
+    out, lse = call(q)
+    torch.cuda.synchronize()
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], wl[~bad])
+    assert bool(torch.isnan(out[bad]).all()) and not bool(torch.isfinite(lse[bad]).any())
