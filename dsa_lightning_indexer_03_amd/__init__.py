@@ -604,13 +604,15 @@ def latent_attention_shared(q, latent_cache, prefix_table, prefix_len: int, bloc
                             scale: float, max_context_len: int | None = None, latent_scale=None,
                             want_lse: bool = False, workspace: torch.Tensor | None = None):
     """One decode step of B queries over a prefix that all of them share, read
-    once for the batch, and each sequence's own positions behind it.
+    once for each block of up to 128 query rows, and each sequence's own
+    positions behind it.
 
     q [B,H,E] bf16, latent_cache and latent_scale as latent_attention_topk;
     prefix_table [n] int32 page ids of the prefix's first ``prefix_len``
     positions (None when that is 0); block_table [B,max_pages] int32 and
     context_lens [B] int32: the sequences' own pages and lengths.
-    ``max_context_len`` bounds context_lens (default: max_pages * page).
+    ``max_context_len`` bounds context_lens (default: max_pages * page); the work
+    is cut for contexts of that length, so a bound near the longest is faster.
     ``workspace``: the caller's scratch of latent_shared_workspace_bytes, not
     shared by calls in flight (default: a new one each call).
     Returns (out bf16 [B,H,v_dim], lse fp32 [B,H] or None); a query without a

@@ -22,9 +22,11 @@
 // none of its own, and stores nothing.
 //
 // Bound by HBM with many tokens: 32768 tokens of 576 + 128 columns, bf16 rows
-// (92 MB with the angles): 21 us, 4.3 TB/s (a 1 GiB copy: 5.2); two tokens a
-// wave in full rounds of lanes took 24.  fp8 rows (68 MB): 24 us, bound by the
-// exact quotients.  One token: 3 us, the launch.
+// (94 MB with the angles): 27 us, 3.5 TB/s, from inputs that no cache holds (a
+// 1 GiB copy: 5.2), 21 us where the inputs are still in one; two tokens a wave in
+// full rounds of lanes took 24 there.  fp8 rows (75 MB): 27 and 23 us, bound by
+// vector instructions, 487 a token, most of them the exact quotients: 50 more
+// took 1.6 us longer.  One token: 2.5 us, the launch.
 #include "common.h"
 #include "fp8_row.h"
 #include "kernels.h"

@@ -26,9 +26,12 @@
 // the waves and only moves when a score exceeds it by more than kSlack
 // (base 2): a flag in LDS, read behind the barrier that the exchange of P needs
 // anyway, sends all waves through a second pass that takes the tile's maximum,
-// rescales and rewrites P.  Sums are fp32; P is rounded to bf16, the second
-// product's operand (its sum is taken before the rounding; the output is bf16
-// too).
+// rescales and rewrites P.  Sums are fp32; P is rounded to bf16, because the
+// matrix cores take both operands of the second product in the values' type: an
+// output is off by at most 2^-8 of sum P |c| for that, beside its own rounding
+// (2.0e-3 rms of the outputs where the rounding alone is 1.7e-3; a second
+// operand with the rest of P would double that product).  P's sum is taken before
+// the rounding, so that lse does not have it.
 // When the rows alone do not fill the GPU the key tiles are split over
 // workgroups, whose fp32 partial sums a second kernel joins by their maxima.
 //
@@ -121,7 +124,7 @@ latent_attention_kernel(LatentArgs a, LatentPlan p) {
         const uint16_t* q = a.q + (int64_t)keys.r0 * E;
 #pragma unroll
         for (int i = 0; i < 16 * MT / NW; ++i) {
-                const int r = 16 * MT / NW * wave + i;
+            const int r = 16 * MT / NW * wave + i;
             copy_to_lds(q + (int64_t)min(r, nrows - 1) * E, 16 * lane, lds0 + L::kQ + r * kRowB);
         }
         if constexpr (KD > 16)
@@ -522,10 +525,11 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 int pad8(int n) { return (n + 7) / 8 * 8; }
 
 // Query rows of a workgroup: the smallest block that holds all of them, at
-// most 128.  1000 queries, 2048 selected rows of 576 (bf16 / fp8), in us:
+// most 128.  1000 queries, 2048 selected rows of 576 (bf16 / fp8), in us a call,
+// calls in a row:
 //   32 heads: blocks of 16: 422 / 427, of 32: 229 / 242, of 64: 272 / 344
 //   64 heads: of 32: 493 / 516, of 64: 319 / 397, of 128: 377 / 457
-//   128 heads: of 64: 622 / 787, of 128: 542 / 589
+//   128 heads: of 64: 622 / 787, of 128: 542 / 589 (on another card 552 / 587)
 int block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
 // Time of a 64-key tile in a block of that many rows, on a busy GPU and not
@@ -542,6 +546,9 @@ constexpr int64_t kMaxThreads = (1ll << 32) - 1;
 // CU, prefix parts first; joining takes 4 and reads and writes every slot's
 // sums.  A run of own tiles takes as long as one of the prefix.  64 queries of
 // 16 heads, 2048 selected: 2 splits 45.6 us, 4 (chosen) 36.
+// Counts tried: each up to 8, then steps of a seventh to a quarter.  The times are
+// rough, and a finer list gives the rule more near-ties to lose: with 20 counts 64
+// queries of 16 heads on a prefix of 32768 took 30 parts for 28, 109 us for 91.
 double split(int64_t blocks_p, int tiles_p, int64_t blocks_o, int tiles_o, int64_t rows, int H, bool fp8,
              LatentPlan& p) {
     static const int kSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32};

@@ -24,11 +24,12 @@
 // Bound by the matrix cores and, behind them, LDS reads: a tile of 128 rows
 // needs 4352 cycles of the first (a SIMD) and, at the measured rates of the two
 // kinds of reads, 5200 of the second.  1000 queries of 128 heads, 2048 selected
-// rows of 576 (571 GFLOP): 542 us, 1.05 PFLOP/s; 64 queries of 128 heads on a
-// prefix of 32751 (588 GFLOP): 515 us, 1.14 PFLOP/s, where a bf16 matrix
-// product of 8192 cubed reached 1.09 to 1.28 on the same cards: at these rates
-// the power limit sets the clock (with zeros for data the second takes 449 us).
-// fp8 rows: 589 and 556 us.
+// rows of 576 (571 GFLOP): 552 us a call, calls in a row (1.03 PFLOP/s); 64
+// queries of 128 heads on a prefix of 32751 (588 GFLOP): 526 us (1.12), where a
+// bf16 matrix product of 8192 cubed reached 1.09 to 1.28: at these rates the
+// power limit sets the clock, by card and by run (542 and 515 us on another card,
+// medians of 593 and 552 in a profile's bursts; with zeros for data the second
+// takes 449).  fp8 rows: 587 and 557 us.
 #include "device_once.h"
 #include "latent_common.h"
 

@@ -406,7 +406,8 @@ dsaidx_status indexer_cache_append_rope(const void* kv, int64_t kv_stride, int k
  *     S[t,h,j] = scale * q[t,h] . c[j]      over the query's selected rows j
  *     out[t,h] = sum_j softmax_j(S) c[j][:V],  lse[t,h] = log sum_j exp S[t,h,j]
  * Scores, sums and the softmax's statistics are fp32; the probabilities
- * enter the second product rounded to bf16; out is rounded once to bf16.
+ * enter the second product rounded to bf16 (lse without that rounding); out is
+ * rounded once to bf16.
  * A query without a row gives out = 0 and lse = -inf.
  *
  *   q            [T][H][E] bf16 (q_dtype must be DSAIDX_BF16)
@@ -443,9 +444,11 @@ size_t indexer_latent_attention_topk_workspace_bytes(int T, int H, int E, int V,
 
 /*
  * indexer_latent_attention_shared -- one decode step of B queries that share
- * a long prefix: the prefix's rows are read once for the whole batch (the
- * B * H query rows are stacked against them), each sequence's own rows once
- * for its H heads, and the two parts are joined.
+ * a long prefix: the B * H query rows are stacked against the prefix's rows,
+ * which are read once for each block of up to 128 of them, each sequence's own
+ * rows once for its H heads, and the two parts are joined.  (Where that does not
+ * pay, as with 128 heads, whose rows fill a block alone, each query walks the
+ * prefix and its own rows in one.)
  *
  * The same attention as indexer_latent_attention_topk (shapes, types,
  * rounding), over every position: query b sees the prefix's positions
@@ -460,7 +463,9 @@ size_t indexer_latent_attention_topk_workspace_bytes(int T, int H, int E, int V,
  *   prefix_len   host value in [0, prefix_pages * page_size]; 0: no prefix
  *   block_table  [B][max_pages_per_seq] int32 page ids
  *   context_lens [B] int32 (device), clamped to [0, max_context_len]
- *   max_context_len  host bound, <= max_pages_per_seq * page_size
+ *   max_context_len  host bound, <= max_pages_per_seq * page_size.  The work is
+ *                cut and the workspace sized for contexts of that length, so a
+ *                bound near the longest one is faster than the table's width
  * A page id outside [0, num_pages) is a page without rows.  A query without
  * a row gives out = 0 and lse = -inf.  B = 0 is a no-op.
  *   workspace    indexer_latent_attention_shared_workspace_bytes(B, H, E, V,
