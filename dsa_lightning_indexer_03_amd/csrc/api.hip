@@ -7,6 +7,7 @@
 #include "device_once.h"
 #include "dsaidx.h"
 #include "kernels.h"
+#include "latent.h"
 
 namespace {
 

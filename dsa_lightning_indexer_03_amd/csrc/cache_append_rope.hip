@@ -29,7 +29,7 @@
 // took 1.6 us longer.  One token: 2.5 us, the launch.
 #include "common.h"
 #include "fp8_row.h"
-#include "kernels.h"
+#include "latent.h"
 
 namespace dsaidx {
 namespace {

@@ -3,7 +3,7 @@
 #pragma once
 
 #include "common.h"
-#include "kernels.h"
+#include "latent.h"
 
 namespace dsaidx {
 
