@@ -11,6 +11,9 @@ device, and passes pointers and the current HIP stream.
     cache_append_rope(kv, seq_ids, positions, block_table, latent_cache, cos_sin, index_k=None, ...)
     latent_attention_topk(q, latent_cache, block_table, topk_idx, v_dim, scale, ...)
     latent_attention_shared(q, latent_cache, prefix_table, prefix_len, block_table, context_lens, v_dim, scale, ...)
+    kv_append_rope(k, v, seq_ids, positions, block_table, k_cache, v_cache, cos_sin=None, ...)
+    prompt_attention(q, k, v, cu_seqlens, scale, want_lse=False)
+    kv_attention_decode(q, k_cache, v_cache, block_table, context_lens, scale, topk_idx=None, ...)
 
 Input formats: fp32 tensors; bf16 as torch.bfloat16 or int16/uint16 bit
 patterns; OCP FP8 E4M3 as torch.float8_e4m3fn or uint8 codes with fp32
@@ -28,7 +31,8 @@ __all__ = ["indexer_prefill", "indexer_prefill_noalloc", "indexer_decode_paged",
            "topk_gather_layers",
            "prefill_chunk_paged", "prefill_chunk_varlen",
            "cache_append_rope", "latent_attention_topk", "latent_attention_shared", "latent_topk_workspace_bytes",
-           "latent_shared_workspace_bytes", "dtype_code", "F32", "BF16", "FP8_E4M3"]
+           "latent_shared_workspace_bytes", "kv_append_rope", "prompt_attention", "kv_attention_decode",
+           "kv_decode_workspace_bytes", "dtype_code", "F32", "BF16", "FP8_E4M3"]
 
 
 def dtype_code(t: torch.Tensor) -> int:
@@ -645,4 +649,170 @@ def latent_attention_shared(q, latent_cache, prefix_table, prefix_len: int, bloc
                                              _ptr(lse), _ptr(ws), nws, _raw_stream(index))
     if st:
         _lib.check(st, "indexer_latent_attention_shared")
+    return out, lse
+
+
+def _heads(t, name: str, index: int, dtypes):
+    """Token and head stride (elements) of a [T, heads, columns] tensor on GPU `index` whose rows are contiguous."""
+    if t.dtype not in dtypes:
+        _need(t, name, *dtypes)
+    if t.get_device() != index or index < 0:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        raise ValueError(f"{name} must be on device {index}, the device of the other tensors")
+    s = t.stride()
+    if len(s) != 3 or (s[2] != 1 and t.shape[2] != 1):
+        raise ValueError(f"{name} must be [tokens, heads, columns] with contiguous rows")
+    return s[0], s[1]
+
+
+def _kv_caches(index: int, k_cache, v_cache, k_scale, v_scale, G: int, D: int, *others):
+    """Checks of the paged key and value caches; returns (P, page, dtype code)."""
+    _all(index, (("k_cache", k_cache, _LATENT), ("v_cache", v_cache, _LATENT), ("k_scale", k_scale, _FLOATS),
+                 ("v_scale", v_scale, _FLOATS), *others))
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[1] != G or shape[3] != D or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must be [P, G, page, D] with the G and D of the other tensors")
+    fp8 = k_cache.dtype in _CODES
+    if (v_cache.dtype in _CODES) != fp8:
+        raise ValueError("k_cache and v_cache must both be bf16 or both fp8")
+    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if fp8 != (s is not None) or (fp8 and s.shape != shape[:3]):
+            raise ValueError(f"{name} [P, G, page] goes with fp8 caches, None with bf16 ones")
+    return shape[0], shape[2], FP8_E4M3 if fp8 else BF16
+
+
+def kv_append_rope(k, v, seq_ids, positions, block_table, k_cache, v_cache, cos_sin=None, k_scale=None, v_scale=None,
+                   interleaved: bool = False) -> None:
+    """Writes T new tokens' keys, rotated by their positions, and values into
+    paged caches with G heads of their own, in place, in one launch.
+
+    k, v [T,G,D] bf16 or fp32 (tokens and heads may be strided); cos_sin
+    [rope_len,R] fp32 (R/2 cosines, then R/2 sines, of each position) turns the
+    first R columns of every key, None: no rotation; seq_ids, positions [T] int32
+    (a token outside the table, rope_len or the pool is skipped); block_table
+    [B,max_pages] int32; k_cache, v_cache [P,G,page,D] bf16, or uint8 /
+    float8_e4m3fn codes with k_scale, v_scale [P,G,page] fp32.  interleaved: pair
+    i is columns (2i, 2i+1), else (i, i + R/2).  Returns nothing."""
+    lib = _lib.load()
+    index = k.get_device()
+    ks, kh = _heads(k, "k", index, _NEW)
+    vs, vh = _heads(v, "v", index, _NEW)
+    T, G, D = k.shape
+    if v.shape != k.shape or (v.dtype == torch.float32) != (k.dtype == torch.float32):
+        raise ValueError("k and v must be [T, G, D] of one type")
+    P, page, dt = _kv_caches(index, k_cache, v_cache, k_scale, v_scale, G, D, ("cos_sin", cos_sin, _FLOATS),
+                             ("seq_ids", seq_ids, _INTS), ("positions", positions, _INTS),
+                             ("block_table", block_table, _INTS))
+    if block_table.dim() != 2 or (cos_sin is not None and cos_sin.dim() != 2):
+        raise ValueError("cos_sin must be [rope_len, R] and block_table [B, max_pages]")
+    if seq_ids.shape != (T,) or positions.shape != (T,):
+        raise ValueError("seq_ids / positions must have one entry per token")
+    _inference_only("kv_append_rope", k, v, cos_sin, k_cache, v_cache, k_scale, v_scale)
+    B, max_pages = block_table.shape
+    rope_len, R = (0, 0) if cos_sin is None else cos_sin.shape
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return kv_append_rope(k, v, seq_ids, positions, block_table, k_cache, v_cache, cos_sin, k_scale, v_scale,
+                                  interleaved)
+    st = lib.indexer_kv_append_rope(k.data_ptr(), ks, kh, v.data_ptr(), vs, vh,
+                                    F32 if k.dtype == torch.float32 else BF16, _ptr(cos_sin), rope_len, R,
+                                    1 if interleaved else 0, seq_ids.data_ptr(), positions.data_ptr(),
+                                    block_table.data_ptr(), B, max_pages, k_cache.data_ptr(), _ptr(k_scale),
+                                    v_cache.data_ptr(), _ptr(v_scale), dt, P, T, G, D, page, _raw_stream(index))
+    if st:
+        _lib.check(st, "indexer_kv_append_rope")
+
+
+def prompt_attention(q, k, v, cu_seqlens, scale: float, want_lse: bool = False):
+    """Causal attention over whole prompts, packed one after another, with
+    grouped heads: row i of a sequence attends over its rows 0 .. i, query head h
+    over key/value head h // (H / G).
+
+    q [T,H,D], k [T,G,D], v [T,G,V] bf16 (tokens and heads may be strided);
+    cu_seqlens [B+1] int32 (device): sequence b is rows cu_seqlens[b] ..
+    cu_seqlens[b+1]-1.  Returns (out bf16 [T,H,V], lse fp32 [T,H] or None); rows
+    behind the last sequence give zeros and -inf."""
+    lib = _lib.load()
+    index = q.get_device()
+    qs, qh = _heads(q, "q", index, _BF16)
+    ks, kh = _heads(k, "k", index, _BF16)
+    vs, vh = _heads(v, "v", index, _BF16)
+    _all(index, (("cu_seqlens", cu_seqlens, _INTS),))
+    T, H, D = q.shape
+    G, V = v.shape[1:]
+    if k.shape != (T, G, D) or v.shape[0] != T:
+        raise ValueError("q must be [T, H, D], k [T, G, D] and v [T, G, V]")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be [B + 1] with B >= 1")
+    _inference_only("prompt_attention", q, k, v)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return prompt_attention(q, k, v, cu_seqlens, scale, want_lse)
+    out = q.new_empty((T, H, V), dtype=torch.bfloat16)
+    lse = q.new_empty((T, H), dtype=torch.float32) if want_lse else None
+    st = lib.indexer_prompt_attention(q.data_ptr(), qs, qh, k.data_ptr(), ks, kh, v.data_ptr(), vs, vh, BF16,
+                                      cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, T, H, G, D, V, scale,
+                                      out.data_ptr(), _ptr(lse), _raw_stream(index))
+    if st:
+        _lib.check(st, "indexer_prompt_attention")
+    return out, lse
+
+
+def kv_decode_workspace_bytes(B: int, H: int, G: int, D: int, max_context_len: int, topk: int = 0,
+                              fp8: bool = False) -> int:
+    return _lib.load().indexer_kv_attention_decode_workspace_bytes(B, H, G, D, max_context_len, topk,
+                                                                   FP8_E4M3 if fp8 else BF16)
+
+
+def kv_attention_decode(q, k_cache, v_cache, block_table, context_lens, scale: float, topk_idx=None,
+                        max_context_len: int | None = None, k_scale=None, v_scale=None, want_lse: bool = False,
+                        workspace: torch.Tensor | None = None):
+    """One decode step over paged caches with G key/value heads: the new token of
+    each of B sequences attends over its whole context, or over the positions
+    selected for it; query head h reads key/value head h // (H / G).
+
+    q [B,H,D] bf16; k_cache, v_cache [P,G,page,D] bf16, or uint8 / float8_e4m3fn
+    codes with k_scale, v_scale [P,G,page] fp32, as kv_append_rope writes them;
+    block_table [B,max_pages] int32; context_lens [B] int32; topk_idx [B,K] int32
+    positions (-1, or outside the context: no row), None: every position.
+    ``max_context_len`` bounds context_lens (default: max_pages * page); the work
+    is cut for contexts of that length, so a bound near the longest is faster.
+    ``workspace``: the caller's scratch of kv_decode_workspace_bytes, not shared
+    by calls in flight (default: a new one each call).
+    Returns (out bf16 [B,H,D], lse fp32 [B,H] or None); a query without a position
+    gives zeros and -inf."""
+    lib = _lib.load()
+    index = q.get_device()
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [B, H, D] and the caches [P, G, page, D]")
+    B, H, D = q.shape
+    G = k_cache.shape[1]
+    P, page, dt = _kv_caches(index, k_cache, v_cache, k_scale, v_scale, G, D, ("q", q, _BF16),
+                             ("block_table", block_table, _INTS), ("context_lens", context_lens, _INTS),
+                             ("topk_idx", topk_idx, _INTS))
+    if block_table.dim() != 2 or block_table.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError("block_table / context_lens shape mismatch")
+    if topk_idx is not None and (topk_idx.dim() != 2 or topk_idx.shape[0] != B or topk_idx.shape[1] < 1):
+        raise ValueError("topk_idx must be [B, K] with K >= 1")
+    _inference_only("kv_attention_decode", q, k_cache, v_cache, k_scale, v_scale)
+    max_pages = block_table.shape[1]
+    mcl = max_pages * page if max_context_len is None else int(max_context_len)
+    if mcl >> 31:
+        raise ValueError("max_context_len must be in [0, 2^31)")
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return kv_attention_decode(q, k_cache, v_cache, block_table, context_lens, scale, topk_idx,
+                                       max_context_len, k_scale, v_scale, want_lse, workspace)
+    K = 0 if topk_idx is None else topk_idx.shape[1]
+    out = q.new_empty((B, H, D), dtype=torch.bfloat16)
+    lse = q.new_empty((B, H), dtype=torch.float32) if want_lse else None
+    nws = lib.indexer_kv_attention_decode_workspace_bytes(B, H, G, D, mcl, K, dt)
+    ws = _scratch(workspace, nws, q)
+    st = lib.indexer_kv_attention_decode(q.data_ptr(), BF16, k_cache.data_ptr(), _ptr(k_scale), v_cache.data_ptr(),
+                                         _ptr(v_scale), dt, block_table.data_ptr(), max_pages, P,
+                                         context_lens.data_ptr(), mcl, _ptr(topk_idx), K, B, H, G, D, page, scale,
+                                         out.data_ptr(), _ptr(lse), _ptr(ws), nws, _raw_stream(index))
+    if st:
+        _lib.check(st, "indexer_kv_attention_decode")
     return out, lse

@@ -7,6 +7,7 @@
 #include "device_once.h"
 #include "dsaidx.h"
 #include "kernels.h"
+#include "kv.h"
 #include "latent.h"
 
 namespace {
@@ -392,6 +393,224 @@ dsaidx_status indexer_latent_attention_shared(const void* q, int q_dtype, const 
                       indexer_latent_attention_shared_workspace_bytes(B, H, E, V, prefix_len, max_context_len,
                                                                       latent_dtype),
                       "indexer_latent_attention_shared", stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int kMaxKvHeads = 128;
+
+// Heads and scale of the attention calls with keys and values of G groups.
+dsaidx_status kv_heads_check(int H, int G, float scale) {
+    if (H < 1 || G < 1 || H % G != 0) return fail(DSAIDX_ERR_SHAPE, "H=%d G=%d (H a multiple of G)", H, G);
+    if (H > kMaxKvHeads) return fail(DSAIDX_ERR_UNSUPPORTED, "H=%d > %d", H, kMaxKvHeads);
+    const float in_base_2 = scale * kLog2E;
+    if (!(in_base_2 - in_base_2 == 0.f)) return fail(DSAIDX_ERR_SHAPE, "scale * log2(e) must be finite");
+    return DSAIDX_OK;
+}
+
+// The paged key and value caches; `empty`: a call without rows, whose pointers may be NULL.
+dsaidx_status kv_caches_check(const void* k_cache, const float* k_scale, const void* v_cache, const float* v_scale,
+                              int cache_dtype, int num_pages, int G, int D, int page_size, int max_pages_per_seq,
+                              bool empty) {
+    if (D < 1 || page_size < 1 || num_pages < 1)
+        return fail(DSAIDX_ERR_SHAPE, "D=%d page_size=%d num_pages=%d", D, page_size, num_pages);
+    if (cache_dtype != DSAIDX_F32 && cache_dtype != DSAIDX_BF16 && cache_dtype != DSAIDX_FP8_E4M3)
+        return fail(DSAIDX_ERR_DTYPE, "cache_dtype=%d", cache_dtype);
+    if (cache_dtype == DSAIDX_F32) return fail(DSAIDX_ERR_UNSUPPORTED, "the caches must be bf16 or fp8");
+    if (D != 64 && D != 128) return fail(DSAIDX_ERR_UNSUPPORTED, "D=%d (64 or 128)", D);
+    if (G > kMaxKvHeads) return fail(DSAIDX_ERR_UNSUPPORTED, "G=%d > %d", G, kMaxKvHeads);
+    if (page_size != 64) return fail(DSAIDX_ERR_UNSUPPORTED, "page_size=%d (64)", page_size);
+    // (rows of a pool are counted in 31 bits, positions of a table in 27)
+    if ((int64_t)max_pages_per_seq * page_size > kMaxLatentTokens ||
+        (int64_t)num_pages * G * page_size > 0x7FFFFFFF)
+        return fail(DSAIDX_ERR_UNSUPPORTED, "max_pages_per_seq=%d num_pages=%d G=%d (tables of at most %d tokens, pools "
+                    "of less than 2^31 rows)", max_pages_per_seq, num_pages, G, kMaxLatentTokens);
+    if (empty) return DSAIDX_OK;
+    if (!k_cache) return fail(DSAIDX_ERR_NULL, "k_cache is NULL");
+    if (!v_cache) return fail(DSAIDX_ERR_NULL, "v_cache is NULL");
+    const bool fp8 = cache_dtype == DSAIDX_FP8_E4M3;
+    if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr))
+        return fail(DSAIDX_ERR_SHAPE, "k_scale and v_scale go with fp8 caches, NULL with bf16 ones");
+    if (!aligned16(k_cache) || !aligned16(v_cache))
+        return fail(DSAIDX_ERR_UNSUPPORTED, "k_cache and v_cache must be 16-byte aligned");
+    return DSAIDX_OK;
+}
+
+// Every row of [T][heads] starts at 16 bytes (`per16` elements).
+bool heads_ok(const void* p, int64_t stride, int64_t head_stride, int T, int heads, int per16) {
+    return aligned16(p) && (T <= 1 || stride % per16 == 0) && (heads <= 1 || head_stride % per16 == 0);
+}
+
+}  // namespace
+
+extern "C" {
+
+dsaidx_status indexer_kv_append_rope(const void* k, int64_t k_stride, int64_t k_head_stride, const void* v,
+                                     int64_t v_stride, int64_t v_head_stride, int in_dtype, const float* cos_sin,
+                                     int rope_len, int rope_dim, int interleaved, const int32_t* seq_ids,
+                                     const int32_t* positions, const int32_t* block_table, int B,
+                                     int max_pages_per_seq, void* k_cache, float* k_scale, void* v_cache,
+                                     float* v_scale, int cache_dtype, int num_pages, int T, int G, int D,
+                                     int page_size, void* stream) {
+    g_err[0] = 0;
+    if (T < 0 || B < 1 || max_pages_per_seq < 1 || G < 1 || (cos_sin && (rope_len < 1 || rope_dim < 1)))
+        return fail(DSAIDX_ERR_SHAPE, "T=%d B=%d max_pages_per_seq=%d G=%d rope_len=%d rope_dim=%d", T, B,
+                    max_pages_per_seq, G, rope_len, rope_dim);
+    if (in_dtype != DSAIDX_F32 && in_dtype != DSAIDX_BF16 && in_dtype != DSAIDX_FP8_E4M3)
+        return fail(DSAIDX_ERR_DTYPE, "in_dtype=%d", in_dtype);
+    if (in_dtype == DSAIDX_FP8_E4M3) return fail(DSAIDX_ERR_UNSUPPORTED, "new rows must be bf16 or f32");
+    const dsaidx_status st = kv_caches_check(k_cache, k_scale, v_cache, v_scale, cache_dtype, num_pages, G, D,
+                                             page_size, max_pages_per_seq, T == 0);
+    if (st != DSAIDX_OK) return st;
+    if (cos_sin && (rope_dim % 16 != 0 || rope_dim > D))
+        return fail(DSAIDX_ERR_UNSUPPORTED, "rope_dim=%d (a multiple of 16, at most D)", rope_dim);
+    // (up to 32 lanes a token and head, and a launch holds less than 2^32 threads)
+    if ((int64_t)T * G > 1 << 26) return fail(DSAIDX_ERR_UNSUPPORTED, "T * G = %lld > 2^26", (long long)T * G);
+    if (T == 0) return DSAIDX_OK;
+    if (!k) return fail(DSAIDX_ERR_NULL, "k is NULL");
+    if (!v) return fail(DSAIDX_ERR_NULL, "v is NULL");
+    if (!seq_ids) return fail(DSAIDX_ERR_NULL, "seq_ids is NULL");
+    if (!positions) return fail(DSAIDX_ERR_NULL, "positions is NULL");
+    if (!block_table) return fail(DSAIDX_ERR_NULL, "block_table is NULL");
+    const int per16 = in_dtype == DSAIDX_BF16 ? 8 : 4;  // elements of 16 bytes
+    if (!heads_ok(k, k_stride, k_head_stride, T, G, per16) || !heads_ok(v, v_stride, v_head_stride, T, G, per16) ||
+        !aligned16(cos_sin))
+        return fail(DSAIDX_ERR_UNSUPPORTED, "rows of k and v and cos_sin must be 16-byte aligned");
+    dsaidx::KvAppendArgs a{};
+    a.in[0] = {k, k_stride, k_head_stride};
+    a.in[1] = {v, v_stride, v_head_stride};
+    a.cos_sin = cos_sin;
+    a.seq_ids = seq_ids;
+    a.positions = positions;
+    a.block_table = block_table;
+    a.cache[0] = k_cache;
+    a.cache[1] = v_cache;
+    a.scale[0] = k_scale;
+    a.scale[1] = v_scale;
+    a.T = T;
+    a.G = G;
+    a.B = B;
+    a.max_pages = max_pages_per_seq;
+    a.num_pages = num_pages;
+    a.R = cos_sin ? rope_dim : 0;
+    a.rope_len = cos_sin ? rope_len : 0x7FFFFFFF;
+    a.pairs = interleaved != 0;
+    const hipError_t e = dsaidx::launch_kv_append_rope(a, D, in_dtype == DSAIDX_F32, cache_dtype == DSAIDX_FP8_E4M3,
+                                                       (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "indexer_kv_append_rope");
+    return DSAIDX_OK;
+}
+
+dsaidx_status indexer_prompt_attention(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k,
+                                       int64_t k_stride, int64_t k_head_stride, const void* v, int64_t v_stride,
+                                       int64_t v_head_stride, int dtype, const int32_t* cu_seqlens, int B, int T,
+                                       int H, int G, int D, int V, float scale, void* out, float* lse, void* stream) {
+    g_err[0] = 0;
+    if (T < 0 || B < 1) return fail(DSAIDX_ERR_SHAPE, "T=%d B=%d", T, B);
+    if (dtype != DSAIDX_F32 && dtype != DSAIDX_BF16 && dtype != DSAIDX_FP8_E4M3)
+        return fail(DSAIDX_ERR_DTYPE, "dtype=%d", dtype);
+    if (dtype != DSAIDX_BF16) return fail(DSAIDX_ERR_UNSUPPORTED, "q, k and v must be bf16");
+    const dsaidx_status st = kv_heads_check(H, G, scale);
+    if (st != DSAIDX_OK) return st;
+    if (!((D == 64 && V == 64) || ((D == 128 || D == 192) && V == 128)))
+        return fail(DSAIDX_ERR_UNSUPPORTED, "D=%d V=%d (64 and 64, 128 and 128, or 192 and 128)", D, V);
+    // (a launch holds less than 2^32 threads)
+    if (dsaidx::prompt_threads(T, B, H) >= (int64_t)1 << 32)
+        return fail(DSAIDX_ERR_UNSUPPORTED, "T=%d B=%d H=%d: more than 2^32 threads", T, B, H);
+    if (T == 0) return DSAIDX_OK;
+    if (!q) return fail(DSAIDX_ERR_NULL, "q is NULL");
+    if (!k) return fail(DSAIDX_ERR_NULL, "k is NULL");
+    if (!v) return fail(DSAIDX_ERR_NULL, "v is NULL");
+    if (!cu_seqlens) return fail(DSAIDX_ERR_NULL, "cu_seqlens is NULL");
+    if (!out) return fail(DSAIDX_ERR_NULL, "out is NULL");
+    if (!heads_ok(q, q_stride, q_head_stride, T, H, 8) || !heads_ok(k, k_stride, k_head_stride, T, G, 8) ||
+        !heads_ok(v, v_stride, v_head_stride, T, G, 8) || !aligned16(out))
+        return fail(DSAIDX_ERR_UNSUPPORTED, "rows of q, k and v and out must be 16-byte aligned");
+    // (a tile's rows are addressed with 32 bits)
+    if (k_stride < 0 || v_stride < 0 || k_stride >= 1 << 24 || v_stride >= 1 << 24)
+        return fail(DSAIDX_ERR_UNSUPPORTED, "k_stride=%lld v_stride=%lld (in [0, 2^24))", (long long)k_stride,
+                    (long long)v_stride);
+    dsaidx::PromptArgs a{};
+    a.q = {q, q_stride, q_head_stride};
+    a.k = {k, k_stride, k_head_stride};
+    a.v = {v, v_stride, v_head_stride};
+    a.cu = cu_seqlens;
+    a.out = reinterpret_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.scale_log2 = scale * kLog2E;
+    a.T = T;
+    a.H = H;
+    a.G = G;
+    a.B = B;
+    const hipError_t e = dsaidx::launch_prompt_attention(a, D, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "indexer_prompt_attention");
+    return DSAIDX_OK;
+}
+
+size_t indexer_kv_attention_decode_workspace_bytes(int B, int H, int G, int D, int max_context_len, int topk,
+                                                   int cache_dtype) {
+    if (B < 1 || G < 1 || H < G || H > kMaxKvHeads || (D != 64 && D != 128) || max_context_len < 0 || topk < 0) return 0;
+    return dsaidx::kv_decode_workspace_bytes(B, H, G, D, max_context_len, topk, cache_dtype == DSAIDX_FP8_E4M3);
+}
+
+dsaidx_status indexer_kv_attention_decode(const void* q, int q_dtype, const void* k_cache, const float* k_scale,
+                                          const void* v_cache, const float* v_scale, int cache_dtype,
+                                          const int32_t* block_table, int max_pages_per_seq, int num_pages,
+                                          const int32_t* context_lens, int max_context_len, const int32_t* topk_idx,
+                                          int topk, int B, int H, int G, int D, int page_size, float scale, void* out,
+                                          float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    if (B < 0 || max_pages_per_seq < 1) return fail(DSAIDX_ERR_SHAPE, "B=%d max_pages_per_seq=%d", B, max_pages_per_seq);
+    if (q_dtype != DSAIDX_F32 && q_dtype != DSAIDX_BF16 && q_dtype != DSAIDX_FP8_E4M3)
+        return fail(DSAIDX_ERR_DTYPE, "q_dtype=%d", q_dtype);
+    if (q_dtype != DSAIDX_BF16) return fail(DSAIDX_ERR_UNSUPPORTED, "queries must be bf16");
+    dsaidx_status st = kv_heads_check(H, G, scale);
+    if (st != DSAIDX_OK) return st;
+    st = kv_caches_check(k_cache, k_scale, v_cache, v_scale, cache_dtype, num_pages, G, D, page_size,
+                         max_pages_per_seq, B == 0);
+    if (st != DSAIDX_OK) return st;
+    if (max_context_len < 0 || (int64_t)max_context_len > (int64_t)max_pages_per_seq * page_size)
+        return fail(DSAIDX_ERR_SHAPE, "max_context_len=%d > max_pages_per_seq*page_size=%lld", max_context_len,
+                    (long long)max_pages_per_seq * page_size);
+    if ((topk_idx != nullptr) != (topk > 0))
+        return fail(DSAIDX_ERR_SHAPE, "topk=%d: at least 1 with topk_idx, 0 without", topk);
+    if (topk > kMaxL) return fail(DSAIDX_ERR_UNSUPPORTED, "topk=%d > %d", topk, kMaxL);
+    if ((int64_t)B * H > 1 << 23) return fail(DSAIDX_ERR_UNSUPPORTED, "B * H = %lld > 2^23", (long long)B * H);
+    if (B == 0) return DSAIDX_OK;
+    if (!q) return fail(DSAIDX_ERR_NULL, "q is NULL");
+    if (!block_table) return fail(DSAIDX_ERR_NULL, "block_table is NULL");
+    if (!context_lens) return fail(DSAIDX_ERR_NULL, "context_lens is NULL");
+    if (!out) return fail(DSAIDX_ERR_NULL, "out is NULL");
+    if (!aligned16(q) || !aligned16(out)) return fail(DSAIDX_ERR_UNSUPPORTED, "q and out must be 16-byte aligned");
+    const size_t need = indexer_kv_attention_decode_workspace_bytes(B, H, G, D, max_context_len, topk, cache_dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(DSAIDX_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    if (need > 0 && !aligned16(workspace)) return fail(DSAIDX_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
+    dsaidx::KvDecodeArgs a{};
+    a.q = reinterpret_cast<const uint16_t*>(q);
+    a.cache[0] = k_cache;
+    a.cache[1] = v_cache;
+    a.scale[0] = k_scale;
+    a.scale[1] = v_scale;
+    a.block_table = block_table;
+    a.lens = context_lens;
+    a.idx = topk_idx;
+    a.out = reinterpret_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.workspace = workspace;
+    a.scale_log2 = scale * kLog2E;
+    a.B = B;
+    a.H = H;
+    a.G = G;
+    a.max_pages = max_pages_per_seq;
+    a.num_pages = num_pages;
+    a.max_ctx = max_context_len;
+    a.K = topk;
+    const hipError_t e = dsaidx::launch_kv_decode(a, D, cache_dtype == DSAIDX_FP8_E4M3, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "indexer_kv_attention_decode");
+    return DSAIDX_OK;
 }
 
 dsaidx_status dsaidx_probe_mfma(int kind, int blocks, int iters, float* out, void* stream) {

@@ -1,0 +1,443 @@
+// Causal attention over whole prompts: packed sequences of different lengths,
+// H query heads over G key/value heads (query head h reads head h / (H / G)).
+//
+//   S[i, j] = scale * q[i] . k[j]  for the rows j <= i of i's sequence
+//   out[i] = sum_j softmax_j(S) v[j],  lse[i] = log sum_j exp S[i, j]
+//
+// The attention of prompts that are too short for a selection ("Study MLA
+// Indexer", the last of the "three whys": dense attention where the prompt has
+// no more rows than the selection takes).
+//
+// One workgroup takes a head and a block of query rows, 32 to a wave, which
+// carries them alone through both products:
+//   S^T (64 keys x 32 rows) = K Q^T, its queries in registers;
+//   O^T (V columns x 32 rows) += V^T P^T.
+// The first product leaves a lane with row lane % 32 and keys 4h .. 4h+3 of
+// every eight (h = lane / 32), which is the second one's operand when its 16
+// keys are counted as 4h .. 4h+3 of two eights: P never leaves its registers,
+// and the values are read transposed in that order.  The softmax's factors are
+// per lane; the exponent's reference moves when a score passes it by 2^kSlack.
+// Sums are fp32; P is rounded to bf16, because the matrix cores take both
+// operands of the second product in one type: an output is off by at most 2^-8
+// of sum P |v| for that, beside its own rounding.  P's sum is taken before the
+// rounding, so that lse does not have it.
+//
+// Tiles of 64 keys and values are copied to LDS while the tile before is
+// computed.  A wave walks its keys from its own rows down to the first: the one
+// tile that the causal mask cuts comes first, while the sums are still zero.
+// There, and only there, a masked row can meet a value that is not finite, as 0
+// times it in the product; the sums then are not finite either, and that tile's
+// values are taken again with such elements apart.
+#include "device_once.h"
+#include "kv.h"
+#include "tile_copy.h"
+
+namespace dsaidx {
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+constexpr int kTile = 64;       // keys of a tile
+constexpr int kWaves = 4;
+constexpr int kRows = 32 * kWaves;
+constexpr int kAhead = 4;       // operand reads in flight
+constexpr float kFar = 0x1p30f; // references of this size are taken off rounded scores
+
+// A tile's rows lie one behind another in LDS, their 16-byte pieces permuted
+// within each 8 (or 16, where a row has a multiple of that) by the row's number.
+// The 64 banks serve 16 lanes of a 16-byte read at once (rows of 16 different
+// numbers mod 16), 32 lanes of an 8-byte one (64 bytes of four consecutive rows):
+// with this permutation both use every bank once.
+template <int P>
+__device__ __forceinline__ int permute(int row) {
+    return P % 16 == 0 ? (row & 3) << 2 | (row >> 2 & 3) : (row >> 1 & 1) << 2 | (row >> 2 & 3);
+}
+
+template <typename T>
+__device__ __forceinline__ __attribute__((address_space(3))) T* lds_pointer(uint32_t at) {
+    return (__attribute__((address_space(3))) T*)(uintptr_t)at;
+}
+template <typename T>
+__device__ __forceinline__ T lds_read(uint32_t at) {
+    return *lds_pointer<T>(at);
+}
+
+// A wave's copies of a tile of rows of P pieces: N of 1024 bytes, a multiple of
+// 8 rows each kBase.  A lane's place in its source row is found once for kBase
+// copies; the next ones are a number of rows on, and permuted by one bit more.
+template <int P, int N>
+struct Copies {
+    static constexpr int kBase = P == 24 ? 3 : 1, kStep = P == 16 ? 4 : 8, kBit = P == 16 ? 16 : 32;
+    static_assert(N % kBase == 0 && (N / kBase <= (P == 16 ? 4 : 2)), "the permutation's bits");
+    int row[kBase];       // of the tile
+    uint32_t piece[kBase];
+    int64_t stride;       // bytes
+    uint32_t first;       // byte of the tile in LDS
+    __device__ __forceinline__ Copies(int wave, int lane, int64_t row_stride) {
+        stride = 2 * row_stride;
+        first = (uint32_t)(wave * N * 1024);
+#pragma unroll
+        for (int i = 0; i < kBase; ++i) {
+            const int at = (wave * N + i) * 64 + lane;
+            row[i] = at / P;
+            piece[i] = 16u * (uint32_t)(at % P ^ permute<P>(at / P));
+        }
+    }
+    __device__ __forceinline__ void tile(const uint16_t* src, uint32_t lds) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            copy_to_lds(reinterpret_cast<const char*>(src) + i / kBase * kStep * stride,
+                        (piece[i % kBase] ^ (uint32_t)(i / kBase * kBit)) + (uint32_t)row[i % kBase] * (uint32_t)stride,
+                        lds + first + i * 1024);
+    }
+    // The same where row `last` is the last one: rows behind it are that row again.
+    __device__ __forceinline__ void last_tile(const uint16_t* src, uint32_t lds, int last) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            copy_to_lds(src, (piece[i % kBase] ^ (uint32_t)(i / kBase * kBit)) +
+                                 (uint32_t)min(row[i % kBase] + i / kBase * kStep, last) * (uint32_t)stride,
+                        lds + first + i * 1024);
+    }
+};
+
+// Rows of a block of one sequence.
+struct Block {
+    int start, len;   // the sequence
+    int r0;           // the block's first row in it
+    bool pad;         // rows of no sequence, behind the last one
+};
+
+// Block `item` of all, false: there are fewer.  The rows behind the last
+// sequence count as one more.  With few sequences the blocks come longest first
+// (a block's work grows with its first row), so that the last ones to start are
+// short; else sequence by sequence, which takes one pass over them.
+__device__ __forceinline__ bool find_block(const PromptArgs& a, int item, Block& out) {
+    const int lane = lane_id(), segments = a.B + 1;
+    auto load = [&](int b, int& s, int& e) {
+        s = e = 0;
+        if (b < segments) {
+            s = min(max(a.cu[b], 0), a.T);
+            e = b < a.B ? min(max(a.cu[b + 1], s), a.T) : a.T;
+        }
+    };
+    int s, e, level, found;
+    if (segments <= kWave) {
+        load(lane, s, e);
+        const int n = (e - s + kRows - 1) / kRows;
+        if (item >= (int)wave_sum((uint32_t)n)) return false;
+        // largest level with more than `item` blocks at or above it
+        int lo = 0, hi = (a.T + kRows - 1) / kRows;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if ((int)wave_sum((uint32_t)max(n - mid, 0)) > item) lo = mid;
+            else hi = mid;
+        }
+        level = lo;
+        const int rank = item - (int)wave_sum((uint32_t)max(n - level - 1, 0));
+        const uint64_t mask = wave_ballot(n > level);
+        found = __builtin_ctzll(wave_ballot(n > level && lanes_below(mask) == rank));
+        out.pad = found == a.B;
+    } else {
+        int base = 0, at = 0;
+        uint32_t incl;
+        for (;; at += kWave) {
+            if (at >= segments) return false;
+            load(at + lane, s, e);
+            incl = wave_incl_scan((uint32_t)((e - s + kRows - 1) / kRows));
+            const int all = __builtin_amdgcn_readlane((int)incl, kWave - 1);
+            if (base + all > item) break;
+            base += all;
+        }
+        found = __builtin_ctzll(wave_ballot(base + (int)incl > item));
+        level = base + __builtin_amdgcn_readlane((int)incl, found) - 1 - item;
+        out.pad = at + found == a.B;
+    }
+    out.start = __builtin_amdgcn_readlane(s, found);
+    out.len = __builtin_amdgcn_readlane(e, found) - out.start;
+    out.r0 = level * kRows;
+    return true;
+}
+
+// bf16 pairs: 1.0 where an element is not finite and of that sign (NaN: of both).
+__device__ __forceinline__ uint32_t not_finite(uint32_t x, uint32_t sign) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 32; i += 16) {
+        const uint32_t u = x >> i & 0xFFFFu;
+        if ((u & 0x7FFFu) > 0x7F80u || u == (sign | 0x7F80u)) r |= 0x3F80u << i;
+    }
+    return r;
+}
+__device__ __forceinline__ uint32_t finite(uint32_t x) {
+    if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+    if ((x & 0x7F800000u) == 0x7F800000u) x &= 0xFFFFu;
+    return x;
+}
+
+template <int D, int V>
+__global__ void __launch_bounds__(64 * kWaves, 2)
+prompt_attention_kernel(PromptArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int KP = D / 8, VP = V / 8;                       // 16-byte pieces of a row
+    constexpr int kKeyB = kTile * D * 2, kTileB = kKeyB + kTile * V * 2;
+    constexpr int KI = kKeyB / 1024 / kWaves, VI = kTile * V * 2 / 1024 / kWaves;  // copies of a wave
+    constexpr int KS = D / 16, MT = V / 32;                     // steps of the first product, blocks of the second
+    const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
+    const int n = lane & 31, h = lane >> 5;
+
+    // heads of one key/value head go to one XCD (workgroups go to the 8 in turn)
+    const int j = (int)(blockIdx.x % (unsigned)a.H);
+    const int head = a.H % 8 == 0 ? (j & 7) * (a.H >> 3) + (j >> 3) : j;
+    Block blk;
+    if (!find_block(a, (int)(blockIdx.x / (unsigned)a.H), blk)) return;
+    const int rows = min(kRows, blk.len - blk.r0);
+    const int64_t out_row = (int64_t)(blk.start + blk.r0) * a.H + head;   // of [T][H]
+    if (blk.pad) {
+        for (int i = (int)threadIdx.x; i < rows * VP; i += 64 * kWaves)
+            *reinterpret_cast<v4i*>(a.out + (out_row + (int64_t)(i / VP) * a.H) * V + 8 * (i % VP)) = v4i{0, 0, 0, 0};
+        if (a.lse)
+            for (int i = (int)threadIdx.x; i < rows; i += 64 * kWaves)
+                a.lse[out_row + (int64_t)i * a.H] = -__builtin_inff();
+        return;
+    }
+    const int g = head / (a.H / a.G);
+    const uint16_t* kbase = reinterpret_cast<const uint16_t*>(a.k.p) + blk.start * a.k.row + g * a.k.head;
+    const uint16_t* vbase = reinterpret_cast<const uint16_t*>(a.v.p) + blk.start * a.v.row + g * a.v.head;
+
+    // ---- queries: B operand of 32 rows x 16 columns ----
+    const int r0 = blk.r0 + 32 * wave;   // this wave's first row in the sequence
+    const bool active = 32 * wave < rows;
+    v8bf Q[KS];
+    {
+        const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q.p) +
+                             (blk.start + (int64_t)min(r0 + n, blk.len - 1)) * a.q.row + head * a.q.head + 8 * h;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) Q[ks] = *reinterpret_cast<const v8bf*>(qp + 16 * ks);
+        if (a.scale_log2 < 0.f)   // the products then take the scale's magnitude
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                v4i u = __builtin_bit_cast(v4i, Q[ks]);
+                u ^= (int)0x80008000;
+                Q[ks] = __builtin_bit_cast(v8bf, u);
+            }
+    }
+    // (never 0: a score of -inf has to stay one)
+    const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
+
+    // ---- copies: a wave's part of a tile, 1024 bytes each ----
+    const uint32_t lds0 = lds_address(smem);
+    Copies<KP, KI> kc(wave, lane, a.k.row);
+    Copies<VP, VI> vc(wave, lane, a.v.row);
+    auto stage = [&](int t, int buf) {
+        kc.tile(kbase + (int64_t)kTile * t * a.k.row, lds0 + buf * kTileB);
+        vc.tile(vbase + (int64_t)kTile * t * a.v.row, lds0 + buf * kTileB + kKeyB);
+    };
+
+    v16f O[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) O[mt][i] = 0.f;
+    // the reference starts below every score that is not -inf, so that a row's first one moves it
+    float m = -3.402823466e38f, l = 0.f;
+    bool far = false;
+
+    // operand addresses in the first buffer; a step's columns differ in bits of the permuted piece
+    constexpr int KPX = KP % 16 == 0 ? 16 : 8;
+    const uint32_t k_at = lds0 + n * (2 * D) + 16 * (h ^ permute<KP>(n));
+    const int v_row = 4 * h + (lane >> 2 & 3);
+    const uint32_t v_at = lds0 + kKeyB + v_row * (2 * V) +
+                          16 * ((2 * (lane >> 4 & 1) + (lane >> 1 & 1)) ^ permute<VP>(v_row)) + 8 * (lane & 1);
+
+    const int t_mine = r0 / kTile;   // the tile that the mask cuts for this wave's rows
+    const int t_first = (blk.r0 + rows - 1) / kTile;
+    int buf = 0;
+    // (only the last tile can pass the sequence's last row)
+    kc.last_tile(kbase + (int64_t)kTile * t_first * a.k.row, lds0, blk.len - 1 - kTile * t_first);
+    vc.last_tile(vbase + (int64_t)kTile * t_first * a.v.row, lds0 + kKeyB, blk.len - 1 - kTile * t_first);
+    for (int t = t_first; t >= 0; --t, buf ^= 1) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the tile
+        tile_barrier();
+        if (t > 0) stage(t - 1, buf ^ 1);
+        if (!active || t > t_mine) continue;
+        // ---- scores ----
+        const uint32_t kp = k_at + buf * kTileB, vp = v_at + buf * kTileB;
+        auto read_k = [&](int f) {   // step f: columns 16 (f / 2) .., keys 32 (f % 2) ..
+            const int c = 2 * (f / 2);
+            return lds_read<v8bf>((kp ^ (16 * (c % KPX))) + 16 * (c / KPX * KPX) + f % 2 * (64 * D));
+        };
+        v16f S[2];
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[kt][i] = 0.f;
+        v8bf K[kAhead];
+#pragma unroll
+        for (int f = 0; f < kAhead; ++f) K[f] = read_k(f);
+#pragma unroll
+        for (int f = 0; f < 2 * KS; ++f) {
+            __builtin_amdgcn_sched_barrier(0);
+            S[f % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K[f % kAhead], Q[f / 2], S[f % 2], 0, 0, 0);
+            if (f + kAhead < 2 * KS) K[f % kAhead] = read_k(f + kAhead);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // ---- softmax ----
+        if (t == t_mine) {
+            const int mine = (r0 & (kTile - 1)) + n;
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (32 * kt + 8 * (i / 4) + 4 * h + i % 4 > mine) S[kt][i] = -__builtin_inff();
+        }
+        float top = S[0][0];
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, S[kt][i]);
+        top *= scale;
+        if (wave_ballot(top > m + kSlack)) {
+            // a row's reference moves to these keys' maximum where that is so far above it (the
+            // rows beside it keep theirs: no row's result depends on another's)
+            top = fmaxf(top, __shfl_xor(top, 32, kWave));
+            const float to = top > m + kSlack ? top : m;
+            const float f = __builtin_amdgcn_exp2f(m - to);
+            m = to;
+            l *= f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) O[mt] *= f;
+            far = wave_ballot(fabsf(m) >= kFar) != 0;
+        }
+        if (far) {
+#pragma clang fp contract(off)
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float x = S[kt][i] * scale;
+                    S[kt][i] = __builtin_amdgcn_exp2f(fabsf(m) >= kFar ? x - m : fmaf(S[kt][i], scale, -m));
+                }
+        } else {
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[kt][i] = __builtin_amdgcn_exp2f(fmaf(S[kt][i], scale, -m));
+        }
+        v8bf P[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            v4i u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = S[s / 2][8 * (s % 2) + 2 * i], y = S[s / 2][8 * (s % 2) + 2 * i + 1];
+                l += x;
+                l += y;
+                u[i] = (int)pack_bf16(x, y);
+            }
+            P[s] = __builtin_bit_cast(v8bf, u);
+        }
+        // ---- values: A operand of 32 columns x 16 keys ----
+        auto read_v = [&](int f) {   // step f: columns 32 (f % MT) .., keys 16 (f / MT) ..
+            const uint32_t at = vp ^ (64 * (f % MT));
+            const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>(at + f / MT * (32 * V)));
+            const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>((at ^ 32) + f / MT * (32 * V) + 16 * V));
+            return __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        v8bf W[kAhead];
+#pragma unroll
+        for (int f = 0; f < kAhead; ++f) W[f] = read_v(f);
+#pragma unroll
+        for (int f = 0; f < 4 * MT; ++f) {
+            __builtin_amdgcn_sched_barrier(0);
+            O[f % MT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(W[f % kAhead], P[f / MT], O[f % MT], 0, 0, 0);
+            if (f + kAhead < 4 * MT) W[f % kAhead] = read_v(f + kAhead);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (t == t_mine) {
+            float z = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) z = fmaf(O[mt][i], 0.f, z);
+            if (wave_ballot(z != z)) {
+                // once more: finite elements as before, the others by which rows see them
+                const int mine = (r0 & (kTile - 1)) + n;
+                v8bf see[4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    v4i u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = 16 * s + 8 * (i / 2) + 4 * h + 2 * (i % 2);
+                        u[i] = (key <= mine ? 0x3F80 : 0) | (key + 1 <= mine ? 0x3F800000 : 0);
+                    }
+                    see[s] = __builtin_bit_cast(v8bf, u);
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    v16f up, down;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) O[mt][i] = up[i] = down[i] = 0.f;
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const v4i w = __builtin_bit_cast(v4i, read_v(MT * s + mt));
+                        v4i f, p, q;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            f[i] = (int)finite((uint32_t)w[i]);
+                            p[i] = (int)not_finite((uint32_t)w[i], 0);
+                            q[i] = (int)not_finite((uint32_t)w[i], 0x8000u);
+                        }
+                        O[mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, f), P[s], O[mt], 0, 0, 0);
+                        up = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, p), see[s], up, 0, 0, 0);
+                        down = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, q), see[s], down, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (up[i] > 0.f) O[mt][i] += __builtin_inff();
+                        if (down[i] > 0.f) O[mt][i] -= __builtin_inff();
+                    }
+                }
+            }
+        }
+    }
+
+    // ---- write: columns 4h .. 4h+3 of every eight of row n ----
+    l += __shfl_xor(l, 32, kWave);
+    if (32 * wave + n >= rows) return;
+    const int64_t r = out_row + (int64_t)(32 * wave + n) * a.H;
+    const float inv = 1.f / l;
+    uint16_t* out = a.out + r * V + 4 * h;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint2*>(out + 32 * mt + 8 * i) =
+                l == 0.f ? uint2{0, 0}
+                         : uint2{pack_bf16(O[mt][4 * i] * inv, O[mt][4 * i + 1] * inv),
+                                 pack_bf16(O[mt][4 * i + 2] * inv, O[mt][4 * i + 3] * inv)};
+    if (a.lse && h == 0) a.lse[r] = l == 0.f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945f;
+}
+
+template <int D, int V>
+hipError_t run(const PromptArgs& a, hipStream_t stream) {
+    static PerDevice<int> once;
+    constexpr int lds = 2 * kTile * 2 * (D + V);
+    const hipError_t e = set_lds_limit(once, (const void*)prompt_attention_kernel<D, V>, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((prompt_attention_kernel<D, V>), dim3((unsigned)(prompt_threads(a.T, a.B, a.H) / (64 * kWaves))),
+                       dim3(64 * kWaves), lds, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// At most floor(T / kRows) whole blocks and a rest of each of the B sequences and of the rows behind them.
+int64_t prompt_threads(int T, int B, int H) { return ((int64_t)T / kRows + B + 1) * H * (64 * kWaves); }
+
+hipError_t launch_prompt_attention(const PromptArgs& a, int D, hipStream_t stream) {
+    if (a.T <= 0) return hipSuccess;
+    return D == 64 ? run<64, 64>(a, stream) : D == 128 ? run<128, 128>(a, stream) : run<192, 128>(a, stream);
+}
+
+}  // namespace dsaidx

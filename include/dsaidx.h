@@ -485,6 +485,129 @@ size_t indexer_latent_attention_shared_workspace_bytes(int B, int H, int E, int 
                                                        int max_context_len, int latent_dtype);
 
 /*
+ * indexer_kv_append_rope -- the write of a layer's paged key and value caches
+ * where its attention has G key/value heads of its own: T new tokens' key rows,
+ * rotated by their positions, and value rows, in one launch.
+ *
+ * Passage: "Study MLA Indexer", the data-flow diagram and the notes on its two
+ * caches (a cache is written before the attention that reads it); grouped
+ * heads: the same page's comparison with other schemes.  The first rope_dim
+ * columns of every key row are rotated as indexer_cache_append_rope rotates a
+ * latent row's last ones (pair i: columns (2i, 2i + 1) with `interleaved`
+ * nonzero, (i, i + rope_dim/2) else); values are not.  bf16 rows are rounded once
+ * to nearest even; fp8 rows are quantised as indexer_kcache_append does, one
+ * scale per row of D columns, and keep NaNs as the codes 0x7F or 0xFF.
+ *
+ *   k, v         [T][G] rows of D elements in in_dtype (BF16 or F32); row
+ *                (t, g) starts t * stride + g * head_stride elements in
+ *   cos_sin      [rope_len][rope_dim] fp32 as indexer_cache_append_rope, or
+ *                NULL: keys are not rotated (rope_len and rope_dim unused)
+ *   seq_ids, positions, block_table: as indexer_kcache_append.  A token whose
+ *                sequence lies outside [0, B), whose position lies outside the
+ *                table or (with cos_sin) rope_len, or whose page id lies outside
+ *                [0, num_pages) is skipped
+ *   k_cache, v_cache  [num_pages][G][page_size][D] in cache_dtype (BF16, or
+ *                FP8_E4M3 codes with k_scale, v_scale [num_pages][G][page_size]
+ *                fp32; NULL with BF16), updated in place
+ * Slots no token addresses are not touched.  Two tokens of one call with the
+ * same (sequence, position) leave that slot's contents undefined.  T = 0 is a
+ * no-op.  No workspace.
+ *
+ * Supported: D 64 or 128, G <= 128, page_size = 64, T * G <= 2^26, rope_dim a
+ * multiple of 16 up to D; rows, cos_sin and caches 16-byte aligned; tables of at
+ * most 2^27 tokens, pools of less than 2^31 rows.
+ */
+dsaidx_status indexer_kv_append_rope(const void* k, int64_t k_stride, int64_t k_head_stride, const void* v,
+                                     int64_t v_stride, int64_t v_head_stride, int in_dtype, const float* cos_sin,
+                                     int rope_len, int rope_dim, int interleaved, const int32_t* seq_ids,
+                                     const int32_t* positions, const int32_t* block_table, int B,
+                                     int max_pages_per_seq, void* k_cache, float* k_scale, void* v_cache,
+                                     float* v_scale, int cache_dtype, int num_pages, int T, int G, int D,
+                                     int page_size, void* stream);
+
+/*
+ * indexer_prompt_attention -- causal attention over whole prompts: B packed
+ * sequences of different lengths, H query heads over G key/value heads.
+ *
+ * Passage: "Study MLA Indexer", the last of the "three whys" (a prompt with no
+ * more rows than the selection takes is attended to densely); "From principle to
+ * code", section 3 (the lower-triangular mask keeps j <= i).  With row i of a
+ * sequence and query head h, which reads key/value head h / (H / G):
+ *     S[i,j] = scale * q[i,h] . k[j]        for the rows j <= i of its sequence
+ *     out[i,h] = sum_j softmax_j(S) v[j],  lse[i,h] = log sum_j exp S[i,j]
+ * Scores, sums and the softmax's statistics are fp32; the probabilities enter
+ * the second product rounded to bf16 (lse without that rounding); out is rounded
+ * once to bf16.  What a row does not see does not reach it, whatever it holds
+ * (infinities, NaN).
+ *
+ *   q, k, v      [T][H], [T][G] rows of D elements and [T][G] rows of V, in
+ *                dtype (BF16); row (t, h) starts t * stride + h * head_stride
+ *                elements in
+ *   cu_seqlens   [B+1] int32 (device): sequence b is rows cu_seqlens[b] ..
+ *                cu_seqlens[b+1]-1; cu_seqlens[0] = 0, nondecreasing (a sequence
+ *                may have none).  Rows from cu_seqlens[B] on belong to none: their
+ *                out is 0 and their lse -inf
+ *   T            rows, at least cu_seqlens[B]
+ *   out          out [T][H][V] bf16;  lse  out [T][H] fp32 or NULL
+ * No workspace.  T = 0 is a no-op.
+ *
+ * Supported: (D, V) = (64, 64), (128, 128) or (192, 128), H <= 128 a multiple of
+ * G, rows and out 16-byte aligned, strides of k and v below 2^24; (T / 128 + B +
+ * 1) * H < 2^24.
+ */
+dsaidx_status indexer_prompt_attention(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k,
+                                       int64_t k_stride, int64_t k_head_stride, const void* v, int64_t v_stride,
+                                       int64_t v_head_stride, int dtype, const int32_t* cu_seqlens, int B, int T,
+                                       int H, int G, int D, int V, float scale, void* out, float* lse, void* stream);
+
+/*
+ * indexer_kv_attention_decode -- one decode step of B sequences over the paged
+ * caches that indexer_kv_append_rope writes: each sequence's new token attends
+ * over every position of its context, or over the positions selected for it.
+ *
+ * Passage: "Lightning Indexer explained", section 2 (decode walkthrough: the
+ * core attention runs over the selected set; section 2.3: a short context is
+ * taken whole); "Study MLA Indexer", the data-flow diagram's last step.  The
+ * same attention as indexer_prompt_attention (heads, rounding), for one query
+ * per sequence.
+ *
+ *   q            [B][H][D] bf16 (q_dtype must be DSAIDX_BF16)
+ *   k_cache, v_cache, k_scale, v_scale: as indexer_kv_append_rope.  fp8 codes
+ *                enter the products exactly; a key's scale multiplies its score,
+ *                a value's its probability
+ *   block_table  [B][max_pages_per_seq] int32 page ids; position s of sequence b
+ *                is page block_table[b][s / page_size], slot s % page_size.  A page
+ *                id outside [0, num_pages) is a page without rows
+ *   context_lens [B] int32 (device), clamped to [0, max_context_len]
+ *   max_context_len  host bound, <= max_pages_per_seq * page_size.  The work is
+ *                cut for contexts of that length
+ *   topk_idx     [B][topk] int32 positions in any order, e.g. the output of
+ *                indexer_decode_paged; an entry outside [0, context length) is no
+ *                row (-1 pads), a position listed twice counts twice.  NULL (and
+ *                topk 0): every position
+ *   out          out [B][H][D] bf16;  lse  out [B][H] fp32 or NULL.  A query
+ *                without a row gives out = 0 and lse = -inf
+ *   workspace    indexer_kv_attention_decode_workspace_bytes(B, H, G, D,
+ *                max_context_len, topk, cache_dtype) bytes of caller-owned device
+ *                memory, 16-byte aligned, scratch (its contents on entry do not
+ *                matter; two calls in flight on one workspace race)
+ * B = 0 is a no-op.
+ *
+ * Supported: D 64 or 128, H <= 128 a multiple of G, page_size = 64, topk <=
+ * 131072, B * H <= 2^23; q, out and caches 16-byte aligned; tables of at most
+ * 2^27 tokens, pools of less than 2^31 rows.
+ */
+dsaidx_status indexer_kv_attention_decode(const void* q, int q_dtype, const void* k_cache, const float* k_scale,
+                                          const void* v_cache, const float* v_scale, int cache_dtype,
+                                          const int32_t* block_table, int max_pages_per_seq, int num_pages,
+                                          const int32_t* context_lens, int max_context_len, const int32_t* topk_idx,
+                                          int topk, int B, int H, int G, int D, int page_size, float scale, void* out,
+                                          float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t indexer_kv_attention_decode_workspace_bytes(int B, int H, int G, int D, int max_context_len, int topk,
+                                                   int cache_dtype);
+
+/*
  * topk_select -- the token selector on its own: top-k of each row of a score
  * matrix.
  *
