@@ -40,7 +40,6 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 constexpr int kTile = 64;       // keys of a tile
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;
-constexpr int kAhead = 4;       // operand reads in flight
 constexpr float kFar = 0x1p30f; // references of this size are taken off rounded scores
 
 // A tile's rows lie one behind another in LDS, their 16-byte pieces permuted
@@ -181,6 +180,7 @@ prompt_attention_kernel(PromptArgs a) {
     constexpr int KP = D / 8, VP = V / 8;                       // 16-byte pieces of a row
     constexpr int kKeyB = kTile * D * 2, kTileB = kKeyB + kTile * V * 2;
     constexpr int KI = kKeyB / 1024 / kWaves, VI = kTile * V * 2 / 1024 / kWaves;  // copies of a wave
+    constexpr int kAhead = D == 192 ? 3 : 4;                    // operand reads in flight
     constexpr int KS = D / 16, MT = V / 32;                     // steps of the first product, blocks of the second
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int n = lane & 31, h = lane >> 5;
@@ -260,45 +260,72 @@ prompt_attention_kernel(PromptArgs a) {
         tile_barrier();
         if (t > 0) stage(t - 1, buf ^ 1);
         if (!active || t > t_mine) continue;
-        // ---- scores ----
+        // ---- scores: keys 32 .. 63, then 0 .. 31; beside the second half the first one's
+        //      probabilities against the reference as it stands ----
         const uint32_t kp = k_at + buf * kTileB, vp = v_at + buf * kTileB;
-        auto read_k = [&](int f) {   // step f: columns 16 (f / 2) .., keys 32 (f % 2) ..
-            const int c = 2 * (f / 2);
-            return lds_read<v8bf>((kp ^ (16 * (c % KPX))) + 16 * (c / KPX * KPX) + f % 2 * (64 * D));
+        auto read_k = [&](int f) {   // step f: columns 16 (f % KS) .., keys 32 (1 - f / KS) ..
+            const int c = 2 * (f % KS);
+            return lds_read<v8bf>((kp ^ (16 * (c % KPX))) + 16 * (c / KPX * KPX) + (1 - f / KS) * (64 * D));
         };
         v16f S[2];
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
             for (int i = 0; i < 16; ++i) S[kt][i] = 0.f;
+        v4i P[4];             // of keys 16 s ..
+        float sum = 0.f, x2 = 0.f, by = scale, off = m;
+        // elements of half kt in step f of n
+        auto weigh = [&](int kt, int f, int n) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i * n / 16 == f) {
+                    const float x = __builtin_amdgcn_exp2f(fmaf(S[kt][i], by, -off));
+                    sum += x;
+                    if (i % 2) P[2 * kt + i / 8][i % 8 / 2] = (int)pack_bf16(x2, x);
+                    x2 = x;
+                }
+        };
         v8bf K[kAhead];
 #pragma unroll
         for (int f = 0; f < kAhead; ++f) K[f] = read_k(f);
 #pragma unroll
         for (int f = 0; f < 2 * KS; ++f) {
             __builtin_amdgcn_sched_barrier(0);
-            S[f % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K[f % kAhead], Q[f / 2], S[f % 2], 0, 0, 0);
+            S[1 - f / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K[f % kAhead], Q[f % KS], S[1 - f / KS], 0, 0, 0);
             if (f + kAhead < 2 * KS) K[f % kAhead] = read_k(f + kAhead);
+            if (f >= KS) weigh(1, f - KS, KS);
         }
+        // (made here, beside the products, not where it is known that they are used)
+        asm volatile("" : "+v"(P[2]), "+v"(P[3]), "+v"(sum));
         __builtin_amdgcn_sched_barrier(0);
-        // ---- softmax ----
-        if (t == t_mine) {
-            const int mine = (r0 & (kTile - 1)) + n;
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (32 * kt + 8 * (i / 4) + 4 * h + i % 4 > mine) S[kt][i] = -__builtin_inff();
-        }
+        auto read_v = [&](int f) {   // step f: columns 32 (f % MT) .., keys 16 s ..
+            const int s = 2 * (1 - f / (2 * MT)) + f / MT % 2;
+            const uint32_t at = vp ^ (64 * (f % MT));
+            const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>(at + s * (32 * V)));
+            const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>((at ^ 32) + s * (32 * V) + 16 * V));
+            return __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
         float top = S[0][0];
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, S[kt][i]);
-        top *= scale;
-        if (wave_ballot(top > m + kSlack)) {
+        if (t == t_mine || far || wave_ballot(top * scale > m + kSlack)) {
+            if (t == t_mine) {
+                int mine = (r0 & (kTile - 1)) + n - 4 * h;
+                asm volatile("" : "+v"(mine));   // (compared here, not once for all tiles in registers that none has left)
+                top = -__builtin_inff();
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (32 * kt + 8 * (i / 4) + i % 4 > mine) S[kt][i] = -__builtin_inff();
+                        top = fmaxf(top, S[kt][i]);
+                    }
+            }
             // a row's reference moves to these keys' maximum where that is so far above it (the
             // rows beside it keep theirs: no row's result depends on another's)
+            top *= scale;
             top = fmaxf(top, __shfl_xor(top, 32, kWave));
             const float to = top > m + kSlack ? top : m;
             const float f = __builtin_amdgcn_exp2f(m - to);
@@ -306,53 +333,42 @@ prompt_attention_kernel(PromptArgs a) {
             l *= f;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) O[mt] *= f;
-            far = wave_ballot(fabsf(m) >= kFar) != 0;
-        }
-        if (far) {
+            // rows with a reference that far off: scores are rounded before it is taken off them (left
+            // whole in an fma, they would keep what it has not: 2 to that may be infinite)
+            const bool here = fabsf(m) >= kFar;
+            far = wave_ballot(here) != 0;
+            by = here ? 1.f : scale;
+            off = here ? 0.f : m;
+            if (far) {
 #pragma clang fp contract(off)
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
+                for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float x = S[kt][i] * scale;
-                    S[kt][i] = __builtin_amdgcn_exp2f(fabsf(m) >= kFar ? x - m : fmaf(S[kt][i], scale, -m));
-                }
-        } else {
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) S[kt][i] = __builtin_amdgcn_exp2f(fmaf(S[kt][i], scale, -m));
-        }
-        v8bf P[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            v4i u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = S[s / 2][8 * (s % 2) + 2 * i], y = S[s / 2][8 * (s % 2) + 2 * i + 1];
-                l += x;
-                l += y;
-                u[i] = (int)pack_bf16(x, y);
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = S[kt][i] * scale;
+                        S[kt][i] = here ? x - m : S[kt][i];
+                    }
             }
-            P[s] = __builtin_bit_cast(v8bf, u);
+            sum = 0.f;
+            weigh(1, 0, 1);
         }
-        // ---- values: A operand of 32 columns x 16 keys ----
-        auto read_v = [&](int f) {   // step f: columns 32 (f % MT) .., keys 16 (f / MT) ..
-            const uint32_t at = vp ^ (64 * (f % MT));
-            const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>(at + f / MT * (32 * V)));
-            const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>((at ^ 32) + f / MT * (32 * V) + 16 * V));
-            return __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-        };
+        // ---- values, beside the first half of them the second half's probabilities: A operand of
+        //      32 columns x 16 keys ----
         v8bf W[kAhead];
 #pragma unroll
         for (int f = 0; f < kAhead; ++f) W[f] = read_v(f);
 #pragma unroll
         for (int f = 0; f < 4 * MT; ++f) {
+            const int s = 2 * (1 - f / (2 * MT)) + f / MT % 2;
             __builtin_amdgcn_sched_barrier(0);
-            O[f % MT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(W[f % kAhead], P[f / MT], O[f % MT], 0, 0, 0);
+            O[f % MT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(W[f % kAhead], __builtin_bit_cast(v8bf, P[s]),
+                                                                O[f % MT], 0, 0, 0);
             if (f + kAhead < 4 * MT) W[f % kAhead] = read_v(f + kAhead);
+            if (f < 2 * MT) weigh(0, f, 2 * MT);
         }
+        asm volatile("" : "+v"(sum));
         __builtin_amdgcn_sched_barrier(0);
+        l += sum;
         if (t == t_mine) {
             float z = 0.f;
 #pragma unroll
@@ -361,14 +377,15 @@ prompt_attention_kernel(PromptArgs a) {
                 for (int i = 0; i < 16; ++i) z = fmaf(O[mt][i], 0.f, z);
             if (wave_ballot(z != z)) {
                 // once more: finite elements as before, the others by which rows see them
-                const int mine = (r0 & (kTile - 1)) + n;
+                int mine = (r0 & (kTile - 1)) + n - 4 * h;
+                asm volatile("" : "+v"(mine));
                 v8bf see[4];
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     v4i u;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int key = 16 * s + 8 * (i / 2) + 4 * h + 2 * (i % 2);
+                        const int key = 16 * s + 8 * (i / 2) + 2 * (i % 2);
                         u[i] = (key <= mine ? 0x3F80 : 0) | (key + 1 <= mine ? 0x3F800000 : 0);
                     }
                     see[s] = __builtin_bit_cast(v8bf, u);
@@ -380,7 +397,7 @@ prompt_attention_kernel(PromptArgs a) {
                     for (int i = 0; i < 16; ++i) O[mt][i] = up[i] = down[i] = 0.f;
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
-                        const v4i w = __builtin_bit_cast(v4i, read_v(MT * s + mt));
+                        const v4i w = __builtin_bit_cast(v4i, read_v(MT * (2 * (1 - s / 2) + s % 2) + mt));
                         v4i f, p, q;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -388,7 +405,8 @@ prompt_attention_kernel(PromptArgs a) {
                             p[i] = (int)not_finite((uint32_t)w[i], 0);
                             q[i] = (int)not_finite((uint32_t)w[i], 0x8000u);
                         }
-                        O[mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, f), P[s], O[mt], 0, 0, 0);
+                        O[mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, f),
+                                                                        __builtin_bit_cast(v8bf, P[s]), O[mt], 0, 0, 0);
                         up = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, p), see[s], up, 0, 0, 0);
                         down = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, q), see[s], down, 0, 0, 0);
                     }
