@@ -516,9 +516,9 @@ dsaidx_status indexer_prompt_attention(const void* q, int64_t q_stride, int64_t 
     if (st != DSAIDX_OK) return st;
     if (!((D == 64 && V == 64) || ((D == 128 || D == 192) && V == 128)))
         return fail(DSAIDX_ERR_UNSUPPORTED, "D=%d V=%d (64 and 64, 128 and 128, or 192 and 128)", D, V);
-    // (a launch holds less than 2^32 threads)
-    if (dsaidx::prompt_threads(T, B, H) >= (int64_t)1 << 32)
-        return fail(DSAIDX_ERR_UNSUPPORTED, "T=%d B=%d H=%d: more than 2^32 threads", T, B, H);
+    // (a launch holds less than 2^32 threads, 256 a workgroup where there are many)
+    if (dsaidx::prompt_blocks(T, B, H) >= 1 << 24)
+        return fail(DSAIDX_ERR_UNSUPPORTED, "T=%d B=%d H=%d: 2^24 blocks of rows or more", T, B, H);
     if (T == 0) return DSAIDX_OK;
     if (!q) return fail(DSAIDX_ERR_NULL, "q is NULL");
     if (!k) return fail(DSAIDX_ERR_NULL, "k is NULL");

@@ -54,7 +54,7 @@ struct KvDecodeArgs {
 };
 
 hipError_t launch_kv_append_rope(const KvAppendArgs& a, int D, bool f32, bool fp8, hipStream_t stream);
-int64_t prompt_threads(int T, int B, int H);   // of a launch
+int64_t prompt_blocks(int T, int B, int H);   // workgroups of a launch
 hipError_t launch_prompt_attention(const PromptArgs& a, int D, hipStream_t stream);
 size_t kv_decode_workspace_bytes(int B, int H, int G, int D, int max_ctx, int K, bool fp8);
 hipError_t launch_kv_decode(const KvDecodeArgs& a, int D, bool fp8, hipStream_t stream);

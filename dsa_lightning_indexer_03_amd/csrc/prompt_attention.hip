@@ -28,6 +28,8 @@
 // There, and only there, a masked row can meet a value that is not finite, as 0
 // times it in the product; the sums then are not finite either, and that tile's
 // values are taken again with such elements apart.
+#include <utility>
+
 #include "device_once.h"
 #include "kv.h"
 #include "tile_copy.h"
@@ -38,8 +40,9 @@ namespace {
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kTile = 64;       // keys of a tile
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;       // waves that share a tile's rows of queries
 constexpr int kRows = 32 * kWaves;
+constexpr int kFewBlocks = 300;
 constexpr float kFar = 0x1p30f; // references of this size are taken off rounded scores
 
 // A tile's rows lie one behind another in LDS, their 16-byte pieces permuted
@@ -173,8 +176,52 @@ __device__ __forceinline__ uint32_t finite(uint32_t x) {
     return x;
 }
 
-template <int D, int V>
-__global__ void __launch_bounds__(64 * kWaves, 2)
+// f(0), f(1), ..., f(N - 1) with numbers known while compiling
+template <typename F, int... I>
+__device__ __forceinline__ void steps(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void steps(F&& f) {
+    steps(f, std::make_integer_sequence<int, N>{});
+}
+
+// The products of a turn, in order: scores of the next tile (half `a` of its keys,
+// 16 columns b) between values of this one (16 keys a, 32 columns b).
+struct Step {
+    bool values;
+    int a, b;
+};
+template <int KS, int MT>
+struct Turn {
+    static constexpr int kSteps = 2 * KS + 4 * MT;
+    static constexpr Step step(int f) {
+        if (f < KS) return {false, 0, f};
+        f -= KS;
+        for (int s = 0; s < 2; ++s) {
+            if (f < MT) return {true, s, f};
+            f -= MT;
+            if (f < KS / 2) return {false, 1, s * (KS / 2) + f};
+            f -= KS / 2;
+        }
+        return {true, 2 + f / MT, f % MT};
+    }
+    // elements of a lane's 32 whose probabilities are made before step f: 8 (s + 1) of them
+    // before the values of keys 16 s take the first
+    static constexpr int made(int f) {
+        constexpr int len[6] = {KS, MT, KS / 2, MT, KS / 2, MT}, el[6] = {12, 4, 4, 4, 4, 4};
+        int n = 0;
+        for (int i = 0; i < 6; ++i) {
+            if (f <= len[i]) return n + el[i] * f / len[i];
+            n += el[i];
+            f -= len[i];
+        }
+        return n;
+    }
+};
+
+template <int D, int V, int KG>
+__global__ void __launch_bounds__(64 * kWaves * KG, 2)
 prompt_attention_kernel(PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int KP = D / 8, VP = V / 8;                       // 16-byte pieces of a row
@@ -182,8 +229,9 @@ prompt_attention_kernel(PromptArgs a) {
     constexpr int KI = kKeyB / 1024 / kWaves, VI = kTile * V * 2 / 1024 / kWaves;  // copies of a wave
     constexpr int kAhead = D == 192 ? 3 : 4;                    // operand reads in flight
     constexpr int KS = D / 16, MT = V / 32;                     // steps of the first product, blocks of the second
-    const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
-    const int n = lane & 31, h = lane >> 5;
+    const int wave = uniform((int)threadIdx.x >> 6) % kWaves, kg = KG == 1 ? 0 : uniform((int)threadIdx.x >> 6) / kWaves;
+    const int lane = lane_id(), n = lane & 31, h = lane >> 5;
+    constexpr int kThreads = 64 * kWaves * KG;
 
     // heads of one key/value head go to one XCD (workgroups go to the 8 in turn)
     const int j = (int)(blockIdx.x % (unsigned)a.H);
@@ -193,10 +241,10 @@ prompt_attention_kernel(PromptArgs a) {
     const int rows = min(kRows, blk.len - blk.r0);
     const int64_t out_row = (int64_t)(blk.start + blk.r0) * a.H + head;   // of [T][H]
     if (blk.pad) {
-        for (int i = (int)threadIdx.x; i < rows * VP; i += 64 * kWaves)
+        for (int i = (int)threadIdx.x; i < rows * VP; i += kThreads)
             *reinterpret_cast<v4i*>(a.out + (out_row + (int64_t)(i / VP) * a.H) * V + 8 * (i % VP)) = v4i{0, 0, 0, 0};
         if (a.lse)
-            for (int i = (int)threadIdx.x; i < rows; i += 64 * kWaves)
+            for (int i = (int)threadIdx.x; i < rows; i += kThreads)
                 a.lse[out_row + (int64_t)i * a.H] = -__builtin_inff();
         return;
     }
@@ -225,13 +273,9 @@ prompt_attention_kernel(PromptArgs a) {
     const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
 
     // ---- copies: a wave's part of a tile, 1024 bytes each ----
-    const uint32_t lds0 = lds_address(smem);
+    const uint32_t lds0 = lds_address(smem) + kg * 2 * kTileB;   // this key group's two tiles
     Copies<KP, KI> kc(wave, lane, a.k.row);
     Copies<VP, VI> vc(wave, lane, a.v.row);
-    auto stage = [&](int t, int buf) {
-        kc.tile(kbase + (int64_t)kTile * t * a.k.row, lds0 + buf * kTileB);
-        vc.tile(vbase + (int64_t)kTile * t * a.v.row, lds0 + buf * kTileB + kKeyB);
-    };
 
     v16f O[MT];
 #pragma unroll
@@ -241,98 +285,65 @@ prompt_attention_kernel(PromptArgs a) {
     // the reference starts below every score that is not -inf, so that a row's first one moves it
     float m = -3.402823466e38f, l = 0.f;
     bool far = false;
+    v16f S0[2], S1[2];      // scores of this turn's tile and the next one's, in turn
+    float top = 0.f;        // the highest of the next one's
+    v4i P[4];               // probabilities of keys 16 s ..
+    float by = 0.f, off = 0.f, sum = 0.f, even = 0.f;
+    auto weigh = [&](const v16f (&S)[2], int e) {   // element e of a lane's 32
+        const float x = __builtin_amdgcn_exp2f(fmaf(S[e / 16][e % 16], by, -off));
+        sum += x;
+        if (e % 2) P[e / 8][e % 8 / 2] = (int)pack_bf16(even, x);
+        even = x;
+    };
 
-    // operand addresses in the first buffer; a step's columns differ in bits of the permuted piece
+    // operand addresses in the first slot; a step's columns differ in bits of the permuted piece
     constexpr int KPX = KP % 16 == 0 ? 16 : 8;
     const uint32_t k_at = lds0 + n * (2 * D) + 16 * (h ^ permute<KP>(n));
     const int v_row = 4 * h + (lane >> 2 & 3);
     const uint32_t v_at = lds0 + kKeyB + v_row * (2 * V) +
                           16 * ((2 * (lane >> 4 & 1) + (lane >> 1 & 1)) ^ permute<VP>(v_row)) + 8 * (lane & 1);
+    int slot = 0;
+    auto read_k = [&](int kt, int ks) {   // A operand: 32 keys x 16 columns
+        const int c = 2 * ks;
+        return lds_read<v8bf>(((k_at + slot * kTileB) ^ (16 * (c % KPX))) + 16 * (c / KPX * KPX) + kt * (64 * D));
+    };
+    auto read_v = [&](int s, int mt) {    // A operand: 32 columns x 16 keys
+        const uint32_t at = (v_at + slot * kTileB) ^ (64 * mt);
+        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>(at + s * (32 * V)));
+        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>((at ^ 32) + s * (32 * V) + 16 * V));
+        return __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    auto highest = [&](const v16f (&S)[2], int i0, int i1) {
+#pragma unroll
+        for (int i = i0; i < i1; ++i) top = fmaxf(top, S[i / 16][i % 16]);
+    };
+    using T = Turn<KS, MT>;
+    auto read = [&](auto f) {
+        constexpr Step st = T::step(decltype(f)::value);
+        if constexpr (st.values) return read_v(st.a, st.b);
+        else return read_k(st.a, st.b);
+    };
 
-    const int t_mine = r0 / kTile;   // the tile that the mask cuts for this wave's rows
-    const int t_first = (blk.r0 + rows - 1) / kTile;
-    int buf = 0;
-    // (only the last tile can pass the sequence's last row)
-    kc.last_tile(kbase + (int64_t)kTile * t_first * a.k.row, lds0, blk.len - 1 - kTile * t_first);
-    vc.last_tile(vbase + (int64_t)kTile * t_first * a.v.row, lds0 + kKeyB, blk.len - 1 - kTile * t_first);
-    for (int t = t_first; t >= 0; --t, buf ^= 1) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the tile
-        tile_barrier();
-        if (t > 0) stage(t - 1, buf ^ 1);
-        if (!active || t > t_mine) continue;
-        // ---- scores: keys 32 .. 63, then 0 .. 31; beside the second half the first one's
-        //      probabilities against the reference as it stands ----
-        const uint32_t kp = k_at + buf * kTileB, vp = v_at + buf * kTileB;
-        auto read_k = [&](int f) {   // step f: columns 16 (f % KS) .., keys 32 (1 - f / KS) ..
-            const int c = 2 * (f % KS);
-            return lds_read<v8bf>((kp ^ (16 * (c % KPX))) + 16 * (c / KPX * KPX) + (1 - f / KS) * (64 * D));
-        };
-        v16f S[2];
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) S[kt][i] = 0.f;
-        v4i P[4];             // of keys 16 s ..
-        float sum = 0.f, x2 = 0.f, by = scale, off = m;
-        // elements of half kt in step f of n
-        auto weigh = [&](int kt, int f, int n) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (i * n / 16 == f) {
-                    const float x = __builtin_amdgcn_exp2f(fmaf(S[kt][i], by, -off));
-                    sum += x;
-                    if (i % 2) P[2 * kt + i / 8][i % 8 / 2] = (int)pack_bf16(x2, x);
-                    x2 = x;
-                }
-        };
-        v8bf K[kAhead];
-#pragma unroll
-        for (int f = 0; f < kAhead; ++f) K[f] = read_k(f);
-#pragma unroll
-        for (int f = 0; f < 2 * KS; ++f) {
-            __builtin_amdgcn_sched_barrier(0);
-            S[1 - f / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K[f % kAhead], Q[f % KS], S[1 - f / KS], 0, 0, 0);
-            if (f + kAhead < 2 * KS) K[f % kAhead] = read_k(f + kAhead);
-            if (f >= KS) weigh(1, f - KS, KS);
-        }
-        // (made here, beside the products, not where it is known that they are used)
-        asm volatile("" : "+v"(P[2]), "+v"(P[3]), "+v"(sum));
-        __builtin_amdgcn_sched_barrier(0);
-        auto read_v = [&](int f) {   // step f: columns 32 (f % MT) .., keys 16 s ..
-            const int s = 2 * (1 - f / (2 * MT)) + f / MT % 2;
-            const uint32_t at = vp ^ (64 * (f % MT));
-            const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>(at + s * (32 * V)));
-            const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>((at ^ 32) + s * (32 * V) + 16 * V));
-            return __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-        };
-        float top = S[0][0];
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, S[kt][i]);
-        if (t == t_mine || far || wave_ballot(top * scale > m + kSlack)) {
-            if (t == t_mine) {
-                int mine = (r0 & (kTile - 1)) + n - 4 * h;
-                asm volatile("" : "+v"(mine));   // (compared here, not once for all tiles in registers that none has left)
-                top = -__builtin_inff();
-#pragma unroll
-                for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (32 * kt + 8 * (i / 4) + i % 4 > mine) S[kt][i] = -__builtin_inff();
-                        top = fmaxf(top, S[kt][i]);
-                    }
-            }
+    // A turn: the probabilities of the tile with scores S, its values, and the next tile's
+    // scores N (behind the last tile: of keys that are none, for nothing).
+    auto turn = [&](v16f (&S)[2], v16f (&N)[2], bool first) __attribute__((always_inline)) {
+        v8bf F[kAhead];
+        steps<kAhead>([&](auto f) { F[f] = read(f); });
+        by = scale;
+        off = m;
+        sum = 0.f;
+        if (first || far || wave_ballot(top * scale > m + kSlack)) {
             // a row's reference moves to these keys' maximum where that is so far above it (the
             // rows beside it keep theirs: no row's result depends on another's)
-            top *= scale;
-            top = fmaxf(top, __shfl_xor(top, 32, kWave));
-            const float to = top > m + kSlack ? top : m;
+            float to = top * scale;
+            to = fmaxf(to, __shfl_xor(to, 32, kWave));
+            to = to > m + kSlack ? to : m;
             const float f = __builtin_amdgcn_exp2f(m - to);
             m = to;
             l *= f;
+            if (!first)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) O[mt] *= f;
+                for (int mt = 0; mt < MT; ++mt) O[mt] *= f;
             // rows with a reference that far off: scores are rounded before it is taken off them (left
             // whole in an fma, they would keep what it has not: 2 to that may be infinite)
             const bool here = fabsf(m) >= kFar;
@@ -349,26 +360,86 @@ prompt_attention_kernel(PromptArgs a) {
                         S[kt][i] = here ? x - m : S[kt][i];
                     }
             }
-            sum = 0.f;
-            weigh(1, 0, 1);
         }
-        // ---- values, beside the first half of them the second half's probabilities: A operand of
-        //      32 columns x 16 keys ----
-        v8bf W[kAhead];
+        top = -__builtin_inff();
 #pragma unroll
-        for (int f = 0; f < kAhead; ++f) W[f] = read_v(f);
+        for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-        for (int f = 0; f < 4 * MT; ++f) {
-            const int s = 2 * (1 - f / (2 * MT)) + f / MT % 2;
+            for (int i = 0; i < 16; ++i) N[kt][i] = 0.f;
+        steps<T::kSteps>([&](auto step) {
+            constexpr int f = decltype(step)::value, kLast = T::kSteps - MT;
+            constexpr Step st = T::step(f);
             __builtin_amdgcn_sched_barrier(0);
-            O[f % MT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(W[f % kAhead], __builtin_bit_cast(v8bf, P[s]),
-                                                                O[f % MT], 0, 0, 0);
-            if (f + kAhead < 4 * MT) W[f % kAhead] = read_v(f + kAhead);
-            if (f < 2 * MT) weigh(0, f, 2 * MT);
-        }
-        asm volatile("" : "+v"(sum));
+            if constexpr (st.values)
+                O[st.b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(F[f % kAhead], __builtin_bit_cast(v8bf, P[st.a]),
+                                                                  O[st.b], 0, 0, 0);
+            else
+                N[st.a] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(F[f % kAhead], Q[st.b], N[st.a], 0, 0, 0);
+            if constexpr (f + kAhead < T::kSteps) F[f % kAhead] = read(std::integral_constant<int, f + kAhead>{});
+            constexpr int e0 = T::made(f), e1 = T::made(f + 1);
+            steps<e1 - e0>([&](auto e) { weigh(S, e0 + decltype(e)::value); });
+            if constexpr (f >= kLast) highest(N, (f - kLast) * 32 / MT, (f - kLast + 1) * 32 / MT);
+        });
+        // (made here, beside the products, not where it is known that they are used)
+        asm volatile("" : "+v"(sum), "+v"(top));
         __builtin_amdgcn_sched_barrier(0);
         l += sum;
+    };
+
+    // ---- the tiles of this key group, from t_first - kg down.  A slot holds the values of a
+    //      turn's tile t and the keys of the next, t - KG; while a turn is taken the slot of the
+    //      next one is copied.  Every wave meets the others once a turn, with or without work. ----
+    const int t_mine = r0 / kTile;   // the tile that the mask cuts for this wave's rows
+    const int t_first = (blk.r0 + rows - 1) / kTile;
+    int t = t_first - kg + KG;
+    auto stage = [&](int t, int slot) {
+        const int last = blk.len - 1 - kTile * t;   // (only the last tile can pass the sequence's last row)
+        if (t >= KG) kc.tile(kbase + (int64_t)kTile * (t - KG) * a.k.row, lds0 + slot * kTileB);
+        if (t == t_first) vc.last_tile(vbase + (int64_t)kTile * t * a.v.row, lds0 + slot * kTileB + kKeyB, last);
+        else if (t >= 0) vc.tile(vbase + (int64_t)kTile * t * a.v.row, lds0 + slot * kTileB + kKeyB);
+    };
+    auto next_turn = [&]() {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the slot
+        tile_barrier();
+        stage(t - KG, slot ^ 1);
+    };
+    auto done = [&]() {
+        t -= KG;
+        slot ^= 1;
+    };
+    if (t >= KG)
+        kc.last_tile(kbase + (int64_t)kTile * (t - KG) * a.k.row, lds0, blk.len - 1 - kTile * (t - KG));
+    while (t + kg >= 0 && (!active || t - KG > t_mine)) {
+        next_turn();
+        done();
+    }
+    if (t - KG >= 0 && active) {
+        next_turn();
+        {
+            v8bf F[kAhead];
+#pragma unroll
+            for (int f = 0; f < kAhead; ++f) F[f] = read_k(f / KS, f % KS);
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S0[kt][i] = 0.f;
+#pragma unroll
+            for (int f = 0; f < 2 * KS; ++f) {
+                __builtin_amdgcn_sched_barrier(0);
+                S0[f / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(F[f % kAhead], Q[f % KS], S0[f / KS], 0, 0, 0);
+                if (f + kAhead < 2 * KS) F[f % kAhead] = read_k((f + kAhead) / KS, (f + kAhead) % KS);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        done();
+        const int mine = t == t_mine ? (r0 & (kTile - 1)) + n - 4 * h : kTile;
+        top = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (32 * (i / 16) + 8 * (i % 16 / 4) + i % 4 > mine) S0[i / 16][i % 16] = -__builtin_inff();
+        highest(S0, 0, 32);
+        next_turn();
+        turn(S0, S1, true);
         if (t == t_mine) {
             float z = 0.f;
 #pragma unroll
@@ -377,8 +448,6 @@ prompt_attention_kernel(PromptArgs a) {
                 for (int i = 0; i < 16; ++i) z = fmaf(O[mt][i], 0.f, z);
             if (wave_ballot(z != z)) {
                 // once more: finite elements as before, the others by which rows see them
-                int mine = (r0 & (kTile - 1)) + n - 4 * h;
-                asm volatile("" : "+v"(mine));
                 v8bf see[4];
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
@@ -391,13 +460,15 @@ prompt_attention_kernel(PromptArgs a) {
                     see[s] = __builtin_bit_cast(v8bf, u);
                 }
 #pragma unroll
+                for (int e = 0; e < 32; ++e) weigh(S0, e);
+#pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     v16f up, down;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) O[mt][i] = up[i] = down[i] = 0.f;
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
-                        const v4i w = __builtin_bit_cast(v4i, read_v(MT * (2 * (1 - s / 2) + s % 2) + mt));
+                        const v4i w = __builtin_bit_cast(v4i, read_v(s, mt));
                         v4i f, p, q;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -418,6 +489,46 @@ prompt_attention_kernel(PromptArgs a) {
                 }
             }
         }
+        done();
+        while (t >= 0) {
+            next_turn();
+            turn(S1, S0, false);
+            done();
+            if (t < 0) break;
+            next_turn();
+            turn(S0, S1, false);
+            done();
+        }
+    }
+    while (t + kg >= 0) {
+        next_turn();
+        done();
+    }
+
+    if constexpr (KG > 1) {   // ---- join the key groups ----
+        v4f* there = reinterpret_cast<v4f*>(smem) + wave * (4 * MT * 64) + lane;
+        float2* ml = reinterpret_cast<float2*>(smem + kWaves * MT * 4 * 64 * 16) + wave * 64 + lane;
+        static_assert(KG == 2 && kWaves * 64 * (MT * 64 + 8) <= 4 * kTileB, "the sums fit the tiles' place");
+        tile_barrier();
+        if (kg == 1) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    there[(4 * mt + i) * 64] = v4f{O[mt][4 * i], O[mt][4 * i + 1], O[mt][4 * i + 2], O[mt][4 * i + 3]};
+            *ml = float2{m, l};
+        }
+        tile_barrier();
+        if (kg == 1) return;
+        const float2 x = *ml;
+        const float to = fmaxf(m, x.x);
+        const float f = __builtin_amdgcn_exp2f(m - to), fx = __builtin_amdgcn_exp2f(x.x - to);
+        m = to;
+        l = l * f + x.y * fx;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) O[mt][i] = O[mt][i] * f + there[(4 * mt + i / 4) * 64][i % 4] * fx;
     }
 
     // ---- write: columns 4h .. 4h+3 of every eight of row n ----
@@ -437,21 +548,26 @@ prompt_attention_kernel(PromptArgs a) {
     if (a.lse && h == 0) a.lse[r] = l == 0.f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945f;
 }
 
-template <int D, int V>
+template <int D, int V, int KG>
 hipError_t run(const PromptArgs& a, hipStream_t stream) {
     static PerDevice<int> once;
-    constexpr int lds = 2 * kTile * 2 * (D + V);
-    const hipError_t e = set_lds_limit(once, (const void*)prompt_attention_kernel<D, V>, lds);
+    constexpr int lds = KG * 2 * kTile * 2 * (D + V);
+    const hipError_t e = set_lds_limit(once, (const void*)prompt_attention_kernel<D, V, KG>, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((prompt_attention_kernel<D, V>), dim3((unsigned)(prompt_threads(a.T, a.B, a.H) / (64 * kWaves))),
-                       dim3(64 * kWaves), lds, stream, a);
+    hipLaunchKernelGGL((prompt_attention_kernel<D, V, KG>), dim3((unsigned)prompt_blocks(a.T, a.B, a.H)),
+                       dim3(64 * kWaves * KG), lds, stream, a);
     return hipGetLastError();
+}
+
+template <int D, int V>
+hipError_t run(const PromptArgs& a, hipStream_t stream) {
+    return prompt_blocks(a.T, a.B, a.H) <= kFewBlocks ? run<D, V, 2>(a, stream) : run<D, V, 1>(a, stream);
 }
 
 }  // namespace
 
 // At most floor(T / kRows) whole blocks and a rest of each of the B sequences and of the rows behind them.
-int64_t prompt_threads(int T, int B, int H) { return ((int64_t)T / kRows + B + 1) * H * (64 * kWaves); }
+int64_t prompt_blocks(int T, int B, int H) { return ((int64_t)T / kRows + B + 1) * H; }
 
 hipError_t launch_prompt_attention(const PromptArgs& a, int D, hipStream_t stream) {
     if (a.T <= 0) return hipSuccess;
