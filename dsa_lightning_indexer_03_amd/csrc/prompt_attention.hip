@@ -64,13 +64,14 @@ __device__ __forceinline__ T lds_read(uint32_t at) {
     return *lds_pointer<T>(at);
 }
 
-// A wave's copies of a tile of rows of P pieces: N of 1024 bytes, a multiple of
-// 8 rows each kBase.  A lane's place in its source row is found once for kBase
+// A wave's copies of a tile of rows of P pieces: N of 1024 bytes, kStep rows each
+// kBase.  A lane's place in its source row is found once for kBase
 // copies; the next ones are a number of rows on, and permuted by one bit more.
 template <int P, int N>
 struct Copies {
-    static constexpr int kBase = P == 24 ? 3 : 1, kStep = P == 16 ? 4 : 8, kBit = P == 16 ? 16 : 32;
-    static_assert(N % kBase == 0 && (N / kBase <= (P == 16 ? 4 : 2)), "the permutation's bits");
+    static constexpr int kBase = P == 24 ? 3 : 1, kStep = P == 16 ? 4 : 8;
+    static constexpr int kBit = P == 16 ? 16 : 32, kTurns = P == 16 ? 4 : 2;
+    static_assert(N % kBase == 0, "whole steps");
     int row[kBase];       // of the tile
     uint32_t piece[kBase];
     int64_t stride;       // bytes
@@ -89,14 +90,14 @@ struct Copies {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             copy_to_lds(reinterpret_cast<const char*>(src) + i / kBase * kStep * stride,
-                        (piece[i % kBase] ^ (uint32_t)(i / kBase * kBit)) + (uint32_t)row[i % kBase] * (uint32_t)stride,
+                        (piece[i % kBase] ^ (uint32_t)(i / kBase % kTurns * kBit)) + (uint32_t)row[i % kBase] * (uint32_t)stride,
                         lds + first + i * 1024);
     }
     // The same where row `last` is the last one: rows behind it are that row again.
     __device__ __forceinline__ void last_tile(const uint16_t* src, uint32_t lds, int last) const {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            copy_to_lds(src, (piece[i % kBase] ^ (uint32_t)(i / kBase * kBit)) +
+            copy_to_lds(src, (piece[i % kBase] ^ (uint32_t)(i / kBase % kTurns * kBit)) +
                                  (uint32_t)min(row[i % kBase] + i / kBase * kStep, last) * (uint32_t)stride,
                         lds + first + i * 1024);
     }
@@ -227,7 +228,7 @@ prompt_attention_kernel(PromptArgs a) {
     constexpr int KP = D / 8, VP = V / 8;                       // 16-byte pieces of a row
     constexpr int kKeyB = kTile * D * 2, kTileB = kKeyB + kTile * V * 2;
     constexpr int KI = kKeyB / 1024 / kWaves, VI = kTile * V * 2 / 1024 / kWaves;  // copies of a wave
-    constexpr int kAhead = D == 192 ? 3 : 4;                    // operand reads in flight
+    constexpr int kAhead = D >= 128 ? 3 : 4;                    // operand reads in flight
     constexpr int KS = D / 16, MT = V / 32;                     // steps of the first product, blocks of the second
     const int wave = uniform((int)threadIdx.x >> 6) % kWaves, kg = KG == 1 ? 0 : uniform((int)threadIdx.x >> 6) / kWaves;
     const int lane = lane_id(), n = lane & 31, h = lane >> 5;
@@ -252,30 +253,40 @@ prompt_attention_kernel(PromptArgs a) {
     const uint16_t* kbase = reinterpret_cast<const uint16_t*>(a.k.p) + blk.start * a.k.row + g * a.k.head;
     const uint16_t* vbase = reinterpret_cast<const uint16_t*>(a.v.p) + blk.start * a.v.row + g * a.v.head;
 
-    // ---- queries: B operand of 32 rows x 16 columns ----
     const int r0 = blk.r0 + 32 * wave;   // this wave's first row in the sequence
     const bool active = 32 * wave < rows;
-    v8bf Q[KS];
-    {
-        const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q.p) +
-                             (blk.start + (int64_t)min(r0 + n, blk.len - 1)) * a.q.row + head * a.q.head + 8 * h;
+    // (never 0: a score of -inf has to stay one)
+    const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
+
+    // ---- copies: a wave's part of a tile, 1024 bytes each; first of all the first keys and
+    //      the wave's queries, the latter behind the first keys ----
+    const uint32_t lds0 = lds_address(smem) + kg * 2 * kTileB;   // this key group's two slots
+    const Copies<KP, KI> kc(wave, lane, a.k.row);
+    const Copies<VP, VI> vc(wave, lane, a.v.row);
+    const int t_mine = r0 / kTile;   // the tile that the mask cuts for this wave's rows
+    const int t_first = (blk.r0 + rows - 1) / kTile;
+    int t = t_first - kg + KG;       // (the loop below)
+    if (t >= KG)
+        kc.last_tile(kbase + (int64_t)kTile * (t - KG) * a.k.row, lds0, blk.len - 1 - kTile * (t - KG));
+    v8bf Q[KS];   // B operand of 32 rows x 16 columns
+    if (active) {
+        static_assert(kWaves * 32 * 2 * D <= kTileB + kTile * V * 2, "the queries fit the first values' place and the second slot");
+        const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q.p) + blk.start * a.q.row + head * a.q.head;
+        const uint32_t at = lds0 + kKeyB + wave * (32 * 2 * D);
+        const Copies<KP, D / 16> qc(0, lane, a.q.row);
+        qc.last_tile(qp + (int64_t)r0 * a.q.row, at, min(31, blk.len - 1 - r0));
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+        asm volatile("" ::: "memory");
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) Q[ks] = *reinterpret_cast<const v8bf*>(qp + 16 * ks);
-        if (a.scale_log2 < 0.f)   // the products then take the scale's magnitude
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
+        for (int ks = 0; ks < KS; ++ks) {
+            Q[ks] = lds_read<v8bf>(at + n * (2 * D) + 16 * ((2 * ks + h) ^ permute<KP>(n)));
+            if (a.scale_log2 < 0.f) {   // the products then take the scale's magnitude
                 v4i u = __builtin_bit_cast(v4i, Q[ks]);
                 u ^= (int)0x80008000;
                 Q[ks] = __builtin_bit_cast(v8bf, u);
             }
+        }
     }
-    // (never 0: a score of -inf has to stay one)
-    const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
-
-    // ---- copies: a wave's part of a tile, 1024 bytes each ----
-    const uint32_t lds0 = lds_address(smem) + kg * 2 * kTileB;   // this key group's two tiles
-    Copies<KP, KI> kc(wave, lane, a.k.row);
-    Copies<VP, VI> vc(wave, lane, a.v.row);
 
     v16f O[MT];
 #pragma unroll
@@ -389,9 +400,6 @@ prompt_attention_kernel(PromptArgs a) {
     // ---- the tiles of this key group, from t_first - kg down.  A slot holds the values of a
     //      turn's tile t and the keys of the next, t - KG; while a turn is taken the slot of the
     //      next one is copied.  Every wave meets the others once a turn, with or without work. ----
-    const int t_mine = r0 / kTile;   // the tile that the mask cuts for this wave's rows
-    const int t_first = (blk.r0 + rows - 1) / kTile;
-    int t = t_first - kg + KG;
     auto stage = [&](int t, int slot) {
         const int last = blk.len - 1 - kTile * t;   // (only the last tile can pass the sequence's last row)
         if (t >= KG) kc.tile(kbase + (int64_t)kTile * (t - KG) * a.k.row, lds0 + slot * kTileB);
@@ -407,8 +415,6 @@ prompt_attention_kernel(PromptArgs a) {
         t -= KG;
         slot ^= 1;
     };
-    if (t >= KG)
-        kc.last_tile(kbase + (int64_t)kTile * (t - KG) * a.k.row, lds0, blk.len - 1 - kTile * (t - KG));
     while (t + kg >= 0 && (!active || t - KG > t_mine)) {
         next_turn();
         done();
@@ -531,21 +537,31 @@ prompt_attention_kernel(PromptArgs a) {
             for (int i = 0; i < 16; ++i) O[mt][i] = O[mt][i] * f + there[(4 * mt + i / 4) * 64][i % 4] * fx;
     }
 
-    // ---- write: columns 4h .. 4h+3 of every eight of row n ----
+    // ---- write: rows through LDS, so that a store takes whole ones ----
     l += __shfl_xor(l, 32, kWave);
-    if (32 * wave + n >= rows) return;
-    const int64_t r = out_row + (int64_t)(32 * wave + n) * a.H;
+    constexpr int kOutB = 2 * V + 16;
+    unsigned char* rows_at = smem + wave * (KG > 1 ? MT * 4 * 64 * 16 : 32 * kOutB);
+    static_assert(32 * kOutB <= MT * 4 * 64 * 16 && kWaves * 32 * kOutB <= 2 * kTileB, "the rows fit the sums' or tiles' place");
+    if constexpr (KG == 1) tile_barrier();
+    if (!active) return;
     const float inv = 1.f / l;
-    uint16_t* out = a.out + r * V + 4 * h;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint2*>(out + 32 * mt + 8 * i) =
+        for (int i = 0; i < 4; ++i)   // columns 4h .. 4h+3 of every eight of row n
+            *reinterpret_cast<uint2*>(rows_at + n * kOutB + 64 * mt + 16 * i + 8 * h) =
                 l == 0.f ? uint2{0, 0}
                          : uint2{pack_bf16(O[mt][4 * i] * inv, O[mt][4 * i + 1] * inv),
                                  pack_bf16(O[mt][4 * i + 2] * inv, O[mt][4 * i + 3] * inv)};
-    if (a.lse && h == 0) a.lse[r] = l == 0.f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945f;
+    const int64_t first_row = out_row + (int64_t)(32 * wave) * a.H;
+#pragma unroll
+    for (int i = 0; i < VP / 2; ++i) {
+        const int r = i * (64 / VP) + lane / VP, c = lane % VP;
+        const v4i x = *reinterpret_cast<const v4i*>(rows_at + r * kOutB + 16 * c);
+        if (32 * wave + r < rows) *reinterpret_cast<v4i*>(a.out + (first_row + (int64_t)r * a.H) * V + 8 * c) = x;
+    }
+    if (a.lse && h == 0 && 32 * wave + n < rows)
+        a.lse[first_row + (int64_t)n * a.H] = l == 0.f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945f;
 }
 
 template <int D, int V, int KG>

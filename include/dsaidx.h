@@ -552,7 +552,7 @@ dsaidx_status indexer_kv_append_rope(const void* k, int64_t k_stride, int64_t k_
  * No workspace.  T = 0 is a no-op.
  *
  * Supported: (D, V) = (64, 64), (128, 128) or (192, 128), H <= 128 a multiple of
- * G, rows and out 16-byte aligned, strides of k and v below 2^24; (T / 128 + B +
+ * G, rows and out 16-byte aligned, strides of tokens in [0, 2^24); (T / 128 + B +
  * 1) * H < 2^24.
  */
 dsaidx_status indexer_prompt_attention(const void* q, int64_t q_stride, int64_t q_head_stride, const void* k,
