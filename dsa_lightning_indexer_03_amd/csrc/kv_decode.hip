@@ -41,6 +41,7 @@ constexpr int kKeys = 32;      // positions of a wave's tile
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRound = kKeys * kWaves;
+constexpr int kMaxRuns = 512;  // runs of a sequence
 
 // What an entry without a row is copied from.
 static __device__ __align__(16) const unsigned char kZeros[256] = {};
@@ -94,9 +95,21 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
     const int per = a.B * a.G * p.hb;
     const int slot = (int)(blockIdx.x / (unsigned)per), rest = (int)(blockIdx.x % (unsigned)per);
     const int hb = rest % p.hb, g = rest / p.hb % a.G, b = rest / p.hb / a.G;
+    const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
+    const int32_t* idx = TOPK ? a.idx + (int64_t)b * a.K : nullptr;
+    const int first = slot * p.run, most = min((TOPK ? a.K : a.max_ctx) - first, p.run) + first;
+    int c = first + kKeys * wave;
+    // what the first two tiles need, loaded before the context's length is known: listed
+    // positions, or page ids
+    auto ahead = [&](int c) -> int {
+        const int e = c + (lane & (kKeys - 1));
+        if (e >= most) return -1;
+        return TOPK ? idx[e] : table[e / kPage];
+    };
+    const int a0 = ahead(c), a1 = ahead(c + kRound);
     const int ctx = min(max(a.lens[b], 0), a.max_ctx);
     const int len = TOPK ? a.K : ctx;
-    const int first = slot * p.run, end = min(len - first, p.run) + first;
+    const int end = min(most, len);
     if (first >= len && p.slots > 1) return;
     const int h0 = g * R + hb * p.rows;          // first head
     const int rows = min(p.rows, R - hb * p.rows);
@@ -111,8 +124,6 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
     }
 
     // ---- the wave's tiles: entries, page ids, rows ----
-    const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
-    const int32_t* idx = TOPK ? a.idx + (int64_t)b * a.K : nullptr;
     auto entry = [&](int c) -> int {   // position of entry lane % 32 of the tile at c, -1: none
         const int e = c + (lane & (kKeys - 1));
         if (e >= end) return -1;
@@ -164,13 +175,12 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
     // (never 0: a score of -inf, an entry without a row, has to stay one)
     const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
 
-    int c = first + kKeys * wave;
     float unit = 1.f, inv_unit = 1.f;
     if (c < end) {
-        const int s0 = entry(c);
-        int s1 = entry(c + kRound), s2 = entry(c + 2 * kRound);
-        int row = resolve(s0, page(s0));
-        int page1 = page(s1);
+        const int s0 = TOPK ? (a0 < ctx ? a0 : -1) : entry(c);
+        int s1 = TOPK ? (a1 < ctx ? a1 : -1) : entry(c + kRound), s2 = entry(c + 2 * kRound);
+        int row = resolve(s0, TOPK ? page(s0) : a0);
+        int page1 = TOPK ? page(s1) : a1;
         if constexpr (FP8) {
             const uint64_t some = wave_ballot(row >= 0);
             if (some) {
@@ -336,56 +346,92 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
     }
 }
 
-// One workgroup a row: its waves take the runs in turn, a lane D/64 columns.
+// One workgroup a row: its threads weigh the runs, then a lane takes 4 columns of
+// every run that is its wave part's.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 kv_join_kernel(KvDecodeArgs a, KvPlan p) {
-    constexpr int N = D / 64;
-    __shared__ float sums[kWaves][D];
+    constexpr int N = D / 4, kParts = kThreads / N;   // lanes of a run's row, runs at once
+    __shared__ float weights[kMaxRuns];
+    __shared__ float red[2][kWaves];
+    __shared__ v4f sums[kParts][N];
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int64_t row = blockIdx.x, rows = (int64_t)a.B * a.H;
     const int b = (int)(row / a.H);
     const int len = a.idx ? a.K : min(max(a.lens[b], 0), a.max_ctx);
-    const int slots = (len + p.run - 1) / p.run;
+    const int runs = min((len + p.run - 1) / p.run, p.slots);
+    const int part = (int)threadIdx.x / N, col = 4 * ((int)threadIdx.x % N);
+    const float* at = p.part_o + row * D + col;
+    float2 ml[kMaxRuns / kThreads];
     float to = -3.402823466e38f;
-    for (int s = lane; s < slots; s += kWave) to = fmaxf(to, p.part_ml[s * rows + row].x);
+#pragma unroll
+    for (int i = 0; i < kMaxRuns / kThreads; ++i) {
+        const int s = i * kThreads + (int)threadIdx.x;
+        ml[i] = s < runs ? p.part_ml[s * rows + row] : float2{-3.402823466e38f, 0.f};
+        to = fmaxf(to, ml[i].x);
+    }
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) to = fmaxf(to, __shfl_xor(to, d, kWave));
-    float l = 0.f, o[N];
+    if (lane == 0) red[0][wave] = to;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = 0.f;
-    for (int s = lane; s < slots; s += kWave) {
-        const float2 x = p.part_ml[s * rows + row];
-        l += x.y * __builtin_amdgcn_exp2f(x.x - to);
+    for (int w = 0; w < kWaves; ++w) to = fmaxf(to, red[0][w]);
+    float l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxRuns / kThreads; ++i) {
+        const float f = __builtin_amdgcn_exp2f(ml[i].x - to);
+        l += ml[i].y * f;
+        weights[i * kThreads + (int)threadIdx.x] = f;
     }
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) l += __shfl_xor(l, d, kWave);
-#pragma unroll 4
-    for (int s = wave; s < slots; s += kWaves) {
-        const float f = __builtin_amdgcn_exp2f(p.part_ml[s * rows + row].x - to);
-        const float* part = p.part_o + (s * rows + row) * D + N * lane;
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] += part[i] * f;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) sums[wave][N * lane + i] = o[i];
+    if (lane == 0) red[1][wave] = l;
     __syncthreads();
-    if (wave != 0) return;
-    const float inv = 1.f / l;
+    l = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        o[i] = 0.f;
+    for (int w = 0; w < kWaves; ++w) l += red[1][w];
+    v4f o = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int s = part; s < runs; s += kParts) o += *reinterpret_cast<const v4f*>(at + s * rows * D) * weights[s];
+    sums[part][threadIdx.x % N] = o;
+    __syncthreads();
+    if (part != 0) return;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) o[i] += sums[w][N * lane + i];
-        o[i] = l == 0.f ? 0.f : o[i] * inv;
-    }
-    uint16_t* out = a.out + row * D + N * lane;
-    if constexpr (N == 2) *reinterpret_cast<uint32_t*>(out) = pack_bf16(o[0], o[1]);
-    else *out = (uint16_t)pack_bf16(o[0], 0.f);
-    if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -__builtin_inff() : (to + log2f(l)) * 0.693147180559945f;
+    for (int i = 1; i < kParts; ++i) o += sums[i][threadIdx.x];
+    o = l == 0.f ? v4f{0.f, 0.f, 0.f, 0.f} : o * (1.f / l);
+    *reinterpret_cast<uint2*>(a.out + row * D + col) = uint2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+    if (a.lse && col == 0) a.lse[row] = l == 0.f ? -__builtin_inff() : (to + log2f(l)) * 0.693147180559945f;
 }
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Workgroups that the card holds at once.
+int resident(int D, int rows, bool fp8) {
+    int lds = 0;
+    if (D == 64) lds = rows == 16 ? (fp8 ? Lds<64, 1, true>::kBytes : Lds<64, 1, false>::kBytes)
+                       : rows == 32 ? (fp8 ? Lds<64, 2, true>::kBytes : Lds<64, 2, false>::kBytes)
+                                    : (fp8 ? Lds<64, 4, true>::kBytes : Lds<64, 4, false>::kBytes);
+    else lds = rows == 16 ? (fp8 ? Lds<128, 1, true>::kBytes : Lds<128, 1, false>::kBytes)
+               : rows == 32 ? (fp8 ? Lds<128, 2, true>::kBytes : Lds<128, 2, false>::kBytes)
+                            : (fp8 ? Lds<128, 4, true>::kBytes : Lds<128, 4, false>::kBytes);
+    const int n = 160 * 1024 / lds, by_registers = rows == 64 ? 2 : 4;
+    return 256 * (n < by_registers ? n : by_registers);
+}
+
+// Microseconds of runs of `run` rounds of 128 positions, by what was measured: 3 until
+// a workgroup's first tile and for its join of the waves; a round its bytes' share of
+// 5.9 TB/s or, with part of the card, 0.75 (fp8: 1) and 0.6 of that; 2.5 for the
+// second kernel and 0.03 a run.  8 heads of 128
+// columns, one context of 32768, bf16: 49.6 us in runs of 1 round, 30.4 of 4, 27.6 of
+// 8, 28.1 of 16, 40.6 of 32; 8 contexts of 8192: 58.2, 54.5, 52.0 and 58.4 of 4 to 32;
+// 64 contexts of 4096 to 32768: 978, 855, 824, 817 and, of 128, 853: runs of up to
+// 32 rounds keep contexts of different lengths even.
+double run_cost(int64_t blocks, int64_t rounds, int64_t run, int held, int round_bytes, bool fp8) {
+    const int64_t slots = ceil_div(rounds, run), wgs = blocks * slots, at_once = wgs < held ? wgs : held;
+    const double share = 1e-6 * round_bytes * (double)at_once / 5.9, part = (fp8 ? 1. : 0.75) + 0.6 * share;
+    const double round = share > part ? share : part;
+    return ceil_div(wgs, held) * (3. + round * (double)(run < rounds ? run : rounds)) + (slots > 1 ? 2.5 + 0.03 * slots : 0.);
+}
 
 KvPlan make_plan(int B, int H, int G, int D, int max_ctx, int K, bool fp8) {
     const int R = H / G;
@@ -393,15 +439,19 @@ KvPlan make_plan(int B, int H, int G, int D, int max_ctx, int K, bool fp8) {
     p.rows = R <= 16 ? 16 : R <= 32 ? 32 : 64;
     p.hb = ceil_div(R, p.rows);
     const int64_t len = K > 0 ? K : max_ctx;
-    const int64_t blocks = (int64_t)B * G * p.hb;
-    const int64_t rounds = ceil_div(len, kRound);
-    int64_t want = 1024 / blocks;
-    if (want < 1) want = 1;
-    int64_t run = ceil_div(rounds, want);
-    if (run < 2) run = 2;
-    if (run > 32) run = 32;
+    const int64_t blocks = (int64_t)B * G * p.hb, rounds = ceil_div(len, kRound);
+    const int held = resident(D, p.rows, fp8), round_bytes = kRound * 2 * D * (fp8 ? 1 : 2);
+    int64_t run = 32;
+    double best = 1e300;
+    for (const int r : {32, 24, 16, 12, 8, 6, 4, 3, 2, 1}) {
+        const double us = run_cost(blocks, rounds, r, held, round_bytes, fp8);
+        if (us < best) {
+            best = us;
+            run = r;
+        }
+    }
     // (a launch holds less than 2^32 threads)
-    while (ceil_div(rounds, run) * blocks >= (int64_t)1 << 24) run *= 2;
+    while (ceil_div(rounds, run) > kMaxRuns || ceil_div(rounds, run) * blocks >= (int64_t)1 << 24) run *= 2;
     p.run = (int)(run * kRound);
     p.slots = len > 0 ? ceil_div(len, p.run) : 1;
     return p;

@@ -42,7 +42,6 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 constexpr int kTile = 64;       // keys of a tile
 constexpr int kWaves = 4;       // waves that share a tile's rows of queries
 constexpr int kRows = 32 * kWaves;
-constexpr int kFewBlocks = 300;
 constexpr float kFar = 0x1p30f; // references of this size are taken off rounded scores
 
 // A tile's rows lie one behind another in LDS, their 16-byte pieces permuted
@@ -575,9 +574,16 @@ hipError_t run(const PromptArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Two key groups where the blocks leave waves' places free and sequences are long
+// enough: with up to 640 blocks (256 CUs hold 512 of one group) and more than 256
+// rows a sequence.  Of 128 columns, one and two groups: 2048 rows of 16 heads (272
+// blocks) 38.9 and 33.3 us, 8192 of 8 (528) 165 and 142, 2048 of 32 (576) 48.6 and
+// 47.3, 8192 of 16 (1056) 269 and 272; 256 rows of 16 heads 10.1 and 10.2, 64 6.2
+// and 7.5.
 template <int D, int V>
 hipError_t run(const PromptArgs& a, hipStream_t stream) {
-    return prompt_blocks(a.T, a.B, a.H) <= kFewBlocks ? run<D, V, 2>(a, stream) : run<D, V, 1>(a, stream);
+    const bool two = prompt_blocks(a.T, a.B, a.H) <= 640 && (int64_t)a.T > 256 * (int64_t)a.B;
+    return two ? run<D, V, 2>(a, stream) : run<D, V, 1>(a, stream);
 }
 
 }  // namespace
