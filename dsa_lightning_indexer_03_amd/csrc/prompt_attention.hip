@@ -39,9 +39,6 @@ namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-constexpr int kTile = 64;       // keys of a tile
-constexpr int kWaves = 4;       // waves that share a tile's rows of queries
-constexpr int kRows = 32 * kWaves;
 constexpr float kFar = 0x1p30f; // references of this size are taken off rounded scores
 
 // A tile's rows lie one behind another in LDS, their 16-byte pieces permuted
@@ -113,6 +110,7 @@ struct Block {
 // sequence count as one more.  With few sequences the blocks come longest first
 // (a block's work grows with its first row), so that the last ones to start are
 // short; else sequence by sequence, which takes one pass over them.
+template <int kRows>
 __device__ __forceinline__ bool find_block(const PromptArgs& a, int item, Block& out) {
     const int lane = lane_id(), segments = a.B + 1;
     auto load = [&](int b, int& s, int& e) {
@@ -186,32 +184,33 @@ __device__ __forceinline__ void steps(F&& f) {
     steps(f, std::make_integer_sequence<int, N>{});
 }
 
-// The products of a turn, in order: scores of the next tile (half `a` of its keys,
-// 16 columns b) between values of this one (16 keys a, 32 columns b).
+// The products of a turn, in order: scores of the wave's next keys (32 keys `a` of
+// them, 16 columns b) between values of these (16 keys a, 32 columns b).  NH: 32s
+// of keys.
 struct Step {
     bool values;
     int a, b;
 };
-template <int KS, int MT>
+template <int KS, int MT, int NH>
 struct Turn {
-    static constexpr int kSteps = 2 * KS + 4 * MT;
+    static constexpr int kSteps = NH * (KS + 2 * MT);
     static constexpr Step step(int f) {
         if (f < KS) return {false, 0, f};
         f -= KS;
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 2 && NH == 2; ++s) {
             if (f < MT) return {true, s, f};
             f -= MT;
             if (f < KS / 2) return {false, 1, s * (KS / 2) + f};
             f -= KS / 2;
         }
-        return {true, 2 + f / MT, f % MT};
+        return {true, 2 * (NH - 1) + f / MT, f % MT};
     }
-    // elements of a lane's 32 whose probabilities are made before step f: 8 (s + 1) of them
-    // before the values of keys 16 s take the first
+    // elements of a lane's 16 NH whose probabilities are made before step f: 8 (s + 1) of
+    // them before the values of keys 16 s take the first
     static constexpr int made(int f) {
         constexpr int len[6] = {KS, MT, KS / 2, MT, KS / 2, MT}, el[6] = {12, 4, 4, 4, 4, 4};
         int n = 0;
-        for (int i = 0; i < 6; ++i) {
+        for (int i = 0; i < 2 + 4 * (NH - 1); ++i) {
             if (f <= len[i]) return n + el[i] * f / len[i];
             n += el[i];
             f -= len[i];
@@ -220,24 +219,33 @@ struct Turn {
     }
 };
 
-template <int D, int V, int KG>
-__global__ void __launch_bounds__(64 * kWaves * KG, 2)
+// LDS of a workgroup: two slots, or the key groups' sums
+template <int D, int V, int RG, int KG, int NK>
+constexpr int kSlots = 2 * KG * NK * 2 * (D + V);
+template <int D, int V, int RG, int KG, int NK>
+constexpr int kGroupSums = KG > 1 ? RG * KG * (V / 32 * 4 * 64 * 16 + 64 * 8) : 0;
+template <int D, int V, int RG, int KG, int NK>
+constexpr int kLds = kSlots<D, V, RG, KG, NK> > kGroupSums<D, V, RG, KG, NK> ? kSlots<D, V, RG, KG, NK>
+                                                                            : kGroupSums<D, V, RG, KG, NK>;
+
+template <int D, int V, int RG, int KG, int NK>
+__global__ void __launch_bounds__(64 * RG * KG, 2)
 prompt_attention_kernel(PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int KP = D / 8, VP = V / 8;                       // 16-byte pieces of a row
-    constexpr int kKeyB = kTile * D * 2, kTileB = kKeyB + kTile * V * 2;
+    constexpr int kWaves = RG * KG, kThreads = 64 * kWaves, kRows = 32 * RG;
+    constexpr int kTile = KG * NK, kKeyB = kTile * D * 2, kTileB = kKeyB + kTile * V * 2;
     constexpr int KI = kKeyB / 1024 / kWaves, VI = kTile * V * 2 / 1024 / kWaves;  // copies of a wave
     constexpr int kAhead = D >= 128 ? 3 : 4;                    // operand reads in flight
-    constexpr int KS = D / 16, MT = V / 32;                     // steps of the first product, blocks of the second
-    const int wave = uniform((int)threadIdx.x >> 6) % kWaves, kg = KG == 1 ? 0 : uniform((int)threadIdx.x >> 6) / kWaves;
+    constexpr int KS = D / 16, MT = V / 32, NH = NK / 32;       // steps of the first product, blocks of the second
+    const int wave = uniform((int)threadIdx.x >> 6), rg = wave % RG, kg = wave / RG;
     const int lane = lane_id(), n = lane & 31, h = lane >> 5;
-    constexpr int kThreads = 64 * kWaves * KG;
 
     // heads of one key/value head go to one XCD (workgroups go to the 8 in turn)
     const int j = (int)(blockIdx.x % (unsigned)a.H);
     const int head = a.H % 8 == 0 ? (j & 7) * (a.H >> 3) + (j >> 3) : j;
     Block blk;
-    if (!find_block(a, (int)(blockIdx.x / (unsigned)a.H), blk)) return;
+    if (!find_block<kRows>(a, (int)(blockIdx.x / (unsigned)a.H), blk)) return;
     const int rows = min(kRows, blk.len - blk.r0);
     const int64_t out_row = (int64_t)(blk.start + blk.r0) * a.H + head;   // of [T][H]
     if (blk.pad) {
@@ -252,21 +260,18 @@ prompt_attention_kernel(PromptArgs a) {
     const uint16_t* kbase = reinterpret_cast<const uint16_t*>(a.k.p) + blk.start * a.k.row + g * a.k.head;
     const uint16_t* vbase = reinterpret_cast<const uint16_t*>(a.v.p) + blk.start * a.v.row + g * a.v.head;
 
-    const int r0 = blk.r0 + 32 * wave;   // this wave's first row in the sequence
-    const bool active = 32 * wave < rows;
+    const int r0 = blk.r0 + 32 * rg;   // this wave's first row in the sequence
+    const bool active = 32 * rg < rows;
     // (never 0: a score of -inf has to stay one)
     const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
 
     // ---- copies: a wave's part of a tile, 1024 bytes each; first of all the first keys and
     //      the wave's queries, the latter behind the first keys ----
-    const uint32_t lds0 = lds_address(smem) + kg * 2 * kTileB;   // this key group's two slots
+    const uint32_t lds0 = lds_address(smem);
     const Copies<KP, KI> kc(wave, lane, a.k.row);
     const Copies<VP, VI> vc(wave, lane, a.v.row);
-    const int t_mine = r0 / kTile;   // the tile that the mask cuts for this wave's rows
     const int t_first = (blk.r0 + rows - 1) / kTile;
-    int t = t_first - kg + KG;       // (the loop below)
-    if (t >= KG)
-        kc.last_tile(kbase + (int64_t)kTile * (t - KG) * a.k.row, lds0, blk.len - 1 - kTile * (t - KG));
+    kc.last_tile(kbase + (int64_t)kTile * t_first * a.k.row, lds0, blk.len - 1 - kTile * t_first);
     v8bf Q[KS];   // B operand of 32 rows x 16 columns
     if (active) {
         static_assert(kWaves * 32 * 2 * D <= kTileB + kTile * V * 2, "the queries fit the first values' place and the second slot");
@@ -295,11 +300,11 @@ prompt_attention_kernel(PromptArgs a) {
     // the reference starts below every score that is not -inf, so that a row's first one moves it
     float m = -3.402823466e38f, l = 0.f;
     bool far = false;
-    v16f S0[2], S1[2];      // scores of this turn's tile and the next one's, in turn
+    v16f S0[NH], S1[NH];    // scores of this turn's keys and the next one's, in turn
     float top = 0.f;        // the highest of the next one's
-    v4i P[4];               // probabilities of keys 16 s ..
+    v4i P[2 * NH];               // probabilities of keys 16 s ..
     float by = 0.f, off = 0.f, sum = 0.f, even = 0.f;
-    auto weigh = [&](const v16f (&S)[2], int e) {   // element e of a lane's 32
+    auto weigh = [&](const v16f (&S)[NH], int e) {   // element e of a lane's 16 NH
         const float x = __builtin_amdgcn_exp2f(fmaf(S[e / 16][e % 16], by, -off));
         sum += x;
         if (e % 2) P[e / 8][e % 8 / 2] = (int)pack_bf16(even, x);
@@ -308,9 +313,9 @@ prompt_attention_kernel(PromptArgs a) {
 
     // operand addresses in the first slot; a step's columns differ in bits of the permuted piece
     constexpr int KPX = KP % 16 == 0 ? 16 : 8;
-    const uint32_t k_at = lds0 + n * (2 * D) + 16 * (h ^ permute<KP>(n));
+    const uint32_t k_at = lds0 + (kg * NK + n) * (2 * D) + 16 * (h ^ permute<KP>(n));
     const int v_row = 4 * h + (lane >> 2 & 3);
-    const uint32_t v_at = lds0 + kKeyB + v_row * (2 * V) +
+    const uint32_t v_at = lds0 + kKeyB + (kg * NK + v_row) * (2 * V) +
                           16 * ((2 * (lane >> 4 & 1) + (lane >> 1 & 1)) ^ permute<VP>(v_row)) + 8 * (lane & 1);
     int slot = 0;
     auto read_k = [&](int kt, int ks) {   // A operand: 32 keys x 16 columns
@@ -323,11 +328,11 @@ prompt_attention_kernel(PromptArgs a) {
         const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>((at ^ 32) + s * (32 * V) + 16 * V));
         return __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     };
-    auto highest = [&](const v16f (&S)[2], int i0, int i1) {
+    auto highest = [&](const v16f (&S)[NH], int i0, int i1) {
 #pragma unroll
         for (int i = i0; i < i1; ++i) top = fmaxf(top, S[i / 16][i % 16]);
     };
-    using T = Turn<KS, MT>;
+    using T = Turn<KS, MT, NH>;
     auto read = [&](auto f) {
         constexpr Step st = T::step(decltype(f)::value);
         if constexpr (st.values) return read_v(st.a, st.b);
@@ -336,7 +341,7 @@ prompt_attention_kernel(PromptArgs a) {
 
     // A turn: the probabilities of the tile with scores S, its values, and the next tile's
     // scores N (behind the last tile: of keys that are none, for nothing).
-    auto turn = [&](v16f (&S)[2], v16f (&N)[2], bool first) __attribute__((always_inline)) {
+    auto turn = [&](v16f (&S)[NH], v16f (&N)[NH], bool first) __attribute__((always_inline)) {
         v8bf F[kAhead];
         steps<kAhead>([&](auto f) { F[f] = read(f); });
         by = scale;
@@ -363,7 +368,7 @@ prompt_attention_kernel(PromptArgs a) {
             if (far) {
 #pragma clang fp contract(off)
 #pragma unroll
-                for (int kt = 0; kt < 2; ++kt)
+                for (int kt = 0; kt < NH; ++kt)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float x = S[kt][i] * scale;
@@ -373,7 +378,7 @@ prompt_attention_kernel(PromptArgs a) {
         }
         top = -__builtin_inff();
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
+        for (int kt = 0; kt < NH; ++kt)
 #pragma unroll
             for (int i = 0; i < 16; ++i) N[kt][i] = 0.f;
         steps<T::kSteps>([&](auto step) {
@@ -388,7 +393,7 @@ prompt_attention_kernel(PromptArgs a) {
             if constexpr (f + kAhead < T::kSteps) F[f % kAhead] = read(std::integral_constant<int, f + kAhead>{});
             constexpr int e0 = T::made(f), e1 = T::made(f + 1);
             steps<e1 - e0>([&](auto e) { weigh(S, e0 + decltype(e)::value); });
-            if constexpr (f >= kLast) highest(N, (f - kLast) * 32 / MT, (f - kLast + 1) * 32 / MT);
+            if constexpr (f >= kLast) highest(N, (f - kLast) * 16 * NH / MT, (f - kLast + 1) * 16 * NH / MT);
         });
         // (made here, beside the products, not where it is known that they are used)
         asm volatile("" : "+v"(sum), "+v"(top));
@@ -396,56 +401,61 @@ prompt_attention_kernel(PromptArgs a) {
         l += sum;
     };
 
-    // ---- the tiles of this key group, from t_first - kg down.  A slot holds the values of a
-    //      turn's tile t and the keys of the next, t - KG; while a turn is taken the slot of the
-    //      next one is copied.  Every wave meets the others once a turn, with or without work. ----
+    // ---- the tiles, from t_first down.  A slot holds the values of a turn's tile t and the
+    //      keys of the next, t - 1; while a turn is taken the slot of the next one is copied.
+    //      Every wave meets the others once a turn, with or without work. ----
+    const int own = r0 / NK;                          // the last NK keys that this wave's rows see, cut by the mask
+    const int t_mine = own >= kg ? (own - kg) / KG : -1;   // the tile with the last of this wave's keys that they see
+    int t = t_first + 1;
     auto stage = [&](int t, int slot) {
-        const int last = blk.len - 1 - kTile * t;   // (only the last tile can pass the sequence's last row)
-        if (t >= KG) kc.tile(kbase + (int64_t)kTile * (t - KG) * a.k.row, lds0 + slot * kTileB);
-        if (t == t_first) vc.last_tile(vbase + (int64_t)kTile * t * a.v.row, lds0 + slot * kTileB + kKeyB, last);
-        else if (t >= 0) vc.tile(vbase + (int64_t)kTile * t * a.v.row, lds0 + slot * kTileB + kKeyB);
+        if (t > 0) kc.tile(kbase + (int64_t)kTile * (t - 1) * a.k.row, lds0 + slot * kTileB);
+        const uint16_t* src = vbase + (int64_t)kTile * t * a.v.row;
+        const uint32_t at = lds0 + slot * kTileB + kKeyB;
+        if (t == t_first) vc.last_tile(src, at, blk.len - 1 - kTile * t);   // (no other can pass the sequence's last row)
+        else if (t >= 0) vc.tile(src, at);
     };
     auto next_turn = [&]() {
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the slot
         tile_barrier();
-        stage(t - KG, slot ^ 1);
+        stage(t - 1, slot ^ 1);
     };
     auto done = [&]() {
-        t -= KG;
+        --t;
         slot ^= 1;
     };
-    while (t + kg >= 0 && (!active || t - KG > t_mine)) {
+    while (t >= 0 && (!active || t - 1 > t_mine)) {
         next_turn();
         done();
     }
-    if (t - KG >= 0 && active) {
+    if (t > 0 && active) {
         next_turn();
         {
             v8bf F[kAhead];
 #pragma unroll
             for (int f = 0; f < kAhead; ++f) F[f] = read_k(f / KS, f % KS);
 #pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
+            for (int kt = 0; kt < NH; ++kt)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) S0[kt][i] = 0.f;
 #pragma unroll
-            for (int f = 0; f < 2 * KS; ++f) {
+            for (int f = 0; f < NH * KS; ++f) {
                 __builtin_amdgcn_sched_barrier(0);
                 S0[f / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(F[f % kAhead], Q[f % KS], S0[f / KS], 0, 0, 0);
-                if (f + kAhead < 2 * KS) F[f % kAhead] = read_k((f + kAhead) / KS, (f + kAhead) % KS);
+                if (f + kAhead < NH * KS) F[f % kAhead] = read_k((f + kAhead) / KS, (f + kAhead) % KS);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
         done();
-        const int mine = t == t_mine ? (r0 & (kTile - 1)) + n - 4 * h : kTile;
+        const bool cut = KG * t + kg == own;
+        const int mine = cut ? r0 % NK + n - 4 * h : NK;
         top = -__builtin_inff();
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 16 * NH; ++i)
             if (32 * (i / 16) + 8 * (i % 16 / 4) + i % 4 > mine) S0[i / 16][i % 16] = -__builtin_inff();
-        highest(S0, 0, 32);
+        highest(S0, 0, 16 * NH);
         next_turn();
         turn(S0, S1, true);
-        if (t == t_mine) {
+        if (cut) {
             float z = 0.f;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -453,9 +463,9 @@ prompt_attention_kernel(PromptArgs a) {
                 for (int i = 0; i < 16; ++i) z = fmaf(O[mt][i], 0.f, z);
             if (wave_ballot(z != z)) {
                 // once more: finite elements as before, the others by which rows see them
-                v8bf see[4];
+                v8bf see[2 * NH];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
+                for (int s = 0; s < 2 * NH; ++s) {
                     v4i u;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -465,14 +475,14 @@ prompt_attention_kernel(PromptArgs a) {
                     see[s] = __builtin_bit_cast(v8bf, u);
                 }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) weigh(S0, e);
+                for (int e = 0; e < 16 * NH; ++e) weigh(S0, e);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     v16f up, down;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) O[mt][i] = up[i] = down[i] = 0.f;
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
+                    for (int s = 0; s < 2 * NH; ++s) {
                         const v4i w = __builtin_bit_cast(v4i, read_v(s, mt));
                         v4i f, p, q;
 #pragma unroll
@@ -505,17 +515,18 @@ prompt_attention_kernel(PromptArgs a) {
             done();
         }
     }
-    while (t + kg >= 0) {
+    while (t >= 0) {
         next_turn();
         done();
     }
 
-    if constexpr (KG > 1) {   // ---- join the key groups ----
-        v4f* there = reinterpret_cast<v4f*>(smem) + wave * (4 * MT * 64) + lane;
-        float2* ml = reinterpret_cast<float2*>(smem + kWaves * MT * 4 * 64 * 16) + wave * 64 + lane;
-        static_assert(KG == 2 && kWaves * 64 * (MT * 64 + 8) <= 4 * kTileB, "the sums fit the tiles' place");
+    if constexpr (KG > 1) {   // ---- join the key groups: a row's sums through LDS to the first ----
+        constexpr int kSums = 4 * MT * 64 * 16;   // bytes of a wave's
+        static_assert(kWaves * (kSums + 64 * 8) <= kLds<D, V, RG, KG, NK> && kLds<D, V, RG, KG, NK> <= 160 * 1024, "LDS");
+        v4f* there = reinterpret_cast<v4f*>(smem + wave * kSums) + lane;
+        float2* ml = reinterpret_cast<float2*>(smem + kWaves * kSums) + wave * 64 + lane;
         tile_barrier();
-        if (kg == 1) {
+        if (kg > 0) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -524,23 +535,37 @@ prompt_attention_kernel(PromptArgs a) {
             *ml = float2{m, l};
         }
         tile_barrier();
-        if (kg == 1) return;
-        const float2 x = *ml;
-        const float to = fmaxf(m, x.x);
-        const float f = __builtin_amdgcn_exp2f(m - to), fx = __builtin_amdgcn_exp2f(x.x - to);
-        m = to;
-        l = l * f + x.y * fx;
+        if (kg > 0) return;
+        float2 x[KG];
+        x[0] = float2{m, l};
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int i = 1; i < KG; ++i) {
+            x[i] = ml[i * RG * 64];
+            m = fmaxf(m, x[i].x);
+        }
+        l = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) O[mt][i] = O[mt][i] * f + there[(4 * mt + i / 4) * 64][i % 4] * fx;
+        for (int i = 0; i < KG; ++i) {
+            x[i].x = __builtin_amdgcn_exp2f(x[i].x - m);
+            l += x[i].y * x[i].x;
+        }
+#pragma unroll
+        for (int e = 0; e < 4 * MT; ++e) {
+            v4f o = v4f{O[e / 4][e % 4 * 4], O[e / 4][e % 4 * 4 + 1], O[e / 4][e % 4 * 4 + 2], O[e / 4][e % 4 * 4 + 3]} *
+                    x[0].x;
+#pragma unroll
+            for (int i = 1; i < KG; ++i) o += there[i * RG * (kSums / 16) + e * 64] * x[i].x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) O[e / 4][e % 4 * 4 + j] = o[j];
+            if (e % 4 == 3) asm volatile("" : "+v"(O[e / 4]) : : "memory");   // (a block's reads at a time: registers)
+        }
     }
 
     // ---- write: rows through LDS, so that a store takes whole ones ----
     l += __shfl_xor(l, 32, kWave);
     constexpr int kOutB = 2 * V + 16;
-    unsigned char* rows_at = smem + wave * (KG > 1 ? MT * 4 * 64 * 16 : 32 * kOutB);
-    static_assert(32 * kOutB <= MT * 4 * 64 * 16 && kWaves * 32 * kOutB <= 2 * kTileB, "the rows fit the sums' or tiles' place");
+    unsigned char* rows_at = smem + rg * (KG > 1 ? MT * 4 * 64 * 16 : 32 * kOutB);
+    static_assert(32 * kOutB <= MT * 4 * 64 * 16 && RG * 32 * kOutB <= 2 * kTileB, "the rows fit the sums' or tiles' place");
     if constexpr (KG == 1) tile_barrier();
     if (!active) return;
     const float inv = 1.f / l;
@@ -552,44 +577,52 @@ prompt_attention_kernel(PromptArgs a) {
                 l == 0.f ? uint2{0, 0}
                          : uint2{pack_bf16(O[mt][4 * i] * inv, O[mt][4 * i + 1] * inv),
                                  pack_bf16(O[mt][4 * i + 2] * inv, O[mt][4 * i + 3] * inv)};
-    const int64_t first_row = out_row + (int64_t)(32 * wave) * a.H;
+    const int64_t first_row = out_row + (int64_t)(32 * rg) * a.H;
 #pragma unroll
     for (int i = 0; i < VP / 2; ++i) {
         const int r = i * (64 / VP) + lane / VP, c = lane % VP;
         const v4i x = *reinterpret_cast<const v4i*>(rows_at + r * kOutB + 16 * c);
-        if (32 * wave + r < rows) *reinterpret_cast<v4i*>(a.out + (first_row + (int64_t)r * a.H) * V + 8 * c) = x;
+        if (32 * rg + r < rows) *reinterpret_cast<v4i*>(a.out + (first_row + (int64_t)r * a.H) * V + 8 * c) = x;
     }
-    if (a.lse && h == 0 && 32 * wave + n < rows)
+    if (a.lse && h == 0 && 32 * rg + n < rows)
         a.lse[first_row + (int64_t)n * a.H] = l == 0.f ? -__builtin_inff() : (m + log2f(l)) * 0.693147180559945f;
 }
 
-template <int D, int V, int KG>
+int64_t blocks_of(int T, int B, int H, int rows) { return ((int64_t)T / rows + B + 1) * H; }
+
+template <int D, int V, int RG, int KG, int NK>
 hipError_t run(const PromptArgs& a, hipStream_t stream) {
     static PerDevice<int> once;
-    constexpr int lds = KG * 2 * kTile * 2 * (D + V);
-    const hipError_t e = set_lds_limit(once, (const void*)prompt_attention_kernel<D, V, KG>, lds);
+    constexpr int lds = kLds<D, V, RG, KG, NK>;
+    const hipError_t e = set_lds_limit(once, (const void*)prompt_attention_kernel<D, V, RG, KG, NK>, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((prompt_attention_kernel<D, V, KG>), dim3((unsigned)prompt_blocks(a.T, a.B, a.H)),
-                       dim3(64 * kWaves * KG), lds, stream, a);
+    hipLaunchKernelGGL((prompt_attention_kernel<D, V, RG, KG, NK>),
+                       dim3((unsigned)blocks_of(a.T, a.B, a.H, 32 * RG)), dim3(64 * RG * KG), lds, stream, a);
     return hipGetLastError();
 }
 
-// Two key groups where the blocks leave waves' places free and sequences are long
-// enough: with up to 640 blocks (256 CUs hold 512 of one group) and more than 256
-// rows a sequence.  Of 128 columns, one and two groups: 2048 rows of 16 heads (272
-// blocks) 38.9 and 33.3 us, 8192 of 8 (528) 165 and 142, 2048 of 32 (576) 48.6 and
-// 47.3, 8192 of 16 (1056) 269 and 272; 256 rows of 16 heads 10.1 and 10.2, 64 6.2
-// and 7.5.
+// The form of a call, by about how many blocks of 64 and 128 rows there are (256 CUs
+// hold 512 workgroups of four waves, 256 of eight) and the sequences' mean length:
+// blocks of 64 rows and four key groups while each has a CU of its own, or two in a
+// row where they are long; 128 rows and two key groups for up to two workgroups a
+// CU; else 128 rows and one group.  Of 128 columns, in that order, us: 128 rows of 8
+// heads 7.9, 8.2, 7.9; 512 of 32 12.3, 14.0, 14.4; 512 of 40 17.1, 14.1, 14.5; 1024 of
+// 32 23.8, 20.7, 22.4; 2048 of 8 23.5, 31.0, 36.5, of 16 32.1, 32.3, 36.9, of 32 62.4,
+// 46.7, 48.2; 8192 of 1 65.8, 96.9, 121, of 4 90, 106, 125, of 8 174, 147, 169, of 12
+// 264, 230, 226.
 template <int D, int V>
 hipError_t run(const PromptArgs& a, hipStream_t stream) {
-    const bool two = prompt_blocks(a.T, a.B, a.H) <= 640 && (int64_t)a.T > 256 * (int64_t)a.B;
-    return two ? run<D, V, 2>(a, stream) : run<D, V, 1>(a, stream);
+    const int64_t mean = a.T / a.B;
+    const int64_t narrow = (2 * ((int64_t)a.T / 64) + a.B) * a.H / 2, wide = (2 * ((int64_t)a.T / 128) + a.B) * a.H / 2;
+    if ((narrow <= 300 && mean > 128) || (narrow <= 540 && mean >= 2048)) return run<D, V, 2, 4, 32>(a, stream);
+    if (wide <= 560 && mean >= 512) return run<D, V, 4, 2, 64>(a, stream);
+    return run<D, V, 4, 1, 64>(a, stream);
 }
 
 }  // namespace
 
-// At most floor(T / kRows) whole blocks and a rest of each of the B sequences and of the rows behind them.
-int64_t prompt_blocks(int T, int B, int H) { return ((int64_t)T / kRows + B + 1) * H; }
+// At most floor(T / 128) whole blocks and a rest of each of the B sequences and of the rows behind them.
+int64_t prompt_blocks(int T, int B, int H) { return blocks_of(T, B, H, 128); }
 
 hipError_t launch_prompt_attention(const PromptArgs& a, int D, hipStream_t stream) {
     if (a.T <= 0) return hipSuccess;
