@@ -38,9 +38,7 @@ namespace {
 
 constexpr int kPage = 64;
 constexpr int kKeys = 32;      // positions of a wave's tile
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kRound = kKeys * kWaves;
+constexpr int kJoinThreads = 256;
 constexpr int kMaxRuns = 512;  // runs of a sequence
 
 // What an entry without a row is copied from.
@@ -49,6 +47,7 @@ static __device__ __align__(16) const unsigned char kZeros[256] = {};
 struct KvPlan {
     int rows;     // query heads of a workgroup: 16, 32 or 64
     int hb;       // workgroups for the heads of one key/value head
+    int waves;    // of a workgroup
     int run;      // positions of a run
     int slots;    // runs of a sequence
     float* part_o;      // [slots][B * H][D]
@@ -68,25 +67,26 @@ __device__ __forceinline__ int permute(int r) {
     return (r >> 2 & 1) | ((r >> 3 ^ r >> 4) & 1) << 1;
 }
 
-template <int D, int MT, bool FP8>
+template <int D, int MT, bool FP8, int W>
 struct Lds {
     static constexpr int RB = D * (FP8 ? 1 : 2);
     static constexpr int kRows = kKeys * RB;              // keys or values of a tile
     static constexpr int kTile = 2 * kRows + (FP8 ? 2 * kKeys * 4 : 0);
     static constexpr int kSumB = D * 4 + 16;              // a row of sums, padded
     static constexpr int kSums = 16 * MT * kSumB;         // a wave's sums
-    static constexpr int kTiles = kWaves * 2 * kTile;
-    static constexpr int kMl = kWaves * kSums;            // (maximum, sum) of each wave's rows
-    static constexpr int kJoin = kMl + kWaves * 16 * MT * 8;
+    static constexpr int kTiles = W * 2 * kTile;
+    static constexpr int kMl = W * kSums;            // (maximum, sum) of each wave's rows
+    static constexpr int kJoin = kMl + W * 16 * MT * 8;
     static constexpr int kBytes = kTiles > kJoin ? kTiles : kJoin;
     static_assert(kBytes <= 160 * 1024, "LDS budget");
 };
 
-template <int D, int MT, bool TOPK, bool FP8>
-__global__ void __launch_bounds__(kThreads, MT == 4 ? 1 : 2)
+template <int D, int MT, bool TOPK, bool FP8, int W>
+__global__ void __launch_bounds__(64 * W, MT == 4 ? 1 : 2)
 kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
     extern __shared__ __align__(16) unsigned char smem[];
-    using L = Lds<D, MT, FP8>;
+    using L = Lds<D, MT, FP8, W>;
+    constexpr int kRound = kKeys * W, kThreads = 64 * W;
     constexpr int RB = L::RB, KS = D / 32, CT = D / 16;
     constexpr int PL = RB / 16, RPC = 64 / PL, NC = kKeys / RPC;   // lanes of a row; rows and number of copies
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
@@ -189,7 +189,7 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
                 inv_unit = 1.f / unit;
             }
         }
-        stage(row, 0);
+        if (wave_ballot(row >= 0)) stage(row, 0);
         int buf = 0;
         for (; c < end; c += kRound, buf ^= 1) {
             __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the tile, and the loads behind it
@@ -199,7 +199,8 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
             page1 = page(s2);
             s1 = s2;
             s2 = entry(c + 3 * kRound);
-            if (c + kRound < end) stage(row, buf ^ 1);
+            if (wave_ballot(row >= 0)) stage(row, buf ^ 1);
+            if (here == 0) continue;   // (no row: nothing was copied)
             const unsigned char* kt = smem + wave * 2 * L::kTile + buf * L::kTile;
             const unsigned char* vt = kt + L::kRows;
             // ---- scores ----
@@ -311,7 +312,7 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
     for (int mt = 0; mt < MT; ++mt) {
         float to = m[mt];
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) to = fmaxf(to, ml[w * 16 * MT + 16 * mt + n].x);
+        for (int w = 0; w < W; ++w) to = fmaxf(to, ml[w * 16 * MT + 16 * mt + n].x);
         const float f = __builtin_amdgcn_exp2f(m[mt] - to) * unit;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
@@ -324,10 +325,10 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
         const int r = i / (D / 4), col = 4 * (i % (D / 4));
         float to = ml[r].x, sum = 0.f;
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) to = fmaxf(to, ml[w * 16 * MT + r].x);
+        for (int w = 1; w < W; ++w) to = fmaxf(to, ml[w * 16 * MT + r].x);
         v4f o = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < W; ++w) {
             const float2 x = ml[w * 16 * MT + r];
             sum += x.y * __builtin_amdgcn_exp2f(x.x - to);
             o += *reinterpret_cast<const v4f*>(smem + w * L::kSums + r * L::kSumB + 4 * col);
@@ -349,11 +350,11 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
 // One workgroup a row: its threads weigh the runs, then a lane takes 4 columns of
 // every run that is its wave part's.
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kJoinThreads)
 kv_join_kernel(KvDecodeArgs a, KvPlan p) {
-    constexpr int N = D / 4, kParts = kThreads / N;   // lanes of a run's row, runs at once
+    constexpr int N = D / 4, kParts = kJoinThreads / N;   // lanes of a run's row, runs at once
     __shared__ float weights[kMaxRuns];
-    __shared__ float red[2][kWaves];
+    __shared__ float red[2][(kJoinThreads / 64)];
     __shared__ v4f sums[kParts][N];
     const int wave = uniform((int)threadIdx.x >> 6), lane = lane_id();
     const int64_t row = blockIdx.x, rows = (int64_t)a.B * a.H;
@@ -362,11 +363,11 @@ kv_join_kernel(KvDecodeArgs a, KvPlan p) {
     const int runs = min((len + p.run - 1) / p.run, p.slots);
     const int part = (int)threadIdx.x / N, col = 4 * ((int)threadIdx.x % N);
     const float* at = p.part_o + row * D + col;
-    float2 ml[kMaxRuns / kThreads];
+    float2 ml[kMaxRuns / kJoinThreads];
     float to = -3.402823466e38f;
 #pragma unroll
-    for (int i = 0; i < kMaxRuns / kThreads; ++i) {
-        const int s = i * kThreads + (int)threadIdx.x;
+    for (int i = 0; i < kMaxRuns / kJoinThreads; ++i) {
+        const int s = i * kJoinThreads + (int)threadIdx.x;
         ml[i] = s < runs ? p.part_ml[s * rows + row] : float2{-3.402823466e38f, 0.f};
         to = fmaxf(to, ml[i].x);
     }
@@ -375,13 +376,13 @@ kv_join_kernel(KvDecodeArgs a, KvPlan p) {
     if (lane == 0) red[0][wave] = to;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) to = fmaxf(to, red[0][w]);
+    for (int w = 0; w < (kJoinThreads / 64); ++w) to = fmaxf(to, red[0][w]);
     float l = 0.f;
 #pragma unroll
-    for (int i = 0; i < kMaxRuns / kThreads; ++i) {
+    for (int i = 0; i < kMaxRuns / kJoinThreads; ++i) {
         const float f = __builtin_amdgcn_exp2f(ml[i].x - to);
         l += ml[i].y * f;
-        weights[i * kThreads + (int)threadIdx.x] = f;
+        weights[i * kJoinThreads + (int)threadIdx.x] = f;
     }
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) l += __shfl_xor(l, d, kWave);
@@ -389,7 +390,7 @@ kv_join_kernel(KvDecodeArgs a, KvPlan p) {
     __syncthreads();
     l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) l += red[1][w];
+    for (int w = 0; w < (kJoinThreads / 64); ++w) l += red[1][w];
     v4f o = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
     for (int s = part; s < runs; s += kParts) o += *reinterpret_cast<const v4f*>(at + s * rows * D) * weights[s];
@@ -406,26 +407,28 @@ kv_join_kernel(KvDecodeArgs a, KvPlan p) {
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // Workgroups that the card holds at once.
-int resident(int D, int rows, bool fp8) {
-    int lds = 0;
-    if (D == 64) lds = rows == 16 ? (fp8 ? Lds<64, 1, true>::kBytes : Lds<64, 1, false>::kBytes)
-                       : rows == 32 ? (fp8 ? Lds<64, 2, true>::kBytes : Lds<64, 2, false>::kBytes)
-                                    : (fp8 ? Lds<64, 4, true>::kBytes : Lds<64, 4, false>::kBytes);
-    else lds = rows == 16 ? (fp8 ? Lds<128, 1, true>::kBytes : Lds<128, 1, false>::kBytes)
-               : rows == 32 ? (fp8 ? Lds<128, 2, true>::kBytes : Lds<128, 2, false>::kBytes)
-                            : (fp8 ? Lds<128, 4, true>::kBytes : Lds<128, 4, false>::kBytes);
-    const int n = 160 * 1024 / lds, by_registers = rows == 64 ? 2 : 4;
-    return 256 * (n < by_registers ? n : by_registers);
+template <int D, int W>
+int held_by_lds(int rows, bool fp8) {
+    const int lds = rows == 16   ? (fp8 ? Lds<D, 1, true, W>::kBytes : Lds<D, 1, false, W>::kBytes)
+                    : rows == 32 ? (fp8 ? Lds<D, 2, true, W>::kBytes : Lds<D, 2, false, W>::kBytes)
+                                 : (fp8 ? Lds<D, 4, true, W>::kBytes : Lds<D, 4, false, W>::kBytes);
+    return 160 * 1024 / lds;
+}
+int held(int D, int rows, bool fp8, int waves) {
+    const int by_lds = D == 64 ? (waves == 1 ? held_by_lds<64, 1>(rows, fp8) : held_by_lds<64, 4>(rows, fp8))
+                               : (waves == 1 ? held_by_lds<128, 1>(rows, fp8) : held_by_lds<128, 4>(rows, fp8));
+    const int by_registers = (rows == 64 ? 8 : 16) / waves;
+    return 256 * (by_lds < by_registers ? by_lds : by_registers);
 }
 
-// Microseconds of runs of `run` rounds of 128 positions, by what was measured: 3 until
-// a workgroup's first tile and for its join of the waves; a round its bytes' share of
-// 5.9 TB/s or, with part of the card, 0.75 (fp8: 1) and 0.6 of that; 2.5 for the
-// second kernel and 0.03 a run.  8 heads of 128
-// columns, one context of 32768, bf16: 49.6 us in runs of 1 round, 30.4 of 4, 27.6 of
-// 8, 28.1 of 16, 40.6 of 32; 8 contexts of 8192: 58.2, 54.5, 52.0 and 58.4 of 4 to 32;
-// 64 contexts of 4096 to 32768: 978, 855, 824, 817 and, of 128, 853: runs of up to
-// 32 rounds keep contexts of different lengths even.
+// Microseconds of runs of `run` rounds (32 positions a wave), by what was measured: 3
+// until a workgroup's first tile and for its join of the waves; a round its bytes'
+// share of 5.9 TB/s or, with part of the card, 0.75 (fp8: 1) and 0.6 of that; 2.5 for
+// the second kernel and 0.03 a run.  8 heads of 128 columns, bf16, in runs of 1, 4, 8,
+// 16, 32 and 128 rounds of four waves: one context of 32768 49.7, 31.2, 28.9, 29.1,
+// 45.7 and 154 us; 8 of 8192 86, 57.9, 54.4, 52.3 and 59.2; 64 of 4096 to 32768 1575,
+// 973, 860, 824, 822 and 860.  One wave a workgroup and four: 128 contexts of 64 9.2
+// and 17.3, of 300 23.2 and 27.9, of 1024 92 and 96; fp8, 1024, 60.0 and 55.8.
 double run_cost(int64_t blocks, int64_t rounds, int64_t run, int held, int round_bytes, bool fp8) {
     const int64_t slots = ceil_div(rounds, run), wgs = blocks * slots, at_once = wgs < held ? wgs : held;
     const double share = 1e-6 * round_bytes * (double)at_once / 5.9, part = (fp8 ? 1. : 0.75) + 0.6 * share;
@@ -438,49 +441,63 @@ KvPlan make_plan(int B, int H, int G, int D, int max_ctx, int K, bool fp8) {
     KvPlan p{};
     p.rows = R <= 16 ? 16 : R <= 32 ? 32 : 64;
     p.hb = ceil_div(R, p.rows);
-    const int64_t len = K > 0 ? K : max_ctx;
-    const int64_t blocks = (int64_t)B * G * p.hb, rounds = ceil_div(len, kRound);
-    const int held = resident(D, p.rows, fp8), round_bytes = kRound * 2 * D * (fp8 ? 1 : 2);
-    int64_t run = 32;
+    const int64_t len = K > 0 ? K : max_ctx, blocks = (int64_t)B * G * p.hb;
+    p.waves = 4;
+    int64_t run = 32;   // runs of up to 32 rounds keep contexts of different lengths even
     double best = 1e300;
+    const int64_t rounds4 = ceil_div(len, kKeys * 4);
     for (const int r : {32, 24, 16, 12, 8, 6, 4, 3, 2, 1}) {
-        const double us = run_cost(blocks, rounds, r, held, round_bytes, fp8);
+        const double us = run_cost(blocks, rounds4, r, held(D, p.rows, fp8, 4), kKeys * 4 * 2 * D * (fp8 ? 1 : 2), fp8);
         if (us < best) {
             best = us;
             run = r;
         }
     }
+    // short contexts, each with one wave for all of it
+    if (len <= (fp8 ? 512 : 1024)) {
+        const int64_t rounds1 = len > 0 ? ceil_div(len, kKeys) : 1;
+        if (run_cost(blocks, rounds1, rounds1, held(D, p.rows, fp8, 1), kKeys * 2 * D * (fp8 ? 1 : 2), fp8) < best) {
+            p.waves = 1;
+            run = rounds1;
+        }
+    }
+    const int64_t rounds = ceil_div(len, kKeys * p.waves);
     // (a launch holds less than 2^32 threads)
     while (ceil_div(rounds, run) > kMaxRuns || ceil_div(rounds, run) * blocks >= (int64_t)1 << 24) run *= 2;
-    p.run = (int)(run * kRound);
+    p.run = (int)(run * kKeys * p.waves);
     p.slots = len > 0 ? ceil_div(len, p.run) : 1;
     return p;
 }
 
-template <int D, int MT, bool TOPK, bool FP8>
+template <int D, int MT, bool TOPK, bool FP8, int W>
 hipError_t run(const KvDecodeArgs& a, const KvPlan& p, hipStream_t stream) {
     static PerDevice<int> once;
-    constexpr int lds = Lds<D, MT, FP8>::kBytes;
-    const hipError_t e = set_lds_limit(once, (const void*)kv_decode_kernel<D, MT, TOPK, FP8>, lds);
+    constexpr int lds = Lds<D, MT, FP8, W>::kBytes;
+    const hipError_t e = set_lds_limit(once, (const void*)kv_decode_kernel<D, MT, TOPK, FP8, W>, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((kv_decode_kernel<D, MT, TOPK, FP8>), dim3((unsigned)(p.slots * a.B * a.G * p.hb)),
-                       dim3(kThreads), lds, stream, a, p);
+    hipLaunchKernelGGL((kv_decode_kernel<D, MT, TOPK, FP8, W>), dim3((unsigned)(p.slots * a.B * a.G * p.hb)),
+                       dim3(64 * W), lds, stream, a, p);
     return hipGetLastError();
 }
 
-template <int D, int MT>
+template <int D, int MT, int W>
 hipError_t run(const KvDecodeArgs& a, const KvPlan& p, bool fp8, hipStream_t stream) {
-    if (a.idx) return fp8 ? run<D, MT, true, true>(a, p, stream) : run<D, MT, true, false>(a, p, stream);
-    return fp8 ? run<D, MT, false, true>(a, p, stream) : run<D, MT, false, false>(a, p, stream);
+    if (a.idx) return fp8 ? run<D, MT, true, true, W>(a, p, stream) : run<D, MT, true, false, W>(a, p, stream);
+    return fp8 ? run<D, MT, false, true, W>(a, p, stream) : run<D, MT, false, false, W>(a, p, stream);
+}
+
+template <int D, int W>
+hipError_t run(const KvDecodeArgs& a, const KvPlan& p, bool fp8, hipStream_t stream) {
+    return p.rows == 16   ? run<D, 1, W>(a, p, fp8, stream)
+           : p.rows == 32 ? run<D, 2, W>(a, p, fp8, stream)
+                          : run<D, 4, W>(a, p, fp8, stream);
 }
 
 template <int D>
 hipError_t run(const KvDecodeArgs& a, const KvPlan& p, bool fp8, hipStream_t stream) {
-    const hipError_t e = p.rows == 16   ? run<D, 1>(a, p, fp8, stream)
-                         : p.rows == 32 ? run<D, 2>(a, p, fp8, stream)
-                                        : run<D, 4>(a, p, fp8, stream);
+    const hipError_t e = p.waves == 1 ? run<D, 1>(a, p, fp8, stream) : run<D, 4>(a, p, fp8, stream);
     if (e != hipSuccess || p.slots == 1) return e;
-    hipLaunchKernelGGL(kv_join_kernel<D>, dim3((unsigned)(a.B * a.H)), dim3(kThreads), 0, stream, a, p);
+    hipLaunchKernelGGL(kv_join_kernel<D>, dim3((unsigned)(a.B * a.H)), dim3(kJoinThreads), 0, stream, a, p);
     return hipGetLastError();
 }
 

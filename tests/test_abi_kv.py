@@ -132,3 +132,14 @@ def test_wrappers_refuse(lib):
         dsa.kv_append_rope(k, k, n, n, table, cache, cache)
     with pytest.raises(ValueError, match="k must be"):
         dsa.kv_append_rope(k.half(), k, n, n, table, cache, cache)
+
+
+def test_workspace_queries_of_nothing(lib):
+    """A bound or a list of length 0 and 1 are sizes like others."""
+    import dsa_lightning_indexer_03_amd as dsa
+
+    for B in (1, 300, 5000):
+        for fp8 in (False, True):
+            for n in (0, 1, 32, 33, 512, 513, 1024, 1025):
+                assert dsa.kv_decode_workspace_bytes(B, 8, 2, 64, n, fp8=fp8) % (B * 8 * 66 * 4) == 0
+                assert dsa.kv_decode_workspace_bytes(B, 8, 2, 128, 64, topk=n, fp8=fp8) % (B * 8 * 130 * 4) == 0
