@@ -652,6 +652,9 @@ def latent_attention_shared(q, latent_cache, prefix_table, prefix_len: int, bloc
     return out, lse
 
 
+_grad_enabled = torch.is_grad_enabled
+
+
 def _heads(t, name: str, index: int, dtypes):
     """Token and head stride (elements) of a [T, heads, columns] tensor on GPU `index` whose rows are contiguous."""
     if t.dtype not in dtypes:
@@ -666,20 +669,31 @@ def _heads(t, name: str, index: int, dtypes):
     return s[0], s[1]
 
 
-def _kv_caches(index: int, k_cache, v_cache, k_scale, v_scale, G: int, D: int, *others):
+def _kv_caches(index: int, k_cache, v_cache, k_scale, v_scale, G: int, D: int):
     """Checks of the paged key and value caches; returns (P, page, dtype code)."""
-    _all(index, (("k_cache", k_cache, _LATENT), ("v_cache", v_cache, _LATENT), ("k_scale", k_scale, _FLOATS),
-                 ("v_scale", v_scale, _FLOATS), *others))
-    shape = k_cache.shape
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if index < 0 or dtype not in _LATENT or v_cache.dtype not in _LATENT or k_cache.get_device() != index or \
+            v_cache.get_device() != index or not k_cache.is_contiguous() or not v_cache.is_contiguous() or \
+            k_scale is not None or v_scale is not None:
+        _all(index, (("k_cache", k_cache, _LATENT), ("v_cache", v_cache, _LATENT), ("k_scale", k_scale, _FLOATS),
+                     ("v_scale", v_scale, _FLOATS)))
     if len(shape) != 4 or shape[1] != G or shape[3] != D or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [P, G, page, D] with the G and D of the other tensors")
-    fp8 = k_cache.dtype in _CODES
+    fp8 = dtype in _CODES
     if (v_cache.dtype in _CODES) != fp8:
         raise ValueError("k_cache and v_cache must both be bf16 or both fp8")
-    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if fp8 != (s is not None) or (fp8 and s.shape != shape[:3]):
-            raise ValueError(f"{name} [P, G, page] goes with fp8 caches, None with bf16 ones")
+    if fp8 or k_scale is not None or v_scale is not None:
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if fp8 != (s is not None) or (fp8 and s.shape != shape[:3]):
+                raise ValueError(f"{name} [P, G, page] goes with fp8 caches, None with bf16 ones")
     return shape[0], shape[2], FP8_E4M3 if fp8 else BF16
+
+
+def _indices(index: int, checks) -> None:
+    """(name, int32 tensor), contiguous, on GPU `index`."""
+    for _, t in checks:
+        if t.dtype is not _I32 or t.get_device() != index or not t.is_contiguous():
+            _all(index, [(name, x, _INTS) for name, x in checks])
 
 
 def kv_append_rope(k, v, seq_ids, positions, block_table, k_cache, v_cache, cos_sin=None, k_scale=None, v_scale=None,
@@ -699,16 +713,19 @@ def kv_append_rope(k, v, seq_ids, positions, block_table, k_cache, v_cache, cos_
     ks, kh = _heads(k, "k", index, _NEW)
     vs, vh = _heads(v, "v", index, _NEW)
     T, G, D = k.shape
-    if v.shape != k.shape or (v.dtype == torch.float32) != (k.dtype == torch.float32):
+    if v.shape != k.shape or (v.dtype is _F32) != (k.dtype is _F32):
         raise ValueError("k and v must be [T, G, D] of one type")
-    P, page, dt = _kv_caches(index, k_cache, v_cache, k_scale, v_scale, G, D, ("cos_sin", cos_sin, _FLOATS),
-                             ("seq_ids", seq_ids, _INTS), ("positions", positions, _INTS),
-                             ("block_table", block_table, _INTS))
+    P, page, dt = _kv_caches(index, k_cache, v_cache, k_scale, v_scale, G, D)
+    _indices(index, (("seq_ids", seq_ids), ("positions", positions), ("block_table", block_table)))
+    if cos_sin is not None and (cos_sin.dtype is not _F32 or cos_sin.get_device() != index or
+                                not cos_sin.is_contiguous()):
+        _all(index, (("cos_sin", cos_sin, _FLOATS),))
     if block_table.dim() != 2 or (cos_sin is not None and cos_sin.dim() != 2):
         raise ValueError("cos_sin must be [rope_len, R] and block_table [B, max_pages]")
     if seq_ids.shape != (T,) or positions.shape != (T,):
         raise ValueError("seq_ids / positions must have one entry per token")
-    _inference_only("kv_append_rope", k, v, cos_sin, k_cache, v_cache, k_scale, v_scale)
+    if _grad_enabled():
+        _inference_only("kv_append_rope", k, v, cos_sin, k_cache, v_cache, k_scale, v_scale)
     B, max_pages = block_table.shape
     rope_len, R = (0, 0) if cos_sin is None else cos_sin.shape
     if _current_device() != index:
@@ -716,7 +733,7 @@ def kv_append_rope(k, v, seq_ids, positions, block_table, k_cache, v_cache, cos_
             return kv_append_rope(k, v, seq_ids, positions, block_table, k_cache, v_cache, cos_sin, k_scale, v_scale,
                                   interleaved)
     st = lib.indexer_kv_append_rope(k.data_ptr(), ks, kh, v.data_ptr(), vs, vh,
-                                    F32 if k.dtype == torch.float32 else BF16, _ptr(cos_sin), rope_len, R,
+                                    F32 if k.dtype is _F32 else BF16, _ptr(cos_sin), rope_len, R,
                                     1 if interleaved else 0, seq_ids.data_ptr(), positions.data_ptr(),
                                     block_table.data_ptr(), B, max_pages, k_cache.data_ptr(), _ptr(k_scale),
                                     v_cache.data_ptr(), _ptr(v_scale), dt, P, T, G, D, page, _raw_stream(index))
@@ -738,14 +755,15 @@ def prompt_attention(q, k, v, cu_seqlens, scale: float, want_lse: bool = False):
     qs, qh = _heads(q, "q", index, _BF16)
     ks, kh = _heads(k, "k", index, _BF16)
     vs, vh = _heads(v, "v", index, _BF16)
-    _all(index, (("cu_seqlens", cu_seqlens, _INTS),))
+    _indices(index, (("cu_seqlens", cu_seqlens),))
     T, H, D = q.shape
-    G, V = v.shape[1:]
+    _, G, V = v.shape
     if k.shape != (T, G, D) or v.shape[0] != T:
         raise ValueError("q must be [T, H, D], k [T, G, D] and v [T, G, V]")
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must be [B + 1] with B >= 1")
-    _inference_only("prompt_attention", q, k, v)
+    if _grad_enabled():
+        _inference_only("prompt_attention", q, k, v)
     if _current_device() != index:
         with torch.cuda.device(index):
             return prompt_attention(q, k, v, cu_seqlens, scale, want_lse)
@@ -788,14 +806,17 @@ def kv_attention_decode(q, k_cache, v_cache, block_table, context_lens, scale: f
         raise ValueError("q must be [B, H, D] and the caches [P, G, page, D]")
     B, H, D = q.shape
     G = k_cache.shape[1]
-    P, page, dt = _kv_caches(index, k_cache, v_cache, k_scale, v_scale, G, D, ("q", q, _BF16),
-                             ("block_table", block_table, _INTS), ("context_lens", context_lens, _INTS),
-                             ("topk_idx", topk_idx, _INTS))
+    if q.dtype not in _BF16 or not q.is_contiguous():
+        _all(index, (("q", q, _BF16),))
+    P, page, dt = _kv_caches(index, k_cache, v_cache, k_scale, v_scale, G, D)
+    _indices(index, (("block_table", block_table), ("context_lens", context_lens)) if topk_idx is None else
+             (("block_table", block_table), ("context_lens", context_lens), ("topk_idx", topk_idx)))
     if block_table.dim() != 2 or block_table.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("block_table / context_lens shape mismatch")
     if topk_idx is not None and (topk_idx.dim() != 2 or topk_idx.shape[0] != B or topk_idx.shape[1] < 1):
         raise ValueError("topk_idx must be [B, K] with K >= 1")
-    _inference_only("kv_attention_decode", q, k_cache, v_cache, k_scale, v_scale)
+    if _grad_enabled():
+        _inference_only("kv_attention_decode", q, k_cache, v_cache, k_scale, v_scale)
     max_pages = block_table.shape[1]
     mcl = max_pages * page if max_context_len is None else int(max_context_len)
     if mcl >> 31:
@@ -805,7 +826,7 @@ def kv_attention_decode(q, k_cache, v_cache, block_table, context_lens, scale: f
             return kv_attention_decode(q, k_cache, v_cache, block_table, context_lens, scale, topk_idx,
                                        max_context_len, k_scale, v_scale, want_lse, workspace)
     K = 0 if topk_idx is None else topk_idx.shape[1]
-    out = q.new_empty((B, H, D), dtype=torch.bfloat16)
+    out = torch.empty_like(q, dtype=torch.bfloat16)
     lse = q.new_empty((B, H), dtype=torch.float32) if want_lse else None
     nws = lib.indexer_kv_attention_decode_workspace_bytes(B, H, G, D, mcl, K, dt)
     ws = _scratch(workspace, nws, q)

@@ -529,8 +529,8 @@ dsaidx_status indexer_prompt_attention(const void* q, int64_t q_stride, int64_t 
         !heads_ok(v, v_stride, v_head_stride, T, G, 8) || !aligned16(out))
         return fail(DSAIDX_ERR_UNSUPPORTED, "rows of q, k and v and out must be 16-byte aligned");
     // (a tile's rows are addressed with 32 bits)
-    if (q_stride < 0 || k_stride < 0 || v_stride < 0 || q_stride >= 1 << 24 || k_stride >= 1 << 24 ||
-        v_stride >= 1 << 24)
+    if (T > 1 && (q_stride < 0 || k_stride < 0 || v_stride < 0 || q_stride >= 1 << 24 || k_stride >= 1 << 24 ||
+                  v_stride >= 1 << 24))
         return fail(DSAIDX_ERR_UNSUPPORTED, "q_stride=%lld k_stride=%lld v_stride=%lld (in [0, 2^24))",
                     (long long)q_stride, (long long)k_stride, (long long)v_stride);
     dsaidx::PromptArgs a{};
