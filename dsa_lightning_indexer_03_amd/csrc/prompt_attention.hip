@@ -106,23 +106,23 @@ struct Block {
     bool pad;         // rows of no sequence, behind the last one
 };
 
-// Block `item` of all, false: there are fewer.  The rows behind the last
-// sequence count as one more.  With few sequences the blocks come longest first
-// (a block's work grows with its first row), so that the last ones to start are
-// short; else sequence by sequence, which takes one pass over them.
+// Block `item` of the launch, false: none.  The rows behind the last sequence
+// count as one more.  With few sequences the blocks come longest first (a
+// block's work grows with its first row), so that the last ones to start are
+// short.  Else sequence b's blocks have the numbers from cu[b] / kRows + b on,
+// which leaves room for all of them before the next one's, and b is found among
+// 64 places at a time: sequences may be as many as rows.
 template <int kRows>
 __device__ __forceinline__ bool find_block(const PromptArgs& a, int item, Block& out) {
     const int lane = lane_id(), segments = a.B + 1;
-    auto load = [&](int b, int& s, int& e) {
-        s = e = 0;
-        if (b < segments) {
-            s = min(max(a.cu[b], 0), a.T);
-            e = b < a.B ? min(max(a.cu[b + 1], s), a.T) : a.T;
-        }
-    };
-    int s, e, level, found;
+    auto first_row = [&](int b) { return min(max(a.cu[b], 0), a.T); };
+    int start, end, level;
     if (segments <= kWave) {
-        load(lane, s, e);
+        int s = 0, e = 0;
+        if (lane < segments) {
+            s = first_row(lane);
+            e = lane < a.B ? max(first_row(lane + 1), s) : a.T;
+        }
         const int n = (e - s + kRows - 1) / kRows;
         if (item >= (int)wave_sum((uint32_t)n)) return false;
         // largest level with more than `item` blocks at or above it
@@ -135,25 +135,28 @@ __device__ __forceinline__ bool find_block(const PromptArgs& a, int item, Block&
         level = lo;
         const int rank = item - (int)wave_sum((uint32_t)max(n - level - 1, 0));
         const uint64_t mask = wave_ballot(n > level);
-        found = __builtin_ctzll(wave_ballot(n > level && lanes_below(mask) == rank));
+        const int found = __builtin_ctzll(wave_ballot(n > level && lanes_below(mask) == rank));
         out.pad = found == a.B;
+        start = __builtin_amdgcn_readlane(s, found);
+        end = __builtin_amdgcn_readlane(e, found);
     } else {
-        int base = 0, at = 0;
-        uint32_t incl;
-        for (;; at += kWave) {
-            if (at >= segments) return false;
-            load(at + lane, s, e);
-            incl = wave_incl_scan((uint32_t)((e - s + kRows - 1) / kRows));
-            const int all = __builtin_amdgcn_readlane((int)incl, kWave - 1);
-            if (base + all > item) break;
-            base += all;
+        int b = 0, n = segments;
+        while (n > 1) {
+            const int step = (n + kWave - 1) / kWave, at = b + lane * step;
+            const bool in = lane * step < n;
+            const uint64_t upto = wave_ballot(in && first_row(in ? at : b) / kRows + at <= item);
+            const int last = max(__builtin_popcountll(upto) - 1, 0) * step;
+            b += last;
+            n = min(step, n - last);
         }
-        found = __builtin_ctzll(wave_ballot(base + (int)incl > item));
-        level = base + __builtin_amdgcn_readlane((int)incl, found) - 1 - item;
-        out.pad = at + found == a.B;
+        start = uniform(first_row(b));
+        end = b < a.B ? max(uniform(first_row(b + 1)), start) : a.T;
+        out.pad = b == a.B;
+        level = (end - start + kRows - 1) / kRows - 1 - (item - start / kRows - b);
+        if (level < 0) return false;
     }
-    out.start = __builtin_amdgcn_readlane(s, found);
-    out.len = __builtin_amdgcn_readlane(e, found) - out.start;
+    out.start = start;
+    out.len = end - start;
     out.r0 = level * kRows;
     return true;
 }

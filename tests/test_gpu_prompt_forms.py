@@ -115,3 +115,27 @@ def test_the_same_call_twice(form):
     for _ in range(4):
         again = dsa.prompt_attention(*t, cu, 0.1, want_lse=True)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("B,longest", [(64, 5), (65, 300), (4095, 2), (4096, 3), (5000, 1), (300000, 1)])
+def test_as_many_sequences_as_rows(B, longest):
+    """Sequences found 64 places at a time, in one to four steps; empty ones among them."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, longest + 1, B)
+    lens[[0, B // 2, B - 1]] = longest
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    T = int(cu[-1]) + 130
+    t, x = make(rng, T, 2, 1, 64, 64)
+    say(f"{B} sequences of up to {longest} rows")
+    out, lse = dsa.prompt_attention(*(y.cuda() for y in t), ints(cu), 0.125, want_lse=True)
+    torch.cuda.synchronize()
+    assert not bool(out[cu[-1]:].any()) and bool((lse[cu[-1]:] == -float("inf")).all())
+    if longest == 1:
+        assert torch.equal(out[:cu[-1]].cpu(), t[2][:cu[-1]].expand(-1, 2, -1))
+    some = [b for b in np.r_[0:70, rng.integers(0, B, 60), max(0, B - 70):B] if b < B]
+    rows, want = [], []
+    for b in sorted(set(some)):
+        for i in range(cu[b], cu[b + 1]):
+            rows.append(i)
+            want.append(oracle.grouped(x[0][i], x[1][cu[b]:i + 1], x[2][cu[b]:i + 1], 0.125))
+    check(out[rows], lse[rows], want, f"{B} sequences")
