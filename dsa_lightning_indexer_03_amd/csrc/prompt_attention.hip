@@ -9,8 +9,8 @@
 // no more rows than the selection takes).
 //
 // One workgroup takes a head and a block of query rows, 32 to a wave, which
-// carries them alone through both products:
-//   S^T (64 keys x 32 rows) = K Q^T, its queries in registers;
+// carries them through both products:
+//   S^T (keys x 32 rows) = K Q^T, its queries in registers;
 //   O^T (V columns x 32 rows) += V^T P^T.
 // The first product leaves a lane with row lane % 32 and keys 4h .. 4h+3 of
 // every eight (h = lane / 32), which is the second one's operand when its 16
@@ -19,15 +19,32 @@
 // per lane; the exponent's reference moves when a score passes it by 2^kSlack.
 // Sums are fp32; P is rounded to bf16, because the matrix cores take both
 // operands of the second product in one type: an output is off by at most 2^-8
-// of sum P |v| for that, beside its own rounding.  P's sum is taken before the
-// rounding, so that lse does not have it.
+// of sum P |v| for that, beside its own rounding (2.1e-3 rms of the outputs where
+// the rounding alone is 1.6e-3).  P's sum is taken before the rounding, so that
+// lse does not have it.
 //
-// Tiles of 64 keys and values are copied to LDS while the tile before is
-// computed.  A wave walks its keys from its own rows down to the first: the one
-// tile that the causal mask cuts comes first, while the sums are still zero.
-// There, and only there, a masked row can meet a value that is not finite, as 0
-// times it in the product; the sums then are not finite either, and that tile's
-// values are taken again with such elements apart.
+// A turn of a wave makes the probabilities of its keys, 64 of a tile, beside the
+// next tile's scores, and takes these keys' values between those: matrix and
+// vector instructions alternate, and each has about as many cycles as the other
+// (32 rows of 128 columns: 1024 and 900).  Where blocks are few, two or four key
+// groups of waves share a block's tiles and are joined through LDS (choice and
+// figures: run).  Keys and values are copied to LDS by turns, a tile ahead.
+//
+// A wave walks its keys from its own rows down to the first: the one tile that
+// the causal mask cuts comes first, while the sums are still zero.  There, and
+// only there, a masked row can meet a value that is not finite, as 0 times it in
+// the product; the sums then are not finite either, and that tile's values are
+// taken again with such elements apart.
+//
+// Bound by the matrix cores and the power limit, which sets the clock: 32768 rows
+// of 16 heads over 2, 128 columns (4.4 TFLOP): 3.80 ms, 1.16 PFLOP/s, the matrix
+// cores busy 67% of the cycles at about 1.7 GHz, where a bf16 matrix product of
+// 8192 cubed reached 1.16 to 1.36.  64 columns are bound by the vector
+// instructions of the softmax, as many as for 128: 0.93 to 0.96 PFLOP/s; 192 and
+// 128 columns, 8192 rows of 16 heads: 1.06 to 1.09.  16 prompts of 59 to 2331 rows,
+// 16 heads of 192 and 128 columns with keys of their own (79 GFLOP, 252 MB): 102 to
+// 110 us; a workgroup of few tiles waits 2 to 5 us for its first ones.  61 rows: 7
+// us, of which the launch, the first loads and the end are all but one.
 #include <utility>
 
 #include "device_once.h"
