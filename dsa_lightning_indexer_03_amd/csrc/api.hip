@@ -466,7 +466,7 @@ dsaidx_status indexer_kv_append_rope(const void* k, int64_t k_stride, int64_t k_
     if (st != DSAIDX_OK) return st;
     if (cos_sin && (rope_dim % 16 != 0 || rope_dim > D))
         return fail(DSAIDX_ERR_UNSUPPORTED, "rope_dim=%d (a multiple of 16, at most D)", rope_dim);
-    // (up to 32 lanes a token and head, and a launch holds less than 2^32 threads)
+    // (16 lanes a token and head, and a launch holds less than 2^32 threads)
     if ((int64_t)T * G > 1 << 26) return fail(DSAIDX_ERR_UNSUPPORTED, "T * G = %lld > 2^26", (long long)T * G);
     if (T == 0) return DSAIDX_OK;
     if (!k) return fail(DSAIDX_ERR_NULL, "k is NULL");

@@ -169,8 +169,9 @@ __device__ __forceinline__ bool find_block(const PromptArgs& a, int item, Block&
         start = uniform(first_row(b));
         end = b < a.B ? max(uniform(first_row(b + 1)), start) : a.T;
         out.pad = b == a.B;
-        level = (end - start + kRows - 1) / kRows - 1 - (item - start / kRows - b);
-        if (level < 0) return false;
+        const int at = item - start / kRows - b;
+        level = (end - start + kRows - 1) / kRows - 1 - at;
+        if (at < 0 || level < 0) return false;   // (before the first sequence; behind b's last block)
     }
     out.start = start;
     out.len = end - start;
