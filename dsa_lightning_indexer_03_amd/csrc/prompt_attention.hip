@@ -240,17 +240,17 @@ struct Turn {
     }
 };
 
-// LDS of a workgroup: two slots, or the key groups' sums
+// LDS of a workgroup: two slots, the first keys and the queries, or the key groups' sums
 template <int D, int V, int RG, int KG, int NK>
-constexpr int kSlots = 2 * KG * NK * 2 * (D + V);
-template <int D, int V, int RG, int KG, int NK>
-constexpr int kGroupSums = KG > 1 ? RG * KG * (V / 32 * 4 * 64 * 16 + 64 * 8) : 0;
-template <int D, int V, int RG, int KG, int NK>
-constexpr int kLds = kSlots<D, V, RG, KG, NK> > kGroupSums<D, V, RG, KG, NK> ? kSlots<D, V, RG, KG, NK>
-                                                                            : kGroupSums<D, V, RG, KG, NK>;
+constexpr int lds_bytes() {
+    const int slots = 2 * KG * NK * 2 * (D + V), start = KG * NK * 2 * D + RG * KG * 32 * 2 * D;
+    const int sums = KG > 1 ? RG * KG * (V / 32 * 4 * 64 * 16 + 64 * 8) : 0;
+    const int most = slots > start ? slots : start;
+    return most > sums ? most : sums;
+}
 
 template <int D, int V, int RG, int KG, int NK>
-__global__ void __launch_bounds__(64 * RG * KG, 2)
+__global__ void __launch_bounds__(64 * RG * KG, KG == 1 && NK == 32 ? 4 : 2)
 prompt_attention_kernel(PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int KP = D / 8, VP = V / 8;                       // 16-byte pieces of a row
@@ -259,6 +259,8 @@ prompt_attention_kernel(PromptArgs a) {
     constexpr int KI = kKeyB / 1024 / kWaves, VI = kTile * V * 2 / 1024 / kWaves;  // copies of a wave
     constexpr int kAhead = D >= 128 ? 3 : 4;                    // operand reads in flight
     constexpr int KS = D / 16, MT = V / 32, NH = NK / 32;       // steps of the first product, blocks of the second
+    constexpr int kLds = lds_bytes<D, V, RG, KG, NK>();
+    static_assert(kLds <= 160 * 1024, "LDS");
     const int wave = uniform((int)threadIdx.x >> 6), rg = wave % RG, kg = wave / RG;
     const int lane = lane_id(), n = lane & 31, h = lane >> 5;
 
@@ -295,7 +297,6 @@ prompt_attention_kernel(PromptArgs a) {
     kc.last_tile(kbase + (int64_t)kTile * t_first * a.k.row, lds0, blk.len - 1 - kTile * t_first);
     v8bf Q[KS];   // B operand of 32 rows x 16 columns
     if (active) {
-        static_assert(kWaves * 32 * 2 * D <= kTileB + kTile * V * 2, "the queries fit the first values' place and the second slot");
         const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q.p) + blk.start * a.q.row + head * a.q.head;
         const uint32_t at = lds0 + kKeyB + wave * (32 * 2 * D);
         const Copies<KP, D / 16> qc(0, lane, a.q.row);
@@ -499,28 +500,32 @@ prompt_attention_kernel(PromptArgs a) {
                 for (int e = 0; e < 16 * NH; ++e) weigh(S0, e);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    v16f up, down;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) O[mt][i] = up[i] = down[i] = 0.f;
+                    for (int i = 0; i < 16; ++i) O[mt][i] = 0.f;
 #pragma unroll
                     for (int s = 0; s < 2 * NH; ++s) {
-                        const v4i w = __builtin_bit_cast(v4i, read_v(s, mt));
-                        v4i f, p, q;
+                        v4i w = __builtin_bit_cast(v4i, read_v(s, mt));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            f[i] = (int)finite((uint32_t)w[i]);
-                            p[i] = (int)not_finite((uint32_t)w[i], 0);
-                            q[i] = (int)not_finite((uint32_t)w[i], 0x8000u);
-                        }
-                        O[mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, f),
+                        for (int i = 0; i < 4; ++i) w[i] = (int)finite((uint32_t)w[i]);
+                        O[mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, w),
                                                                         __builtin_bit_cast(v8bf, P[s]), O[mt], 0, 0, 0);
-                        up = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, p), see[s], up, 0, 0, 0);
-                        down = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, q), see[s], down, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (up[i] > 0.f) O[mt][i] += __builtin_inff();
-                        if (down[i] > 0.f) O[mt][i] -= __builtin_inff();
+                    for (const uint32_t sign : {0u, 0x8000u}) {
+                        __builtin_amdgcn_sched_barrier(0);   // (one sign's counts at a time: registers)
+                        v16f seen;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) seen[i] = 0.f;
+#pragma unroll
+                        for (int s = 0; s < 2 * NH; ++s) {
+                            v4i w = __builtin_bit_cast(v4i, read_v(s, mt));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[i] = (int)not_finite((uint32_t)w[i], sign);
+                            seen = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, w), see[s], seen, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (seen[i] > 0.f) O[mt][i] += sign ? -__builtin_inff() : __builtin_inff();
                     }
                 }
             }
@@ -543,7 +548,6 @@ prompt_attention_kernel(PromptArgs a) {
 
     if constexpr (KG > 1) {   // ---- join the key groups: a row's sums through LDS to the first ----
         constexpr int kSums = 4 * MT * 64 * 16;   // bytes of a wave's
-        static_assert(kWaves * (kSums + 64 * 8) <= kLds<D, V, RG, KG, NK> && kLds<D, V, RG, KG, NK> <= 160 * 1024, "LDS");
         v4f* there = reinterpret_cast<v4f*>(smem + wave * kSums) + lane;
         float2* ml = reinterpret_cast<float2*>(smem + kWaves * kSums) + wave * 64 + lane;
         tile_barrier();
@@ -586,7 +590,7 @@ prompt_attention_kernel(PromptArgs a) {
     l += __shfl_xor(l, 32, kWave);
     constexpr int kOutB = 2 * V + 16;
     unsigned char* rows_at = smem + rg * (KG > 1 ? MT * 4 * 64 * 16 : 32 * kOutB);
-    static_assert(32 * kOutB <= MT * 4 * 64 * 16 && RG * 32 * kOutB <= 2 * kTileB, "the rows fit the sums' or tiles' place");
+    static_assert(32 * kOutB <= MT * 4 * 64 * 16 && RG * 32 * kOutB <= kLds, "the rows fit the sums' or tiles' place");
     if constexpr (KG == 1) tile_barrier();
     if (!active) return;
     const float inv = 1.f / l;
@@ -614,7 +618,7 @@ int64_t blocks_of(int T, int B, int H, int rows) { return ((int64_t)T / rows + B
 template <int D, int V, int RG, int KG, int NK>
 hipError_t run(const PromptArgs& a, hipStream_t stream) {
     static PerDevice<int> once;
-    constexpr int lds = kLds<D, V, RG, KG, NK>;
+    constexpr int lds = lds_bytes<D, V, RG, KG, NK>();
     const hipError_t e = set_lds_limit(once, (const void*)prompt_attention_kernel<D, V, RG, KG, NK>, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((prompt_attention_kernel<D, V, RG, KG, NK>),
@@ -626,17 +630,24 @@ hipError_t run(const PromptArgs& a, hipStream_t stream) {
 // hold 512 workgroups of four waves, 256 of eight) and the sequences' mean length:
 // blocks of 64 rows and four key groups while each has a CU of its own, or two in a
 // row where they are long; 128 rows and two key groups for up to two workgroups a
-// CU; else 128 rows and one group.  Of 128 columns, in that order, us: 128 rows of 8
-// heads 7.9, 8.2, 7.9; 512 of 32 12.3, 14.0, 14.4; 512 of 40 17.1, 14.1, 14.5; 1024 of
-// 32 23.8, 20.7, 22.4; 2048 of 8 23.5, 31.0, 36.5, of 16 32.1, 32.3, 36.9, of 32 62.4,
-// 46.7, 48.2; 8192 of 1 65.8, 96.9, 121, of 4 90, 106, 125, of 8 174, 147, 169, of 12
-// 264, 230, 226.
+// CU; else 128 rows and one group, which with 64 columns and many short sequences
+// takes tiles of 32 keys, for four workgroups a CU (128 registers a lane; with 128
+// columns three do not fit).
+// Of 128 columns, in that order, us: 128 rows of 8 heads 7.9, 8.2, 7.9; 512 of 32
+// 12.3, 14.0, 14.4; 512 of 40 17.1, 14.1, 14.5; 1024 of 32 23.8, 20.7, 22.4; 2048 of 8
+// 23.5, 31.0, 36.5, of 16 32.1, 32.3, 36.9, of 32 62.4, 46.7, 48.2; 8192 of 1 65.8, 96.9,
+// 121, of 4 90, 106, 125, of 8 174, 147, 169, of 12 264, 230, 226.
+// Of 64 columns, tiles of 64 and 32 keys: 16 sequences of 128 rows, 32 heads 9.4 and
+// 9.4, 64 heads 16.7 and 13.7; 16 of 512, 8 heads 13.9 and 15.1; 32 of 512, 32 heads
+// 73.3 and 68.8; 16 of 1000, 64 heads 214 and 214; one of 8192, 16 heads 168 and 178.
 template <int D, int V>
 hipError_t run(const PromptArgs& a, hipStream_t stream) {
     const int64_t mean = a.T / a.B;
     const int64_t narrow = (2 * ((int64_t)a.T / 64) + a.B) * a.H / 2, wide = (2 * ((int64_t)a.T / 128) + a.B) * a.H / 2;
     if ((narrow <= 300 && mean > 128) || (narrow <= 540 && mean >= 2048)) return run<D, V, 2, 4, 32>(a, stream);
     if (wide <= 560 && mean >= 512) return run<D, V, 4, 2, 64>(a, stream);
+    if constexpr (D == 64)
+        if (wide > 768 && mean <= 512) return run<D, V, 4, 1, 32>(a, stream);
     return run<D, V, 4, 1, 64>(a, stream);
 }
 
