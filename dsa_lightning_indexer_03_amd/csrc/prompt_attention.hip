@@ -107,12 +107,22 @@ struct Copies {
                         lds + first + i * 1024);
     }
     // The same where row `last` is the last one: rows behind it are that row again.
+    __device__ __forceinline__ uint32_t place(int i, int last) const {
+        return (piece[i % kBase] ^ (uint32_t)(i / kBase % kTurns * kBit)) +
+               (uint32_t)min(row[i % kBase] + i / kBase * kStep, last) * (uint32_t)stride;
+    }
     __device__ __forceinline__ void last_tile(const uint16_t* src, uint32_t lds, int last) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            copy_to_lds(src, (piece[i % kBase] ^ (uint32_t)(i / kBase % kTurns * kBit)) +
-                                 (uint32_t)min(row[i % kBase] + i / kBase * kStep, last) * (uint32_t)stride,
-                        lds + first + i * 1024);
+        for (int i = 0; i < N; ++i) copy_to_lds(src, place(i, last), lds + first + i * 1024);
+    }
+    // The same by way of registers.
+    __device__ __forceinline__ void load(v4i (&x)[N], const uint16_t* src, int last) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = *reinterpret_cast<const v4i*>(reinterpret_cast<const char*>(src) + place(i, last));
+    }
+    __device__ __forceinline__ void store(const v4i (&x)[N], uint32_t lds) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) *lds_pointer<v4i>(lds + first + i * 1024 + lane_id() * 16) = x[i];
     }
 };
 
@@ -250,7 +260,7 @@ constexpr int lds_bytes() {
 }
 
 template <int D, int V, int RG, int KG, int NK>
-__global__ void __launch_bounds__(64 * RG * KG, KG == 1 && NK == 32 ? 4 : 2)
+__global__ void __launch_bounds__(64 * RG * KG, KG == 1 && NK == 32 ? (D == 64 ? 4 : 3) : 2)
 prompt_attention_kernel(PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int KP = D / 8, VP = V / 8;                       // 16-byte pieces of a row
@@ -288,24 +298,30 @@ prompt_attention_kernel(PromptArgs a) {
     // (never 0: a score of -inf has to stay one)
     const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
 
-    // ---- copies: a wave's part of a tile, 1024 bytes each; first of all the first keys and
-    //      the wave's queries, the latter behind the first keys ----
+    // ---- copies: a wave's part of a tile, 1024 bytes each.  What the first turns need
+    //      is loaded at once: the first keys, the wave's queries behind them, and in
+    //      registers, until the queries have left their place, the second slot ----
     const uint32_t lds0 = lds_address(smem);
     const Copies<KP, KI> kc(wave, lane, a.k.row);
     const Copies<VP, VI> vc(wave, lane, a.v.row);
-    const int t_first = (blk.r0 + rows - 1) / kTile;
-    kc.last_tile(kbase + (int64_t)kTile * t_first * a.k.row, lds0, blk.len - 1 - kTile * t_first);
-    v8bf Q[KS];   // B operand of 32 rows x 16 columns
+    const int t_first = (blk.r0 + rows - 1) / kTile, last = blk.len - 1 - kTile * t_first;
+    kc.last_tile(kbase + (int64_t)kTile * t_first * a.k.row, lds0, last);
+    const uint32_t q_at = lds0 + kKeyB + wave * (32 * 2 * D);
     if (active) {
         const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q.p) + blk.start * a.q.row + head * a.q.head;
-        const uint32_t at = lds0 + kKeyB + wave * (32 * 2 * D);
         const Copies<KP, D / 16> qc(0, lane, a.q.row);
-        qc.last_tile(qp + (int64_t)r0 * a.q.row, at, min(31, blk.len - 1 - r0));
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-        asm volatile("" ::: "memory");
+        qc.last_tile(qp + (int64_t)r0 * a.q.row, q_at, min(31, blk.len - 1 - r0));
+    }
+    v4i keys[KI], values[VI];
+    if (t_first > 0) kc.load(keys, kbase + (int64_t)kTile * (t_first - 1) * a.k.row, kTile - 1);
+    vc.load(values, vbase + (int64_t)kTile * t_first * a.v.row, last);   // (no other tile can pass the sequence's last row)
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    asm volatile("" ::: "memory");
+    v8bf Q[KS];   // B operand of 32 rows x 16 columns
+    if (active) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            Q[ks] = lds_read<v8bf>(at + n * (2 * D) + 16 * ((2 * ks + h) ^ permute<KP>(n)));
+            Q[ks] = lds_read<v8bf>(q_at + n * (2 * D) + 16 * ((2 * ks + h) ^ permute<KP>(n)));
             if (a.scale_log2 < 0.f) {   // the products then take the scale's magnitude
                 v4i u = __builtin_bit_cast(v4i, Q[ks]);
                 u ^= (int)0x80008000;
@@ -313,7 +329,9 @@ prompt_attention_kernel(PromptArgs a) {
             }
         }
     }
-
+    tile_barrier();
+    if (t_first > 0) kc.store(keys, lds0 + kTileB);
+    vc.store(values, lds0 + kTileB + kKeyB);
     v16f O[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -339,13 +357,13 @@ prompt_attention_kernel(PromptArgs a) {
     const int v_row = 4 * h + (lane >> 2 & 3);
     const uint32_t v_at = lds0 + kKeyB + (kg * NK + v_row) * (2 * V) +
                           16 * ((2 * (lane >> 4 & 1) + (lane >> 1 & 1)) ^ permute<VP>(v_row)) + 8 * (lane & 1);
-    int slot = 0;
+    uint32_t slot = 0;   // its byte
     auto read_k = [&](int kt, int ks) {   // A operand: 32 keys x 16 columns
         const int c = 2 * ks;
-        return lds_read<v8bf>(((k_at + slot * kTileB) ^ (16 * (c % KPX))) + 16 * (c / KPX * KPX) + kt * (64 * D));
+        return lds_read<v8bf>(((k_at + slot) ^ (16 * (c % KPX))) + 16 * (c / KPX * KPX) + kt * (64 * D));
     };
     auto read_v = [&](int s, int mt) {    // A operand: 32 columns x 16 keys
-        const uint32_t at = (v_at + slot * kTileB) ^ (64 * mt);
+        const uint32_t at = (v_at + slot) ^ (64 * mt);
         const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>(at + s * (32 * V)));
         const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>((at ^ 32) + s * (32 * V) + 16 * V));
         return __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -429,28 +447,23 @@ prompt_attention_kernel(PromptArgs a) {
     const int own = r0 / NK;                          // the last NK keys that this wave's rows see, cut by the mask
     const int t_mine = own >= kg ? (own - kg) / KG : -1;   // the tile with the last of this wave's keys that they see
     int t = t_first + 1;
-    auto stage = [&](int t, int slot) {
-        if (t > 0) kc.tile(kbase + (int64_t)kTile * (t - 1) * a.k.row, lds0 + slot * kTileB);
-        const uint16_t* src = vbase + (int64_t)kTile * t * a.v.row;
-        const uint32_t at = lds0 + slot * kTileB + kKeyB;
-        if (t == t_first) vc.last_tile(src, at, blk.len - 1 - kTile * t);   // (no other can pass the sequence's last row)
-        else if (t >= 0) vc.tile(src, at);
-    };
     auto next_turn = [&]() {
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the slot
         tile_barrier();
-        stage(t - 1, slot ^ 1);
+        const uint32_t at = lds0 + (slot == 0 ? kTileB : 0);
+        if (t > 1) kc.tile(kbase + (int64_t)kTile * (t - 2) * a.k.row, at);
+        if (t > 0) vc.tile(vbase + (int64_t)kTile * (t - 1) * a.v.row, at + kKeyB);
     };
     auto done = [&]() {
         --t;
-        slot ^= 1;
+        slot = slot == 0 ? kTileB : 0;
     };
-    while (t >= 0 && (!active || t - 1 > t_mine)) {
-        next_turn();
+    // (turn t_first + 1, in which no values are taken, has begun above)
+    while (t > 0 && (!active || t - 1 > t_mine)) {
         done();
-    }
-    if (t > 0 && active) {
         next_turn();
+    }
+    if (t > 0) {
         {
             v8bf F[kAhead];
 #pragma unroll
@@ -541,10 +554,6 @@ prompt_attention_kernel(PromptArgs a) {
             done();
         }
     }
-    while (t >= 0) {
-        next_turn();
-        done();
-    }
 
     if constexpr (KG > 1) {   // ---- join the key groups: a row's sums through LDS to the first ----
         constexpr int kSums = 4 * MT * 64 * 16;   // bytes of a wave's
@@ -630,24 +639,27 @@ hipError_t run(const PromptArgs& a, hipStream_t stream) {
 // hold 512 workgroups of four waves, 256 of eight) and the sequences' mean length:
 // blocks of 64 rows and four key groups while each has a CU of its own, or two in a
 // row where they are long; 128 rows and two key groups for up to two workgroups a
-// CU; else 128 rows and one group, which with 64 columns and many short sequences
-// takes tiles of 32 keys, for four workgroups a CU (128 registers a lane; with 128
-// columns three do not fit).
+// CU; else 128 rows and one group, which with 64 and 128 columns and many sequences
+// that are not long takes tiles of 32 keys: half of the scores in registers, 128 and
+// 168 a lane, for four and three workgroups a CU (192 columns do not fit 168).
 // Of 128 columns, in that order, us: 128 rows of 8 heads 7.9, 8.2, 7.9; 512 of 32
 // 12.3, 14.0, 14.4; 512 of 40 17.1, 14.1, 14.5; 1024 of 32 23.8, 20.7, 22.4; 2048 of 8
 // 23.5, 31.0, 36.5, of 16 32.1, 32.3, 36.9, of 32 62.4, 46.7, 48.2; 8192 of 1 65.8, 96.9,
 // 121, of 4 90, 106, 125, of 8 174, 147, 169, of 12 264, 230, 226.
-// Of 64 columns, tiles of 64 and 32 keys: 16 sequences of 128 rows, 32 heads 9.4 and
-// 9.4, 64 heads 16.7 and 13.7; 16 of 512, 8 heads 13.9 and 15.1; 32 of 512, 32 heads
-// 73.3 and 68.8; 16 of 1000, 64 heads 214 and 214; one of 8192, 16 heads 168 and 178.
+// Tiles of 64 and 32 keys, 128 columns: 64 sequences of 128 rows, 32 heads 46.0 and
+// 39.6; 32 of 512, 32 heads 133 and 120; 16 of 1000, 4 heads 30.8 and 34.3, 8 heads 55.0
+// and 55.0, 16 heads 93.2 and 87.8; 8 of 2048, 16 heads 158 and 154; 6 of 4096, 8 heads
+// 206 and 220, 64 heads 1615 and 1583.  64 columns: 16 of 128, 32 heads 9.4 and 9.4, 64
+// heads 16.7 and 13.7; 16 of 512, 8 heads 13.9 and 15.1; 32 of 512, 32 heads 73.3 and
+// 68.8; 16 of 1000, 64 heads 214 and 214; one of 8192, 16 heads 168 and 178.
 template <int D, int V>
 hipError_t run(const PromptArgs& a, hipStream_t stream) {
     const int64_t mean = a.T / a.B;
     const int64_t narrow = (2 * ((int64_t)a.T / 64) + a.B) * a.H / 2, wide = (2 * ((int64_t)a.T / 128) + a.B) * a.H / 2;
     if ((narrow <= 300 && mean > 128) || (narrow <= 540 && mean >= 2048)) return run<D, V, 2, 4, 32>(a, stream);
     if (wide <= 560 && mean >= 512) return run<D, V, 4, 2, 64>(a, stream);
-    if constexpr (D == 64)
-        if (wide > 768 && mean <= 512) return run<D, V, 4, 1, 32>(a, stream);
+    if constexpr (D < 192)
+        if (wide > 768 && mean <= (D == 64 ? 512 : 2048)) return run<D, V, 4, 1, 32>(a, stream);
     return run<D, V, 4, 1, 64>(a, stream);
 }
 

@@ -1,5 +1,5 @@
-"""Every form of prompt_attention (128 rows and one or two key groups, with 64
-columns tiles of 64 and 32 keys, 64 rows and four groups) against the fp64
+"""Every form of prompt_attention (128 rows and one key group with tiles
+of 64 and of 32 keys, or two groups, 64 rows and four groups) against the fp64
 oracle, and against each other's results where the heads of a call only change
 its form."""
 import numpy as np
@@ -15,7 +15,7 @@ pytestmark = pytest.mark.gpu
 DIMS = [(64, 64), (128, 128), (192, 128)]
 # lengths, heads, key/value heads: one group (short or many), two groups, four groups
 FORMS = {"one": ([90, 33, 0, 120, 64], 12, 2), "one, many blocks": ([300] * 3 + [1], 120, 1),
-         "one, longer": ([1300, 900], 44, 2),
+         "one, longer": ([1300, 900], 44, 2), "one, long": ([2200, 2150], 24, 3),
          "two": ([700], 64, 2), "two, ragged": ([900, 130, 0, 1100], 24, 3),
          "four": ([200, 191], 8, 2), "four, one head": ([1100, 65, 129], 1, 1), "four, long": ([2100], 16, 1)}
 
