@@ -107,22 +107,12 @@ struct Copies {
                         lds + first + i * 1024);
     }
     // The same where row `last` is the last one: rows behind it are that row again.
-    __device__ __forceinline__ uint32_t place(int i, int last) const {
-        return (piece[i % kBase] ^ (uint32_t)(i / kBase % kTurns * kBit)) +
-               (uint32_t)min(row[i % kBase] + i / kBase * kStep, last) * (uint32_t)stride;
-    }
     __device__ __forceinline__ void last_tile(const uint16_t* src, uint32_t lds, int last) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i) copy_to_lds(src, place(i, last), lds + first + i * 1024);
-    }
-    // The same by way of registers.
-    __device__ __forceinline__ void load(v4i (&x)[N], const uint16_t* src, int last) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = *reinterpret_cast<const v4i*>(reinterpret_cast<const char*>(src) + place(i, last));
-    }
-    __device__ __forceinline__ void store(const v4i (&x)[N], uint32_t lds) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) *lds_pointer<v4i>(lds + first + i * 1024 + lane_id() * 16) = x[i];
+        for (int i = 0; i < N; ++i)
+            copy_to_lds(src, (piece[i % kBase] ^ (uint32_t)(i / kBase % kTurns * kBit)) +
+                                 (uint32_t)min(row[i % kBase] + i / kBase * kStep, last) * (uint32_t)stride,
+                        lds + first + i * 1024);
     }
 };
 
@@ -260,7 +250,7 @@ constexpr int lds_bytes() {
 }
 
 template <int D, int V, int RG, int KG, int NK>
-__global__ void __launch_bounds__(64 * RG * KG, KG == 1 && NK == 32 ? (D == 64 ? 4 : 3) : 2)
+__global__ void __launch_bounds__(64 * RG * KG, KG > 1 || NK > 32 ? 2 : D == 64 ? 4 : 3)
 prompt_attention_kernel(PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int KP = D / 8, VP = V / 8;                       // 16-byte pieces of a row
@@ -268,6 +258,7 @@ prompt_attention_kernel(PromptArgs a) {
     constexpr int kTile = KG * NK, kKeyB = kTile * D * 2, kTileB = kKeyB + kTile * V * 2;
     constexpr int KI = kKeyB / 1024 / kWaves, VI = kTile * V * 2 / 1024 / kWaves;  // copies of a wave
     constexpr int kAhead = D >= 128 ? 3 : 4;                    // operand reads in flight
+    constexpr bool kFew = KG == 1 && NK == 32;
     constexpr int KS = D / 16, MT = V / 32, NH = NK / 32;       // steps of the first product, blocks of the second
     constexpr int kLds = lds_bytes<D, V, RG, KG, NK>();
     static_assert(kLds <= 160 * 1024, "LDS");
@@ -298,9 +289,8 @@ prompt_attention_kernel(PromptArgs a) {
     // (never 0: a score of -inf has to stay one)
     const float scale = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
 
-    // ---- copies: a wave's part of a tile, 1024 bytes each.  What the first turns need
-    //      is loaded at once: the first keys, the wave's queries behind them, and in
-    //      registers, until the queries have left their place, the second slot ----
+    // ---- copies: a wave's part of a tile, 1024 bytes each; first of all the first keys and
+    //      the wave's queries, behind them, then the second slot, where the queries were ----
     const uint32_t lds0 = lds_address(smem);
     const Copies<KP, KI> kc(wave, lane, a.k.row);
     const Copies<VP, VI> vc(wave, lane, a.v.row);
@@ -312,9 +302,6 @@ prompt_attention_kernel(PromptArgs a) {
         const Copies<KP, D / 16> qc(0, lane, a.q.row);
         qc.last_tile(qp + (int64_t)r0 * a.q.row, q_at, min(31, blk.len - 1 - r0));
     }
-    v4i keys[KI], values[VI];
-    if (t_first > 0) kc.load(keys, kbase + (int64_t)kTile * (t_first - 1) * a.k.row, kTile - 1);
-    vc.load(values, vbase + (int64_t)kTile * t_first * a.v.row, last);   // (no other tile can pass the sequence's last row)
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
     asm volatile("" ::: "memory");
     v8bf Q[KS];   // B operand of 32 rows x 16 columns
@@ -330,8 +317,8 @@ prompt_attention_kernel(PromptArgs a) {
         }
     }
     tile_barrier();
-    if (t_first > 0) kc.store(keys, lds0 + kTileB);
-    vc.store(values, lds0 + kTileB + kKeyB);
+    if (t_first > 0) kc.tile(kbase + (int64_t)kTile * (t_first - 1) * a.k.row, lds0 + kTileB);
+    vc.last_tile(vbase + (int64_t)kTile * t_first * a.v.row, lds0 + kTileB + kKeyB, last);   // (no other tile can pass the sequence's last row)
     v16f O[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -357,13 +344,13 @@ prompt_attention_kernel(PromptArgs a) {
     const int v_row = 4 * h + (lane >> 2 & 3);
     const uint32_t v_at = lds0 + kKeyB + (kg * NK + v_row) * (2 * V) +
                           16 * ((2 * (lane >> 4 & 1) + (lane >> 1 & 1)) ^ permute<VP>(v_row)) + 8 * (lane & 1);
-    uint32_t slot = 0;   // its byte
+    int slot = 0;
     auto read_k = [&](int kt, int ks) {   // A operand: 32 keys x 16 columns
         const int c = 2 * ks;
-        return lds_read<v8bf>(((k_at + slot) ^ (16 * (c % KPX))) + 16 * (c / KPX * KPX) + kt * (64 * D));
+        return lds_read<v8bf>(((k_at + slot * kTileB) ^ (16 * (c % KPX))) + 16 * (c / KPX * KPX) + kt * (64 * D));
     };
     auto read_v = [&](int s, int mt) {    // A operand: 32 columns x 16 keys
-        const uint32_t at = (v_at + slot) ^ (64 * mt);
+        const uint32_t at = (v_at + slot * kTileB) ^ (64 * mt);
         const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>(at + s * (32 * V)));
         const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_pointer<v4s>((at ^ 32) + s * (32 * V) + 16 * V));
         return __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -450,13 +437,15 @@ prompt_attention_kernel(PromptArgs a) {
     auto next_turn = [&]() {
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the slot
         tile_barrier();
-        const uint32_t at = lds0 + (slot == 0 ? kTileB : 0);
+        const uint32_t at = lds0 + (slot ^ 1) * kTileB;
         if (t > 1) kc.tile(kbase + (int64_t)kTile * (t - 2) * a.k.row, at);
         if (t > 0) vc.tile(vbase + (int64_t)kTile * (t - 1) * a.v.row, at + kKeyB);
     };
     auto done = [&]() {
         --t;
-        slot = slot == 0 ? kTileB : 0;
+        slot ^= 1;
+        // (where registers are few: addresses of one slot at a time)
+        if constexpr (kFew) asm volatile("" : "+s"(slot));
     };
     // (turn t_first + 1, in which no values are taken, has begun above)
     while (t > 0 && (!active || t - 1 > t_mine)) {
