@@ -5,8 +5,8 @@
 //   out[i] = sum_j softmax_j(S) v[j],  lse[i] = log sum_j exp S[i, j]
 //
 // The attention of prompts that are too short for a selection ("Study MLA
-// Indexer", the last of the "three whys": dense attention where the prompt has
-// no more rows than the selection takes).
+// Indexer": a prompt of no more rows than the selection takes is attended to
+// densely).
 //
 // One workgroup takes a head and a block of query rows, 32 to a wave, which
 // carries them through both products:
@@ -37,14 +37,15 @@
 // taken again with such elements apart.
 //
 // Bound by the matrix cores and the power limit, which sets the clock: 32768 rows
-// of 16 heads over 2, 128 columns (4.4 TFLOP): 3.80 ms, 1.16 PFLOP/s, the matrix
-// cores busy 67% of the cycles at about 1.7 GHz, where a bf16 matrix product of
-// 8192 cubed reached 1.16 to 1.36.  64 columns are bound by the vector
-// instructions of the softmax, as many as for 128: 0.93 to 0.96 PFLOP/s; 192 and
-// 128 columns, 8192 rows of 16 heads: 1.06 to 1.09.  16 prompts of 59 to 2331 rows,
-// 16 heads of 192 and 128 columns with keys of their own (79 GFLOP, 252 MB): 102 to
-// 110 us; a workgroup of few tiles waits 2 to 5 us for its first ones.  61 rows: 7
-// us, of which the launch, the first loads and the end are all but one.
+// of 16 heads over 2, 128 columns (4.4 TFLOP): 3.71 to 4.2 ms on different cards, 1.05
+// to 1.18 PFLOP/s, the matrix cores busy 71% of the cycles at about 1.7 GHz, where a
+// bf16 matrix product of 8192 cubed reached 1.16 to 1.36.  64 columns are bound by the
+// vector instructions of the softmax, as many as for 128: 0.94 to 0.98 PFLOP/s; 192
+// and 128 columns, 8192 rows of 16 heads: 1.06 to 1.09.  Short sequences by their
+// first tiles' latency, the masked part and the end: 16 of 59 to 2331 rows, 16 heads
+// of 192 and 128 columns with keys of their own (79 GFLOP, 252 MB), 102 to 116 us; 32 of
+// 512, 32 heads over 8 of 128 columns (70 GFLOP, 335 MB) 119.  61 rows: 7 us, of which
+// the launch, the first loads and the end are all but one.
 #include <utility>
 
 #include "device_once.h"

@@ -529,9 +529,8 @@ dsaidx_status indexer_kv_append_rope(const void* k, int64_t k_stride, int64_t k_
  * indexer_prompt_attention -- causal attention over whole prompts: B packed
  * sequences of different lengths, H query heads over G key/value heads.
  *
- * Passage: "Study MLA Indexer", the last of the "three whys" (a prompt with no
- * more rows than the selection takes is attended to densely); "From principle to
- * code", section 3 (the lower-triangular mask keeps j <= i).  With row i of a
+ * Passage: "Study MLA Indexer" (a prompt of no more rows than the selection takes
+ * is attended to densely); "From principle to code", section 3 (the lower-triangular mask keeps j <= i).  With row i of a
  * sequence and query head h, which reads key/value head h / (H / G):
  *     S[i,j] = scale * q[i,h] . k[j]        for the rows j <= i of its sequence
  *     out[i,h] = sum_j softmax_j(S) v[j],  lse[i,h] = log sum_j exp S[i,j]
