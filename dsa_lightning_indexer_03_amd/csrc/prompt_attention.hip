@@ -23,7 +23,7 @@
 // the rounding alone is 1.6e-3).  P's sum is taken before the rounding, so that
 // lse does not have it.
 //
-// A turn of a wave makes the probabilities of its keys, 64 of a tile, beside the
+// A turn of a wave makes the probabilities of its keys, 64 or 32 of a tile, beside the
 // next tile's scores, and takes these keys' values between those: matrix and
 // vector instructions alternate, and each has about as many cycles as the other
 // (32 rows of 128 columns: 1024 and 900).  Where blocks are few, two or four key

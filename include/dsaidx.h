@@ -530,8 +530,9 @@ dsaidx_status indexer_kv_append_rope(const void* k, int64_t k_stride, int64_t k_
  * sequences of different lengths, H query heads over G key/value heads.
  *
  * Passage: "Study MLA Indexer" (a prompt of no more rows than the selection takes
- * is attended to densely); "From principle to code", section 3 (the lower-triangular mask keeps j <= i).  With row i of a
- * sequence and query head h, which reads key/value head h / (H / G):
+ * is attended to densely); "From principle to code", section 3 (the
+ * lower-triangular mask keeps j <= i).  With row i of a sequence and query head
+ * h, which reads key/value head h / (H / G):
  *     S[i,j] = scale * q[i,h] . k[j]        for the rows j <= i of its sequence
  *     out[i,h] = sum_j softmax_j(S) v[j],  lse[i,h] = log sum_j exp S[i,j]
  * Scores, sums and the softmax's statistics are fp32; the probabilities enter

@@ -23,7 +23,7 @@ def make_pool(rng, pages, G, D, kind, live=None):
     (page, slot) not in `live` [pages][64] (None: all are) hold NaN, in fp8 pools
     the scale too."""
     x = rng.normal(size=(pages, G, 64, D))
-    dead = np.zeros((pages, G, 64), bool) if live is None else np.broadcast_to(~live[:, None], (pages, G, 64))
+    dead = np.zeros((pages, G, 64), bool) if live is None else np.broadcast_to(~live[:, None], (pages, G, 64)).copy()
     dead_t = torch.from_numpy(np.ascontiguousarray(dead))
     if kind == "bf16":
         t, v = bf16(x)

@@ -269,3 +269,28 @@ def test_refusals_on_the_device():
     with pytest.raises(Exception, match="status"):
         call(q=x["q"][:, :7].contiguous())
     torch.cuda.synchronize()
+
+
+def test_two_graphs_on_one_workspace():
+    """Two captured steps with one scratch between them, replayed one after another."""
+    xs = [big(i, K=k) for i, k in ((5, None), (6, 1500))]
+    n = max(dsa.kv_decode_workspace_bytes(5, 8, 2, 128, x["block_table"].shape[1] * 64, k) for x, k in zip(xs, (0, 1500)))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for x in xs:
+        dsa.kv_attention_decode(**x, scale=0.1, want_lse=True, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(dsa.kv_attention_decode(**x, scale=0.1, want_lse=True, workspace=ws))
+        graphs.append(g)
+    for replay in range(3):
+        say(f"replay {replay} of two graphs on one workspace")
+        for x in xs:
+            x["q"].copy_(torch.randn_like(x["q"]))
+        for g in graphs:
+            g.replay()
+        for x, o in zip(xs, outs):
+            want = dsa.kv_attention_decode(**x, scale=0.1, want_lse=True)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(o, want))
