@@ -358,7 +358,7 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
 
 // One workgroup a row: its threads weigh the runs, then a lane takes 4 columns of
 // every run that is its wave part's, four runs' loads in flight (one context of
-// 131072, 16 heads over one, 512 runs: both kernels 20.5 us, one load at a time 24.7).
+// 131072, 16 heads over one: both kernels 20.5 us, with one load at a time 24.7).
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
 kv_join_kernel(KvDecodeArgs a, KvPlan p) {
