@@ -400,6 +400,7 @@ dsaidx_status indexer_latent_attention_shared(const void* q, int q_dtype, const 
 namespace {
 
 constexpr int kMaxKvHeads = 128;
+constexpr int kMaxKvRows = 1 << 23;        // query rows of a decode call: B * H
 
 // Heads and scale of the attention calls with keys and values of G groups.
 dsaidx_status kv_heads_check(int H, int G, float scale) {
@@ -552,7 +553,11 @@ dsaidx_status indexer_prompt_attention(const void* q, int64_t q_stride, int64_t 
 
 size_t indexer_kv_attention_decode_workspace_bytes(int B, int H, int G, int D, int max_context_len, int topk,
                                                    int cache_dtype) {
-    if (B < 1 || G < 1 || H < G || H > kMaxKvHeads || (D != 64 && D != 128) || max_context_len < 0 || topk < 0) return 0;
+    // (what the call refuses has no plan: its size is 0, and the call says why)
+    if (B < 1 || G < 1 || H < G || H % G != 0 || H > kMaxKvHeads || (int64_t)B * H > kMaxKvRows ||
+        (D != 64 && D != 128) || max_context_len < 0 || max_context_len > kMaxLatentTokens || topk < 0 ||
+        topk > kMaxL || (cache_dtype != DSAIDX_BF16 && cache_dtype != DSAIDX_FP8_E4M3))
+        return 0;
     return dsaidx::kv_decode_workspace_bytes(B, H, G, D, max_context_len, topk, cache_dtype == DSAIDX_FP8_E4M3);
 }
 
@@ -578,7 +583,7 @@ dsaidx_status indexer_kv_attention_decode(const void* q, int q_dtype, const void
     if ((topk_idx != nullptr) != (topk > 0))
         return fail(DSAIDX_ERR_SHAPE, "topk=%d: at least 1 with topk_idx, 0 without", topk);
     if (topk > kMaxL) return fail(DSAIDX_ERR_UNSUPPORTED, "topk=%d > %d", topk, kMaxL);
-    if ((int64_t)B * H > 1 << 23) return fail(DSAIDX_ERR_UNSUPPORTED, "B * H = %lld > 2^23", (long long)B * H);
+    if ((int64_t)B * H > kMaxKvRows) return fail(DSAIDX_ERR_UNSUPPORTED, "B * H = %lld > 2^23", (long long)B * H);
     if (B == 0) return DSAIDX_OK;
     if (!q) return fail(DSAIDX_ERR_NULL, "q is NULL");
     if (!block_table) return fail(DSAIDX_ERR_NULL, "block_table is NULL");

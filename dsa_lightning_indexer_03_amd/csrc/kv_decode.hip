@@ -481,8 +481,9 @@ KvPlan make_plan(int B, int H, int G, int D, int max_ctx, int K, bool fp8) {
         }
     }
     const int64_t rounds = ceil_div(len, kKeys * p.waves);
-    // (a launch holds less than 2^32 threads)
-    while (ceil_div(rounds, run) > kMaxRuns || ceil_div(rounds, run) * blocks >= (int64_t)1 << 24) run *= 2;
+    // (a launch holds less than 2^32 threads: B * H is at most 2^23, so one run a sequence fits)
+    while (run < rounds && (ceil_div(rounds, run) > kMaxRuns || ceil_div(rounds, run) * blocks >= (int64_t)1 << 24))
+        run *= 2;
     p.run = (int)(run * kKeys * p.waves);
     p.slots = len > 0 ? ceil_div(len, p.run) : 1;
     return p;

@@ -604,6 +604,7 @@ dsaidx_status indexer_kv_attention_decode(const void* q, int q_dtype, const void
                                           int topk, int B, int H, int G, int D, int page_size, float scale, void* out,
                                           float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes for such a call; 0 where one run a sequence needs none, and for sizes that the call refuses. */
 size_t indexer_kv_attention_decode_workspace_bytes(int B, int H, int G, int D, int max_context_len, int topk,
                                                    int cache_dtype);
 
