@@ -580,7 +580,8 @@ dsaidx_status indexer_kv_attention_decode(const void* q, int q_dtype, const void
     if (max_context_len < 0 || (int64_t)max_context_len > (int64_t)max_pages_per_seq * page_size)
         return fail(DSAIDX_ERR_SHAPE, "max_context_len=%d > max_pages_per_seq*page_size=%lld", max_context_len,
                     (long long)max_pages_per_seq * page_size);
-    if ((topk_idx != nullptr) != (topk > 0))
+    // (a list for no sequence has no address)
+    if (topk < 0 || (topk_idx ? topk == 0 : topk > 0 && B > 0))
         return fail(DSAIDX_ERR_SHAPE, "topk=%d: at least 1 with topk_idx, 0 without", topk);
     if (topk > kMaxL) return fail(DSAIDX_ERR_UNSUPPORTED, "topk=%d > %d", topk, kMaxL);
     if ((int64_t)B * H > kMaxKvRows) return fail(DSAIDX_ERR_UNSUPPORTED, "B * H = %lld > 2^23", (long long)B * H);
