@@ -720,8 +720,9 @@ def kv_append_rope(k, v, seq_ids, positions, block_table, k_cache, v_cache, cos_
     if cos_sin is not None and (cos_sin.dtype is not _F32 or cos_sin.get_device() != index or
                                 not cos_sin.is_contiguous()):
         _all(index, (("cos_sin", cos_sin, _FLOATS),))
-    if block_table.dim() != 2 or (cos_sin is not None and cos_sin.dim() != 2):
-        raise ValueError("cos_sin must be [rope_len, R] and block_table [B, max_pages]")
+    if block_table.dim() != 2 or (cos_sin is not None and (cos_sin.dim() != 2 or cos_sin.numel() == 0)):
+        # (a table without an entry has no address: it would read as None, no rotation)
+        raise ValueError("cos_sin must be [rope_len, R], neither of them 0, and block_table [B, max_pages]")
     if seq_ids.shape != (T,) or positions.shape != (T,):
         raise ValueError("seq_ids / positions must have one entry per token")
     if _grad_enabled():

@@ -39,3 +39,17 @@ def test_a_step_of_no_sequence(K, kind):
                                        k_scale=scale, v_scale=scale, want_lse=True)
     torch.cuda.synchronize()
     assert out.shape == (0, 8, 128) and lse.shape == (0, 8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(0, 64), (5, 0), (0, 0)])
+def test_angles_of_no_position(shape):
+    """An empty table of angles is refused: it is not the None that means no rotation."""
+    dev = torch.device("cuda")
+    cache = torch.zeros((1, 2, 64, 128), dtype=torch.bfloat16, device=dev)
+    k = torch.ones((3, 2, 128), dtype=torch.bfloat16, device=dev)
+    seq, pos = torch.zeros(3, dtype=torch.int32, device=dev), torch.arange(3, dtype=torch.int32, device=dev)
+    with pytest.raises(ValueError, match="cos_sin"):
+        dsa.kv_append_rope(k, k, seq, pos, seq[:1, None], cache, cache.clone(), cos_sin=torch.zeros(shape, device=dev))
+    torch.cuda.synchronize()
+    assert not cache.any()
