@@ -22,6 +22,7 @@ per-row scales.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from . import _lib
 
@@ -446,10 +447,24 @@ def _rows(t, name: str) -> int:
     return s[0]
 
 
+def _dual_level() -> bool:
+    """Whether this is within a forward_ad.dual_level(), outside of which no tensor has a tangent."""
+    return getattr(_forward_ad, "_current_level", 0) >= 0
+
+
+def _derivatives() -> bool:
+    return torch.is_grad_enabled() or _dual_level()
+
+
 def _inference_only(where: str, *tensors) -> None:
+    """Refuses inputs with a derivative, which the call would drop: a gradient (where gradients are enabled) or a
+    tangent (which no_grad does not switch off)."""
+    grad, dual = torch.is_grad_enabled(), _dual_level()
     for t in tensors:
-        if t is not None and t.requires_grad and torch.is_grad_enabled():
+        if t is not None and grad and t.requires_grad:
             raise ValueError(f"{where} has no backward: call it under torch.no_grad() or detach its inputs")
+        if t is not None and dual and _forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{where} has no forward derivative: call it with the primals of its dual inputs")
 
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
@@ -652,9 +667,6 @@ def latent_attention_shared(q, latent_cache, prefix_table, prefix_len: int, bloc
     return out, lse
 
 
-_grad_enabled = torch.is_grad_enabled
-
-
 def _heads(t, name: str, index: int, dtypes):
     """Token and head stride (elements) of a [T, heads, columns] tensor on GPU `index` whose rows are contiguous."""
     if t.dtype not in dtypes:
@@ -725,7 +737,7 @@ def kv_append_rope(k, v, seq_ids, positions, block_table, k_cache, v_cache, cos_
         raise ValueError("cos_sin must be [rope_len, R], neither of them 0, and block_table [B, max_pages]")
     if seq_ids.shape != (T,) or positions.shape != (T,):
         raise ValueError("seq_ids / positions must have one entry per token")
-    if _grad_enabled():
+    if _derivatives():
         _inference_only("kv_append_rope", k, v, cos_sin, k_cache, v_cache, k_scale, v_scale)
     B, max_pages = block_table.shape
     rope_len, R = (0, 0) if cos_sin is None else cos_sin.shape
@@ -763,7 +775,7 @@ def prompt_attention(q, k, v, cu_seqlens, scale: float, want_lse: bool = False):
         raise ValueError("q must be [T, H, D], k [T, G, D] and v [T, G, V]")
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must be [B + 1] with B >= 1")
-    if _grad_enabled():
+    if _derivatives():
         _inference_only("prompt_attention", q, k, v)
     if _current_device() != index:
         with torch.cuda.device(index):
@@ -816,7 +828,7 @@ def kv_attention_decode(q, k_cache, v_cache, block_table, context_lens, scale: f
         raise ValueError("block_table / context_lens shape mismatch")
     if topk_idx is not None and (topk_idx.dim() != 2 or topk_idx.shape[0] != B or topk_idx.shape[1] < 1):
         raise ValueError("topk_idx must be [B, K] with K >= 1")
-    if _grad_enabled():
+    if _derivatives():
         _inference_only("kv_attention_decode", q, k_cache, v_cache, k_scale, v_scale)
     max_pages = block_table.shape[1]
     mcl = max_pages * page if max_context_len is None else int(max_context_len)
