@@ -18,11 +18,17 @@
 // The first one leaves a lane with head lane % 16 and keys 4g .. 4g+3 (g = lane /
 // 16) of each 16 keys, which is the second one's operand when its 32 keys are
 // counted as 4g .. 4g+3 of two blocks: P never leaves its registers, and the
-// values are read transposed in that order.  Sums are fp32; P is rounded to
-// bf16, the type of the second product's other operand: an output is off by at
-// most 2^-8 of sum P |v| for that, beside its own rounding; P's sum is taken
-// before the rounding.  The exponent's reference moves when a score passes it by
-// 2^kSlack.
+// values are read transposed in that order.  Sums are fp32, P's sum before any
+// rounding.  The exponent's reference moves when a score passes it by 2^kSlack.
+//
+// The second product takes its operands in bf16, and P of bf16 rows enters it in two
+// terms, the leading bits and the rest, so that an output is off by 2^-15 of sum P
+// |v| beside its own rounding, where one term leaves up to 2^-8.  One and two, us: 64
+// contexts of 4096 to 32768 824 and 825, one of 4096 10.5 and 10.5, of 100 4.8 and 4.9;
+// 64 heads over one, 64 of 2048, 28.0 and 30.4.  P of fp8 rows is one term, rounded by
+// up to 2^-8, a sixteenth of the rounding that the row's codes have from their making,
+// 2^-4; two would take 21.9 us for 19.6 (37 contexts of up to 6000) and 60.8 for 59.2
+// (one of 131072).
 //
 // fp8 rows stay codes in LDS and are widened as operands.  A key's scale
 // multiplies its score, a value's its probability, in units of the wave's first
@@ -49,6 +55,12 @@ constexpr int kPage = 64;
 constexpr int kKeys = 32;      // positions of a wave's tile
 constexpr int kJoinThreads = 256;
 constexpr int kMaxRuns = 512;  // runs of a sequence
+
+// The leading bits of a probability, as bf16 in the upper half: less than it, so that
+// what is left is not 0, which would make NaN of an infinite value.  (0 stays 0.)
+__device__ __forceinline__ uint32_t leading(float p) {
+    return __builtin_elementwise_sub_sat(__float_as_uint(p), 1u) & 0xFFFF0000u;
+}
 
 // What an entry without a row is copied from.
 static __device__ __align__(16) const unsigned char kZeros[256] = {};
@@ -243,7 +255,7 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
                     vs[kk] = *reinterpret_cast<const v4f*>(st + 128 + 64 * kk) * inv_unit;
                 }
             }
-            v8bf P[MT];
+            v8bf P[MT], rest[FP8 ? 1 : MT];   // probabilities; what their leading bits leave
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 float top = -__builtin_inff();
@@ -268,7 +280,7 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) O[mt][ct] *= f;
                 }
-                v4i u;
+                v4i u, w;
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     float pr[4];
@@ -278,10 +290,20 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
                         l[mt] += pr[i];
                         if constexpr (FP8) pr[i] *= vs[kk][i];
                     }
-                    u[2 * kk] = (int)pack_bf16(pr[0], pr[1]);
-                    u[2 * kk + 1] = (int)pack_bf16(pr[2], pr[3]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float x = pr[2 * i], y = pr[2 * i + 1];
+                        if constexpr (FP8) {
+                            u[2 * kk + i] = (int)pack_bf16(x, y);
+                        } else {
+                            const uint32_t hx = leading(x), hy = leading(y);
+                            u[2 * kk + i] = (int)(hx >> 16 | hy);
+                            w[2 * kk + i] = (int)pack_bf16(x - __uint_as_float(hx), y - __uint_as_float(hy));
+                        }
+                    }
                 }
                 P[mt] = __builtin_bit_cast(v8bf, u);
+                if constexpr (!FP8) rest[mt] = __builtin_bit_cast(v8bf, w);
             }
             // ---- values: A operand of 16 columns x 32 keys ----
 #pragma unroll
@@ -301,8 +323,11 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
                     w = __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
                 }
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int mt = 0; mt < MT; ++mt) {
+                    if constexpr (!FP8)
+                        O[mt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, rest[mt], O[mt][ct], 0, 0, 0);
                     O[mt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, P[mt], O[mt][ct], 0, 0, 0);
+                }
             }
         }
     }

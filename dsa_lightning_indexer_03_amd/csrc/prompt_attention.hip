@@ -18,10 +18,11 @@
 // and the values are read transposed in that order.  The softmax's factors are
 // per lane; the exponent's reference moves when a score passes it by 2^kSlack.
 // Sums are fp32; P is rounded to bf16, because the matrix cores take both
-// operands of the second product in one type: an output is off by at most 2^-8
-// of sum P |v| for that, beside its own rounding (2.1e-3 rms of the outputs where
-// the rounding alone is 1.6e-3).  P's sum is taken before the rounding, so that
-// lse does not have it.
+// operands of the second product in one type, and a second term for what the
+// rounding leaves would be half as many matrix instructions again in a kernel
+// that they bound: an output is off by at most 2^-8 of sum P |v| for that, beside
+// its own rounding (2.1e-3 rms of the outputs where the rounding alone is 1.6e-3).
+// P's sum is taken before the rounding, so that lse does not have it.
 //
 // A turn of a wave makes the probabilities of its keys, 64 or 32 of a tile, beside the
 // next tile's scores, and takes these keys' values between those: matrix and

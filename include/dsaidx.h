@@ -568,8 +568,9 @@ dsaidx_status indexer_prompt_attention(const void* q, int64_t q_stride, int64_t 
  * Passage: "Lightning Indexer explained", section 2 (decode walkthrough: the
  * core attention runs over the selected set; section 2.3: a short context is
  * taken whole); "Study MLA Indexer", the data-flow diagram's last step.  The
- * same attention as indexer_prompt_attention (heads, rounding), for one query
- * per sequence.
+ * same attention as indexer_prompt_attention (heads, fp32 scores, sums and
+ * statistics), for one query per sequence.  The probabilities of bf16 rows enter
+ * the second product with 15 bits or more, those of fp8 rows rounded to bf16.
  *
  *   q            [B][H][D] bf16 (q_dtype must be DSAIDX_BF16)
  *   k_cache, v_cache, k_scale, v_scale: as indexer_kv_append_rope.  fp8 codes
