@@ -21,19 +21,16 @@
 // values are read transposed in that order.  Sums are fp32, P's sum before any
 // rounding.  The exponent's reference moves when a score passes it by 2^kSlack.
 //
-// The second product takes its operands in bf16, and P of bf16 rows enters it in two
-// terms, the leading bits and the rest, so that an output is off by 2^-15 of sum P
-// |v| beside its own rounding, where one term leaves up to 2^-8.  One and two, us: 64
-// contexts of 4096 to 32768 824 and 825, one of 4096 10.5 and 10.5, of 100 4.8 and 4.9;
-// 64 heads over one, 64 of 2048, 28.0 and 30.4.  P of fp8 rows is one term, rounded by
-// up to 2^-8, a sixteenth of the rounding that the row's codes have from their making,
-// 2^-4; two would take 21.9 us for 19.6 (37 contexts of up to 6000) and 60.8 for 59.2
-// (one of 131072).
+// The second product takes its operands in bf16, and P enters it in two terms, the
+// leading bits and the rest, so that an output is off by 2^-15 of sum P |v| beside its
+// own rounding, where one term leaves up to 2^-8.  One and two, us: 64 contexts of
+// 4096 to 32768 824 and 825, one of 4096 10.5 and 10.5, of 100 4.8 and 4.9; 64 heads
+// over one, 64 of 2048, 28.0 and 29.9; fp8, one of 131072 59.2 and 60.0, 37 of up to
+// 6000 with 64 columns 19.8 and 21.5.
 //
 // fp8 rows stay codes in LDS and are widened as operands.  A key's scale
 // multiplies its score, a value's its probability, in units of the wave's first
-// value scale, so that a run of one row, or of rows of one scale, rounds only
-// probabilities.
+// value scale, so that rows of one scale bring no rounding of it.
 //
 // The runs of a sequence are joined by a second kernel from fp32 sums.
 //
@@ -56,10 +53,20 @@ constexpr int kKeys = 32;      // positions of a wave's tile
 constexpr int kJoinThreads = 256;
 constexpr int kMaxRuns = 512;  // runs of a sequence
 
-// The leading bits of a probability, as bf16 in the upper half: less than it, so that
-// what is left is not 0, which would make NaN of an infinite value.  (0 stays 0.)
+// The two terms of a probability in the second product: its leading bits, bf16 in the
+// upper half of the first word, and what they leave.  Of a bf16 row the first is less
+// than the probability, so that the second is not 0, which would make NaN of an
+// infinite value (0 stays 0).  An fp8 row's codes are finite, but its scale may be
+// infinite, and with it the first term; the second is then a number, 2^127 (it is below
+// 2^121 of any finite one), not the NaN of inf - inf.
+template <bool FP8>
 __device__ __forceinline__ uint32_t leading(float p) {
-    return __builtin_elementwise_sub_sat(__float_as_uint(p), 1u) & 0xFFFF0000u;
+    return FP8 ? __float_as_uint(p) : __builtin_elementwise_sub_sat(__float_as_uint(p), 1u);
+}
+template <bool FP8>
+__device__ __forceinline__ float left(float p, uint32_t lead) {
+    const float rest = p - __uint_as_float(lead & 0xFFFF0000u);
+    return FP8 ? fminf(rest, 0x1p127f) : rest;
 }
 
 // What an entry without a row is copied from.
@@ -255,7 +262,7 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
                     vs[kk] = *reinterpret_cast<const v4f*>(st + 128 + 64 * kk) * inv_unit;
                 }
             }
-            v8bf P[MT], rest[FP8 ? 1 : MT];   // probabilities; what their leading bits leave
+            v8bf P[MT], rest[MT];   // probabilities; what their leading bits leave
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 float top = -__builtin_inff();
@@ -284,26 +291,23 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     float pr[4];
+                    uint32_t lead[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         pr[i] = __builtin_amdgcn_exp2f(S[mt][kk][i] - m[mt]);
                         l[mt] += pr[i];
                         if constexpr (FP8) pr[i] *= vs[kk][i];
+                        lead[i] = leading<FP8>(pr[i]);
+                        pr[i] = left<FP8>(pr[i], lead[i]);
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float x = pr[2 * i], y = pr[2 * i + 1];
-                        if constexpr (FP8) {
-                            u[2 * kk + i] = (int)pack_bf16(x, y);
-                        } else {
-                            const uint32_t hx = leading(x), hy = leading(y);
-                            u[2 * kk + i] = (int)(hx >> 16 | hy);
-                            w[2 * kk + i] = (int)pack_bf16(x - __uint_as_float(hx), y - __uint_as_float(hy));
-                        }
+                        u[2 * kk + i] = (int)__builtin_amdgcn_perm(lead[2 * i + 1], lead[2 * i], 0x07060302u);   // upper halves
+                        w[2 * kk + i] = (int)pack_bf16(pr[2 * i], pr[2 * i + 1]);
                     }
                 }
                 P[mt] = __builtin_bit_cast(v8bf, u);
-                if constexpr (!FP8) rest[mt] = __builtin_bit_cast(v8bf, w);
+                rest[mt] = __builtin_bit_cast(v8bf, w);
             }
             // ---- values: A operand of 16 columns x 32 keys ----
 #pragma unroll
@@ -324,8 +328,7 @@ kv_decode_kernel(KvDecodeArgs a, KvPlan p) {
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    if constexpr (!FP8)
-                        O[mt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, rest[mt], O[mt][ct], 0, 0, 0);
+                    O[mt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, rest[mt], O[mt][ct], 0, 0, 0);
                     O[mt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, P[mt], O[mt][ct], 0, 0, 0);
                 }
             }

@@ -569,8 +569,8 @@ dsaidx_status indexer_prompt_attention(const void* q, int64_t q_stride, int64_t 
  * core attention runs over the selected set; section 2.3: a short context is
  * taken whole); "Study MLA Indexer", the data-flow diagram's last step.  The
  * same attention as indexer_prompt_attention (heads, fp32 scores, sums and
- * statistics), for one query per sequence.  The probabilities of bf16 rows enter
- * the second product with 15 bits or more, those of fp8 rows rounded to bf16.
+ * statistics), for one query per sequence; the probabilities enter the second
+ * product with 15 bits or more.
  *
  *   q            [B][H][D] bf16 (q_dtype must be DSAIDX_BF16)
  *   k_cache, v_cache, k_scale, v_scale: as indexer_kv_append_rope.  fp8 codes

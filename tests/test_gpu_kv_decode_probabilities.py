@@ -1,6 +1,6 @@
-"""kv_attention_decode's probabilities of bf16 rows enter the product with the
-values in two bf16 terms: outputs that cancel keep what one term would lose, and
-infinite values come out as they are."""
+"""kv_attention_decode's probabilities enter the product with the values in two
+bf16 terms: outputs that cancel keep what one term would lose, and infinite values
+come out as they are."""
 import numpy as np
 import pytest
 import torch
@@ -8,6 +8,8 @@ import torch
 import dsa_lightning_indexer_03_amd as dsa
 from gpu_util import say
 from kv_util import bf16, ints
+from oracle.formats import fp8_e4m3_to_f64
+from oracle.kcache import encode_e4m3
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +123,82 @@ def test_a_value_out_of_reach(mpp, R):
     out = call(v)
     torch.cuda.synchronize()
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def paged_codes(codes, scale, table, pages):
+    """[B][n][D] codes, [B][n] scales -> pools, each sequence's rows in its first page; NaN elsewhere."""
+    c, f = np.full((pages, 1, 64, codes.shape[2]), 0x7F, np.uint8), np.full((pages, 1, 64), np.nan, np.float32)
+    for b, row in enumerate(table):
+        c[row[0], 0, :codes.shape[1]], f[row[0], 0, :codes.shape[1]] = codes[b], scale[b]
+    return torch.from_numpy(c).cuda(), torch.from_numpy(f).cuda()
+
+
+@pytest.mark.parametrize("n", [2, 6, 40])
+@pytest.mark.parametrize("R,B,mpp,listed", [(1, 2, 1, False), (1, 2, 1024, False), (8, 200, 1, False), (8, 2, 1, True),
+                                            (24, 2, 1, False), (24, 3, 1024, False), (64, 2, 1, False),
+                                            (64, 2, 1024, True)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_fp8_values_that_cancel(D, R, B, mpp, listed, n):
+    """As with bf16 rows: a key's one element is 1 and its scale the score's, the pair's
+    values are one row and its negative under a scale of their own, of either sign and
+    any size.
+
+    Bound: as there, and three roundings for the scales (the key's product, the value's
+    scale in the run's unit, its product with the probability) and one for the
+    unit's reciprocal and the unit put back: 5 * 2^-24, below 2^-21."""
+    rng = np.random.default_rng(n * R + D)
+    qx = np.zeros((B, R, D))
+    qx[:, :, 3] = rng.uniform(0.25, 1.0, size=(B, R))
+    q, qv = bf16(qx)
+    kc = np.zeros((B, n, D), np.uint8)
+    kc[:, :, 3] = 0x38                                             # 1.0
+    near = rng.integers(128, 255, size=(B, n // 2)) / 128.0
+    ks = np.stack([near, near + 1 / 128], 2).reshape(B, n).astype(np.float32)
+    vc = encode_e4m3(rng.uniform(100, 448, size=(B, n // 2, D)))
+    vc = np.stack([vc, vc ^ 0x80], 2).reshape(B, n, D)
+    vs = np.repeat(np.exp2(rng.uniform(-12, 12, size=(B, n // 2))), 2, axis=1).astype(np.float32)
+    flip = rng.random((B, n)) < 0.3
+    vs[flip] *= -1
+    vc[flip] ^= 0x80
+    pages = B + 1
+    table = np.full((B, mpp), -1)
+    table[:, 0] = rng.permutation(pages)[:B]
+    order = np.stack([rng.permutation(n) for _ in range(B)])
+    say(f"fp8 values that cancel: {n} keys, {R} heads, {D} columns, {B} x {mpp} pages, {'listed' if listed else 'all'}")
+    (k, kf), (v, vf) = paged_codes(kc, ks, table, pages), paged_codes(vc, vs, table, pages)
+    out, _ = dsa.kv_attention_decode(q.cuda(), k, v, ints(table), ints([n] * B), 1.0, k_scale=kf, v_scale=vf,
+                                     topk_idx=ints(order) if listed else None, want_lse=True)
+    torch.cuda.synchronize()
+    p = np.exp(qv[:, :, 3:4] * ks.astype(np.float64)[:, None])
+    p /= p.sum(2, keepdims=True)
+    vx = fp8_e4m3_to_f64(vc) * vs.astype(np.float64)[..., None]
+    want, size = p @ vx, p @ np.abs(vx)
+    err = (2.0 ** -15 + 2.0 ** -18 + 2.0 ** -21 + (n + 16) * 2.0 ** -24) * size
+    err += 2.0 ** -8 * (np.abs(want) + err)
+    d = np.abs(out.double().cpu().numpy() - want)
+    assert (d <= err).all(), f"off by {(d / err).max():.3g} of the bound"
+
+
+@pytest.mark.parametrize("at", [0, 17])
+@pytest.mark.parametrize("R", [1, 20, 64])
+@pytest.mark.parametrize("mpp", [1, 1024])
+def test_an_infinite_scale(mpp, R, at):
+    """A value row that was written with infinite elements has an infinite scale: these
+    read as themselves, the others, codes of 0, as NaN."""
+    rng = np.random.default_rng(R)
+    n, D = 33, 128
+    q = bf16(rng.normal(size=(1, R, D)))[0].cuda()
+    kc, vc = (encode_e4m3(rng.uniform(-448, 448, size=(1, n, D))) for _ in range(2))
+    ks, vs = (rng.uniform(0.002, 0.004, size=(1, n)).astype(np.float32) for _ in range(2))
+    vc[0, at] = 0
+    vc[0, at, 7], vc[0, at, 90] = 0x7E, 0xFE                       # 448 and -448
+    vs[0, at] = np.inf
+    table = np.full((1, mpp), -1)
+    table[0, 0] = 1
+    say(f"an infinite scale: {R} heads, {mpp} pages, row {at}")
+    (k, kf), (v, vf) = paged_codes(kc, ks, table, 2), paged_codes(vc, vs, table, 2)
+    out, lse = dsa.kv_attention_decode(q, k, v, ints(table), ints([n]), 0.1, k_scale=kf, v_scale=vf, want_lse=True)
+    torch.cuda.synchronize()
+    got = out[0].float().cpu().numpy()
+    assert bool(lse.isfinite().all()) and np.isposinf(got[:, 7]).all() and np.isneginf(got[:, 90]).all()
+    assert np.isnan(np.delete(got, [7, 90], axis=1)).all()
