@@ -803,12 +803,13 @@ def kv_attention_decode(q, k_cache, v_cache, block_table, context_lens, scale: f
     each of B sequences attends over its whole context, or over the positions
     selected for it; query head h reads key/value head h // (H / G).
 
-    q [B,H,D] bf16; k_cache, v_cache [P,G,page,D] bf16, or uint8 / float8_e4m3fn
-    codes with k_scale, v_scale [P,G,page] fp32, as kv_append_rope writes them;
-    block_table [B,max_pages] int32; context_lens [B] int32; topk_idx [B,K] int32
-    positions (-1, or outside the context: no row), None: every position.
-    ``max_context_len`` bounds context_lens (default: max_pages * page); the work
-    is cut for contexts of that length, so a bound near the longest is faster.
+    q [B,H,D] bf16, contiguous; k_cache, v_cache [P,G,page,D] bf16, or uint8 /
+    float8_e4m3fn codes with k_scale, v_scale [P,G,page] fp32, as kv_append_rope
+    writes them; block_table [B,max_pages] int32; context_lens [B] int32; topk_idx
+    [B,K] int32 positions (-1, or outside the context: no row), None: every position.
+    ``max_context_len`` bounds context_lens (default: max_pages * page); the work,
+    and the workspace, are cut for contexts of that length, so a bound near the
+    longest is faster (128 contexts of 300: 28 us, with a bound of 131072 112).
     ``workspace``: the caller's scratch of kv_decode_workspace_bytes, not shared
     by calls in flight (default: a new one each call).
     Returns (out bf16 [B,H,D], lse fp32 [B,H] or None); a query without a position

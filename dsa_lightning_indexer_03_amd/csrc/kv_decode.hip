@@ -35,12 +35,12 @@
 // The runs of a sequence are joined by a second kernel from fp32 sums.
 //
 // Bound by HBM: 64 contexts of 4096 to 32768 positions, 8 heads of 128 columns, bf16
-// (4.87 GB, read once by the counters): 823 us, 5.9 TB/s, where a 1 GiB copy moves
-// 5.2 to 5.4 in both directions; 2048 selected of 64 contexts (537 MB): 98 us, 5.5;
-// one context of 131072, fp8 (277 MB): 58 to 62 us with its join.  A wave's next tile
-// is in flight, 64 KB a CU in all: a round takes its share of the bandwidth with the
-// card full, 0.75 to 1 us of latency with little work (run_cost).  Products and
-// softmax take a tenth of the matrix cores' cycles.
+// (4.87 GB, read once by the counters): 825 us, 5.9 TB/s, where reading pages alone
+// reaches 6.1 to 6.3; 2048 selected of 64 contexts (537 MB): 98 us, 5.5 (fp8, 277 MB:
+// 69 to 76 us, 3.6 to 4.0); one context of 131072, fp8 (277 MB): 58 to 62 us with its
+// join.  A wave's next tile is in flight, 64 KB a CU in all: a round takes its share of
+// the bandwidth with the card full, 0.75 to 1 us of latency with little work (run_cost).
+// Products and softmax take up to a tenth of the matrix cores' cycles.
 #include "device_once.h"
 #include "kv.h"
 #include "tile_copy.h"

@@ -38,15 +38,16 @@
 // taken again with such elements apart.
 //
 // Bound by the matrix cores and the power limit, which sets the clock: 32768 rows
-// of 16 heads over 2, 128 columns (4.4 TFLOP): 3.71 to 4.2 ms on different cards, 1.05
-// to 1.18 PFLOP/s, the matrix cores busy 71% of the cycles at about 1.7 GHz, where a
-// bf16 matrix product of 8192 cubed reached 1.16 to 1.36.  64 columns are bound by the
+// of 16 heads over 2, 128 columns (4.4 TFLOP): 3.67 to 4.05 ms on different cards, 1.09
+// to 1.20 PFLOP/s, the matrix cores busy 71% of the cycles at about 1.7 GHz, where a
+// bf16 matrix product of 8192 cubed reaches 1.37 in a row.  64 columns are bound by the
 // vector instructions of the softmax, as many as for 128: 0.94 to 0.98 PFLOP/s; 192
-// and 128 columns, 8192 rows of 16 heads: 1.06 to 1.09.  Short sequences by their
+// and 128 columns, 8192 rows of 16 heads: 1.04 to 1.09.  Short sequences by their
 // first tiles' latency, the masked part and the end: 16 of 59 to 2331 rows, 16 heads
-// of 192 and 128 columns with keys of their own (79 GFLOP, 252 MB), 102 to 116 us; 32 of
-// 512, 32 heads over 8 of 128 columns (70 GFLOP, 335 MB) 119.  61 rows: 7 us, of which
-// the launch, the first loads and the end are all but one.
+// of 192 and 128 columns with keys of their own (79 GFLOP, 252 MB), 113 to 126 us, 106
+// where the caches hold the inputs; 32 of 512, 32 heads over 8 of 128 columns (70
+// GFLOP, 335 MB) 119.  61 rows: 8 us, of which the launch, the first loads and the end
+// are all but one.
 #include <utility>
 
 #include "device_once.h"
@@ -627,7 +628,10 @@ hipError_t run(const PromptArgs& a, hipStream_t stream) {
 }
 
 // The form of a call, by about how many blocks of 64 and 128 rows there are (256 CUs
-// hold 512 workgroups of four waves, 256 of eight) and the sequences' mean length:
+// hold 512 workgroups of four waves, 256 of eight) and the sequences' mean length, all
+// that the host knows (rows of no sequence and empty sequences enter it, and it says
+// little of very unequal ones: 8192 rows of one head take 68 us, beside 100 sequences
+// of up to 5 rows 120):
 // blocks of 64 rows and four key groups while each has a CU of its own, or two in a
 // row where they are long; 128 rows and two key groups for up to two workgroups a
 // CU; else 128 rows and one group, which with 64 and 128 columns and many sequences

@@ -538,7 +538,8 @@ dsaidx_status indexer_kv_append_rope(const void* k, int64_t k_stride, int64_t k_
  * Scores, sums and the softmax's statistics are fp32; the probabilities enter
  * the second product rounded to bf16 (lse without that rounding); out is rounded
  * once to bf16.  What a row does not see does not reach it, whatever it holds
- * (infinities, NaN).
+ * (infinities, NaN).  The sums are divided at the end, with probabilities of up to
+ * 2^16: values of 2^80 and more may make them infinite.
  *
  *   q, k, v      [T][H], [T][G] rows of D elements and [T][G] rows of V, in
  *                dtype (BF16); row (t, h) starts t * stride + h * head_stride
@@ -570,7 +571,8 @@ dsaidx_status indexer_prompt_attention(const void* q, int64_t q_stride, int64_t 
  * taken whole); "Study MLA Indexer", the data-flow diagram's last step.  The
  * same attention as indexer_prompt_attention (heads, fp32 scores, sums and
  * statistics), for one query per sequence; the probabilities enter the second
- * product with 15 bits or more.
+ * product with 15 bits or more, and with fp8 rows it is values of 2^40 and more
+ * that may make the sums infinite.
  *
  *   q            [B][H][D] bf16 (q_dtype must be DSAIDX_BF16)
  *   k_cache, v_cache, k_scale, v_scale: as indexer_kv_append_rope.  fp8 codes
@@ -580,8 +582,8 @@ dsaidx_status indexer_prompt_attention(const void* q, int64_t q_stride, int64_t 
  *                is page block_table[b][s / page_size], slot s % page_size.  A page
  *                id outside [0, num_pages) is a page without rows
  *   context_lens [B] int32 (device), clamped to [0, max_context_len]
- *   max_context_len  host bound, <= max_pages_per_seq * page_size.  The work is
- *                cut for contexts of that length
+ *   max_context_len  host bound, <= max_pages_per_seq * page_size.  The work and
+ *                the workspace are cut for contexts of that length
  *   topk_idx     [B][topk] int32 positions in any order, e.g. the output of
  *                indexer_decode_paged; an entry outside [0, context length) is no
  *                row (-1 pads), a position listed twice counts twice.  NULL (and
