@@ -472,10 +472,11 @@ int held(int D, int rows, bool fp8, int waves) {
 // until a workgroup's first tile and for its join of the waves; a round its bytes'
 // share of 5.9 TB/s or, with part of the card, 0.75 (fp8: 1) and 0.6 of that; 2.5 for
 // the second kernel and 0.03 a run.  8 heads of 128 columns, bf16, in runs of 1, 4, 8,
-// 16, 32 and 128 rounds of four waves: one context of 32768 49.7, 31.2, 28.9, 29.1,
-// 45.7 and 154 us; 8 of 8192 86, 57.9, 54.4, 52.3 and 59.2; 64 of 4096 to 32768 1575,
-// 973, 860, 824, 822 and 860.  One wave a workgroup and four: 128 contexts of 64 9.2
-// and 17.3, of 300 23.2 and 27.9, of 1024 92 and 96; fp8, 1024, 60.0 and 55.8.
+// 16, 32 and 128 rounds of four waves: one context of 32768 44.3, 29.4, 27.3, 30.5,
+// 48.5 and 164 us; 8 of 8192 86, 58.5, 55.0, 52.6, 58.8 and 92.6; 64 of 4096 to 32768
+// 1608, 983, 862, 831, 825 and 867.  One wave a workgroup and four: 128 contexts of 64
+// 9.7 and 17.7, of 300 30.7 and 38.0, of 1024 102 and 105; fp8, 512, 34.2 and 30.1,
+// 1024, 64.5 and 56.9.
 double run_cost(int64_t blocks, int64_t rounds, int64_t run, int held, int round_bytes, bool fp8) {
     const int64_t slots = ceil_div(rounds, run), wgs = blocks * slots, at_once = wgs < held ? wgs : held;
     const double share = 1e-6 * round_bytes * (double)at_once / 5.9, part = (fp8 ? 1. : 0.75) + 0.6 * share;
